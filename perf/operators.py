@@ -1,0 +1,555 @@
+"""The residual-block operators as they are measured: cases, inputs, plain forms.
+
+Four operators that keep a block's activations in 8 bits for the backward pass:
+
+  codes     a tensor packed into 8-bit codes (groups of 32 along the row, one
+            power-of-two scale each) and read back
+  glu       out = act(gate) * up, its inputs kept as codes, and its backward
+            from the codes
+  wgrad     the weight gradient of a linear layer whose input is kept as codes:
+            dW = dY^T (s * X + t), db = sum dY
+  resnorm   the boundary between two blocks, r' = r + alpha * g * post(b) and
+            n = pre(r'), with RMS or layer norms; forward and backward
+
+run() computes the plain form in elementary torch operations (float32, rounded
+once at the end), or, with `own` set, calls the library's entry points.  exact()
+computes the same from the definitions in float64.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+BYTES = {"f32": 4, "bf16": 2, "f16": 2}
+GROUP = 32
+
+
+# ---------------------------------------------------------------------------
+# cases
+
+def listed():
+    return [
+        # an attention input kept for the backward: a slice of a wider projection's output
+        dict(name="codes_slice_bf16", op="codes", T=8192, C=4096, ld=12288, dtype="bf16"),
+        # a small odd batch in full precision, rows not a whole number of groups
+        dict(name="codes_odd_f32", op="codes", T=777, C=1001, ld=1001, dtype="f32"),
+        # the MLP of a training step, gate and up halves of one projection
+        dict(name="glu_silu_bf16", op="glu", T=8192, F=8192, dtype="bf16", act="silu", gated=True),
+        # an odd micro-batch and width, halves not aligned
+        dict(name="glu_gelu_odd_f16", op="glu", T=515, F=1365, dtype="f16", act="gelu_tanh",
+             gated=True),
+        # a square projection's gradient at an ordinary batch, input a norm's output
+        dict(name="wgrad_bf16", op="wgrad", T=8192, N=4096, K=4096, dtype="bf16", affine="scale",
+             bias=False),
+        # a narrow layer over a long batch: few output tiles, a long sum
+        dict(name="wgrad_long_f16", op="wgrad", T=65536, N=512, K=640, dtype="f16", affine="none",
+             bias=True),
+        # full-precision gradients, ragged in every extent, after a layer norm
+        dict(name="wgrad_odd_f32", op="wgrad", T=2049, N=1001, K=777, dtype="f32",
+             affine="shift", bias=True),
+        # one generated token
+        dict(name="resnorm_token_bf16", op="resnorm_fwd", T=1, C=4096, dtype="bf16", post="rms",
+             pre="rms", gate="none", R=1, keep=False),
+        # a training batch, normed on both sides of the block, its xhat kept as codes
+        dict(name="resnorm_train_bf16", op="resnorm_fwd", T=16384, C=4096, dtype="bf16",
+             post="rms", pre="rms", gate="vector", R=16384, keep=True),
+        # full precision, an odd width, a gate for each sample of 125 rows
+        dict(name="resnorm_odd_f32", op="resnorm_fwd", T=1000, C=1537, dtype="f32", post="layer",
+             pre="layer", gate="rows", R=125, keep=False),
+        # the training batch's backward from codes, with the gate vector's gradient
+        dict(name="resnorm_bwd_codes_bf16", op="resnorm_bwd", T=16384, C=4096, dtype="bf16",
+             post="rms", pre="rms", gate="vector", R=16384, source="codes"),
+        # the backward from stored tensors: layer norms, a gate for each sample
+        dict(name="resnorm_bwd_full_f16", op="resnorm_bwd", T=2080, C=1152, dtype="f16",
+             post="layer", pre="layer", gate="rows", R=260, source="full"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def _ragged(rng, v):
+    """A size near v: odd, a multiple of 8, or a multiple of 128."""
+    m = rng.choice((1, 8, 128))
+    return max(1, v | 1) if m == 1 else max(m, v // m * m)
+
+
+def draw(rng):
+    op = rng.choice(("codes", "glu", "wgrad", "resnorm_fwd", "resnorm_bwd"))
+    dtype = rng.choice(("bf16", "bf16", "f16", "f32"))
+    T = _log_int(rng, 1, 16384)
+    C = _ragged(rng, _log_int(rng, 64, 8192))
+    T = max(1, min(T, (48 << 20) // C))
+    if op == "codes":
+        return dict(op=op, T=T, C=C, ld=C * rng.choice((1, 3)), dtype=dtype)
+    if op == "glu":
+        return dict(op=op, T=T, F=C, dtype=dtype,
+                    act=rng.choice(("silu", "gelu", "gelu_tanh")), gated=rng.random() < 0.8)
+    if op == "wgrad":
+        N = _ragged(rng, _log_int(rng, 64, 4096))
+        K = _ragged(rng, _log_int(rng, 64, 4096))
+        T = _log_int(rng, 64, 65536)
+        T = max(1, min(T, int(6e10 / (N * K))))
+        return dict(op=op, T=T, N=N, K=K, dtype=dtype,
+                    affine=rng.choice(("none", "scale", "shift")), bias=rng.random() < 0.5)
+    gate = rng.choice(("none", "vector", "rows", "full"))
+    R = 1
+    if gate == "vector":
+        R = T
+    elif gate == "rows":
+        R = _log_int(rng, 2, 512)
+        T = max(1, T // R) * R
+    c = dict(op=op, T=T, C=C, dtype=dtype, post=rng.choice(("none", "rms", "layer")),
+             pre=rng.choice(("rms", "layer")), gate=gate, R=R)
+    if op == "resnorm_fwd":
+        c["keep"] = dtype != "f32" and rng.random() < 0.5
+    else:
+        c["source"] = rng.choice(("codes", "full"))
+    return c
+
+
+def work(c):
+    e = BYTES[c["dtype"]]
+    code = 1 + 1 / GROUP
+    if c["op"] == "codes":
+        n = c["T"] * c["C"]
+        return {"bytes": n * (2 * e + 2 * code), "flops": n * 4}
+    if c["op"] == "glu":
+        n, k = c["T"] * c["F"], 2 if c["gated"] else 1
+        # forward: inputs, out, codes; backward: codes, dout, the gradients, out again
+        return {"bytes": n * (k * e + e + k * code + k * code + e + k * e + e), "flops": n * 30}
+    if c["op"] == "wgrad":
+        T, N, K = c["T"], c["N"], c["K"]
+        return {"bytes": T * N * e + T * K * code + N * K * 4, "flops": 2.0 * T * N * K}
+    n = c["T"] * c["C"]
+    g = {"none": 0, "vector": 4 * c["C"], "rows": c["T"] // c["R"] * c["C"] * e,
+         "full": n * e}[c["gate"]]
+    if c["op"] == "resnorm_fwd":
+        keep = n * 2 * (2 * code + 2) if c["keep"] else 0
+        return {"bytes": n * 4 * e + g + keep, "flops": n * 16}
+    saved = 2 * code if c["source"] == "codes" else 2 * e
+    return {"bytes": n * (4 * e + saved) + 2 * g, "flops": n * 30}
+
+
+# ---------------------------------------------------------------------------
+# inputs
+
+def _normal(gen, *shape):
+    return torch.randn(*shape, generator=gen, device="cuda")
+
+
+def _activations(gen, T, C):
+    """Activations as blocks give them: unit scale, a few large channels, rows of
+    different size."""
+    x = _normal(gen, T, C)
+    x *= torch.exp(0.5 * _normal(gen, T, 1))
+    big = torch.rand(C, generator=gen, device="cuda") < 0.01
+    return x * torch.where(big, 12.0, 1.0)
+
+
+def _encode(x):
+    """The codes and scale exponents a tensor [T, C] of float32 is kept as."""
+    T, C = x.shape
+    x = torch.nn.functional.pad(x, (0, -C % GROUP)).view(T, -1, GROUP)
+    bits = x.abs().amax(-1).view(torch.int32)
+    exps = (bits >> 23) - 6 + ((bits & 0x7FFFFF) >= 0x7F0000)
+    exps = torch.where(bits == 0, 0, exps.clamp(min=1))
+    q = torch.round(x * ((254 - exps) << 23).view(torch.float32)[..., None])
+    return q.to(torch.int8).view(T, -1), exps.to(torch.uint8)
+
+
+def _gate(c, gen, dt):
+    if c["gate"] == "none":
+        return None
+    if c["gate"] == "vector":
+        return 0.5 + 0.1 * _normal(gen, 1, c["C"])
+    return (0.5 + 0.2 * _normal(gen, c["T"] // c["R"], c["C"])).to(dt)
+
+
+def _stats(x, kind, eps):
+    m = x.mean(1) if kind == "layer" else torch.zeros_like(x[:, 0])
+    v = (x - m[:, None]).square().mean(1)
+    return torch.stack((m, 1.0 / torch.sqrt(v + eps)), 1)
+
+
+def prepare(c, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt = DTYPES[c["dtype"]]
+    s = dict(c, dt=dt, eps=1e-5)
+    if c["op"] == "codes":
+        s["x"] = _activations(gen, c["T"], c["ld"]).to(dt)[:, c["ld"] - c["C"]:]
+    elif c["op"] == "glu":
+        h = _activations(gen, c["T"], (2 if c["gated"] else 1) * c["F"]).to(dt)
+        s["gate"], s["up"] = h[:, :c["F"]], h[:, c["F"]:] if c["gated"] else None
+        s["dout"] = (0.01 * _normal(gen, c["T"], c["F"])).to(dt)
+    elif c["op"] == "wgrad":
+        s["dy"] = (0.01 * _normal(gen, c["T"], c["N"])).to(dt)
+        s["codes"], s["exps"] = _encode(_activations(gen, c["T"], c["K"]))
+        s["scale"] = 1 + 0.2 * _normal(gen, c["K"]) if c["affine"] != "none" else None
+        s["shift"] = 0.1 * _normal(gen, c["K"]) if c["affine"] == "shift" else None
+    else:
+        T, C = c["T"], c["C"]
+        w = lambda: 1 + 0.2 * _normal(gen, C)  # noqa: E731
+        s["alpha"] = 0.7
+        s["gate_values"] = _gate(c, gen, dt)
+        s["post_weight"] = w() if c["post"] != "none" else None
+        s["post_bias"] = 0.1 * _normal(gen, C) if c["post"] == "layer" else None
+        s["pre_weight"] = w()
+        s["pre_bias"] = 0.1 * _normal(gen, C) if c["pre"] == "layer" else None
+        b = _activations(gen, T, C).to(dt)
+        r = (2 * _activations(gen, T, C)).to(dt)
+        if c["op"] == "resnorm_fwd":
+            s["r"], s["b"] = r, b
+        else:
+            r32, b32 = r.float(), b.float()
+            s["pre_stats"] = _stats(r32, c["pre"], 1e-5)
+            s["post_stats"] = _stats(b32, c["post"], 1e-5) if c["post"] != "none" else None
+            if c["source"] == "codes":
+                norm = lambda x, st: (x - st[:, :1]) * st[:, 1:]  # noqa: E731
+                s["codes_n"], s["exps_n"] = _encode(norm(r32, s["pre_stats"]))
+                if c["post"] != "none":
+                    b32 = norm(b32, s["post_stats"])
+                s["codes_b"], s["exps_b"] = _encode(b32)
+            else:
+                s["r_out"], s["b"] = r, b
+            s["dr_out"] = (0.01 * _normal(gen, T, C)).to(dt)
+            s["dn"] = (0.01 * _normal(gen, T, C)).to(dt)
+    return s
+
+
+# ---------------------------------------------------------------------------
+# plain forms
+
+def _decode(codes, exps, C):
+    T = codes.shape[0]
+    scale = (exps.to(torch.int32) << 23).view(torch.float32)
+    return (codes.view(T, -1, GROUP).float() * scale[..., None]).view(T, -1)[:, :C]
+
+
+def _act(g, act):
+    """act(g) and act'(g)."""
+    if act == "silu":
+        sg = 1 / (1 + torch.exp(-g))
+        return g * sg, sg * (1 + g * (1 - sg))
+    if act == "gelu":
+        cdf = 0.5 * (1 + torch.erf(g * math.sqrt(0.5)))
+        return g * cdf, cdf + g * torch.exp(-0.5 * g * g) * (1 / math.sqrt(2 * math.pi))
+    k = math.sqrt(2 / math.pi)
+    t = torch.tanh(k * (g + 0.044715 * g * g * g))
+    return (0.5 * g * (1 + t),
+            0.5 * (1 + t) + 0.5 * g * (1 - t * t) * k * (1 + 3 * 0.044715 * g * g))
+
+
+def _plain_glu(s):
+    g, dout = s["gate"].float(), s["dout"].float()
+    a = _act(g, s["act"])[0]
+    gh = _decode(*_encode(g), s["F"])
+    ah, slope = _act(gh, s["act"])
+    if not s["gated"]:
+        return dict(out=a, dgate=dout * slope, again=ah)
+    u = s["up"].float()
+    uh = _decode(*_encode(u), s["F"])
+    return dict(out=a * u, dgate=dout * uh * slope, dup=dout * ah, again=ah * uh)
+
+
+def _plain_wgrad(s):
+    dy, x = s["dy"].float(), _decode(s["codes"], s["exps"], s["K"])
+    if s["scale"] is not None:
+        x = x * s["scale"]
+    if s["shift"] is not None:
+        x = x + s["shift"]
+    out = dict(dw=dy.t() @ x)
+    if s["bias"]:
+        out["dbias"] = dy.sum(0)
+    return out
+
+
+def _spread(gate, T):
+    """Gate rows [G, C] for T rows."""
+    return gate.float().repeat_interleave(T // gate.shape[0], 0) if gate.shape[0] > 1 \
+        else gate.float()
+
+
+def _normed(x, kind, eps):
+    if kind == "layer":
+        x = x - x.mean(1, keepdim=True)
+    rstd = 1 / torch.sqrt((x * x).mean(1, keepdim=True) + eps)
+    return x * rstd
+
+
+def _affine(x, w, b):
+    return x * w if b is None else x * w + b
+
+
+def _plain_resnorm_fwd(s):
+    r, b = s["r"].float(), s["b"].float()
+    xb = b if s["post"] == "none" else _normed(b, s["post"], s["eps"])
+    p = xb if s["post"] == "none" else _affine(xb, s["post_weight"], s["post_bias"])
+    if s["gate_values"] is not None:
+        p = p * _spread(s["gate_values"], s["T"])
+    ro = r + s["alpha"] * p
+    xn = _normed(ro, s["pre"], s["eps"])
+    out = dict(r_out=ro, n=_affine(xn, s["pre_weight"], s["pre_bias"]))
+    if s["keep"]:
+        out["xhat_b"] = _decode(*_encode(xb), s["C"])
+        out["xhat_n"] = _decode(*_encode(xn), s["C"])
+    return out
+
+
+def _norm_grad(dy, xhat, kind, rstd):
+    """Gradient through the normalisation, from that of its xhat."""
+    d = dy - xhat * (dy * xhat).mean(1, keepdim=True)
+    if kind == "layer":
+        d = d - dy.mean(1, keepdim=True)
+    return d * rstd
+
+
+def _plain_resnorm_bwd(s):
+    C, T = s["C"], s["T"]
+    if s["source"] == "codes":
+        xn = _decode(s["codes_n"], s["exps_n"], C)
+        xb = _decode(s["codes_b"], s["exps_b"], C)
+    else:
+        xn, xb = s["r_out"].float(), s["b"].float()
+        xn = (xn - s["pre_stats"][:, :1]) * s["pre_stats"][:, 1:]
+        if s["post"] != "none":
+            xb = (xb - s["post_stats"][:, :1]) * s["post_stats"][:, 1:]
+    dn = s["dn"].float()
+    D = s["dr_out"].float() + _norm_grad(dn * s["pre_weight"], xn, s["pre"],
+                                         s["pre_stats"][:, 1:])
+    out = dict(dr=D, dpre_weight=(dn * xn).sum(0))
+    if s["pre"] == "layer":
+        out["dpre_bias"] = dn.sum(0)
+    dz = s["alpha"] * D
+    p = xb if s["post"] == "none" else _affine(xb, s["post_weight"], s["post_bias"])
+    if s["gate_values"] is not None:
+        out["dgate"] = (dz * p).view(-1, s["R"], C).sum(1).to(s["gate_values"].dtype)
+        dz = dz * _spread(s["gate_values"], T)
+    if s["post"] == "none":
+        out["db"] = dz
+        return out
+    out["dpost_weight"] = (dz * xb).sum(0)
+    if s["post"] == "layer":
+        out["dpost_bias"] = dz.sum(0)
+    out["db"] = _norm_grad(dz * s["post_weight"], xb, s["post"], s["post_stats"][:, 1:])
+    return out
+
+
+#: Outputs in the storage type; the others are float32.
+STORED = ("x", "out", "again", "dgate", "dup", "r_out", "n", "dr", "db")
+#: 8-bit values: a code times a power of two, exact in bfloat16.
+CODED = ("xhat_b", "xhat_n")
+
+
+def _plain(s):
+    if s["op"] == "codes":
+        out = dict(x=_decode(*_encode(s["x"].float()), s["C"]))
+    else:
+        out = {"glu": _plain_glu, "wgrad": _plain_wgrad, "resnorm_fwd": _plain_resnorm_fwd,
+               "resnorm_bwd": _plain_resnorm_bwd}[s["op"]](s)
+    gate = out.pop("dgate", None) if s["op"] == "resnorm_bwd" else None
+    out = {k: v.to(s["dt"]) if k in STORED else v.bfloat16() if k in CODED else v
+           for k, v in out.items()}
+    if gate is not None:
+        out["dgate"] = gate
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the library's operators
+
+def _own(s):
+    import place_batchnorm_activation_amd as iabn
+    dt = s["dt"]
+    new = lambda *shape, dtype=dt: torch.empty(*shape, device="cuda", dtype=dtype)  # noqa: E731
+    f32 = torch.float32
+    if s["op"] == "codes":
+        T, C = s["T"], s["C"]
+        codes, exps = iabn.codes_empty(T, C, "cuda")
+        x = new(T, C)
+        iabn.iabn_codes_pack(s["x"], codes, exps)
+        iabn.iabn_codes_unpack(codes, exps, x)
+        return dict(x=x)
+    if s["op"] == "glu":
+        T, F = s["T"], s["F"]
+        out, again, dh = new(T, F), new(T, F), new(T, (2 if s["gated"] else 1) * F)
+        dgate, dup = dh[:, :F], dh[:, F:] if s["gated"] else None
+        cg, eg = iabn.codes_empty(T, F, "cuda")
+        cu, eu = iabn.codes_empty(T, F, "cuda") if s["gated"] else (None, None)
+        iabn.iabn_glu_forward(s["gate"], s["up"], out, s["act"], cg, eg, cu, eu)
+        iabn.iabn_glu_backward(cg, eg, cu, eu, s["dout"], dgate, dup, s["act"], out=again)
+        d = dict(out=out, dgate=dgate, again=again)
+        return dict(d, dup=dup) if s["gated"] else d
+    if s["op"] == "wgrad":
+        T, N, K = s["T"], s["N"], s["K"]
+        dw = new(N, K, dtype=f32)
+        dbias = new(N, dtype=f32) if s["bias"] else None
+        ws = iabn.linear_wgrad_workspace(T, N, K, dt, "cuda")
+        iabn.iabn_linear_wgrad(s["dy"], s["codes"], s["exps"], dw, ws, scale=s["scale"],
+                               shift=s["shift"], dbias=dbias)
+        return dict(dw=dw, dbias=dbias) if s["bias"] else dict(dw=dw)
+    T, C = s["T"], s["C"]
+    layer = iabn.ResNormSpec(C, post=s["post"], pre=s["pre"], alpha=s["alpha"], eps=s["eps"],
+                         post_weight=s["post_weight"], post_bias=s["post_bias"],
+                         pre_weight=s["pre_weight"], pre_bias=s["pre_bias"])
+    if s["op"] == "resnorm_fwd":
+        out = dict(r_out=new(T, C), n=new(T, C))
+        kept = {}
+        if s["keep"]:
+            kept["codes_b"], kept["exps_b"] = iabn.codes_empty(T, C, "cuda")
+            kept["codes_n"], kept["exps_n"] = iabn.codes_empty(T, C, "cuda")
+            kept["post_stats"] = new(T, 2, dtype=f32) if s["post"] != "none" else None
+            kept["pre_stats"] = new(T, 2, dtype=f32)
+        iabn.iabn_resnorm_forward(layer, s["r"], s["b"], out["r_out"], out["n"],
+                                  gate=s["gate_values"], **kept)
+        if s["keep"]:
+            out["xhat_b"] = new(T, C, dtype=torch.bfloat16)
+            out["xhat_n"] = new(T, C, dtype=torch.bfloat16)
+            iabn.iabn_codes_unpack(kept["codes_b"], kept["exps_b"], out["xhat_b"])
+            iabn.iabn_codes_unpack(kept["codes_n"], kept["exps_n"], out["xhat_n"])
+        return out
+    out = dict(dr=new(T, C), db=new(T, C), dpre_weight=new(C, dtype=f32))
+    if s["pre"] == "layer":
+        out["dpre_bias"] = new(C, dtype=f32)
+    if s["post"] != "none":
+        out["dpost_weight"] = new(C, dtype=f32)
+    if s["post"] == "layer":
+        out["dpost_bias"] = new(C, dtype=f32)
+    if s["gate_values"] is not None:
+        out["dgate"] = torch.empty_like(s["gate_values"])
+    ws = iabn.resnorm_workspace(T, C, s["R"], "cuda")
+    names = ("codes_b", "exps_b", "codes_n", "exps_n") if s["source"] == "codes" else ("r_out", "b")
+    saved = {k: s[k] for k in names}
+    iabn.iabn_resnorm_backward(layer, s["dr_out"], s["dn"], ws, pre_stats=s["pre_stats"],
+                               post_stats=s["post_stats"], gate=s["gate_values"], **saved, **out)
+    return out
+
+
+def run(s):
+    return _own(s) if own else _plain(s)
+
+
+# ---------------------------------------------------------------------------
+# the definitions in 64 bits
+
+def _pow2(e):
+    """2^e in float64, from its bits (pow() may be an ulp off, which moves ties)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def _code64(x):
+    """x [T, C] as its codes stand for it: for each 32 values of a row the smallest
+    power of two 2^e, e >= -126, under which the largest of them rounds to at most
+    127; each value to the nearest multiple of it, ties to even."""
+    T, C = x.shape
+    full = torch.zeros(T, (C + 31) // 32 * 32, dtype=torch.float64, device=x.device)
+    full[:, :C] = x
+    full = full.reshape(-1, 32)
+    m, k = torch.frexp(full.abs().max(1).values)          # max = m * 2^k, 1/2 <= m < 1
+    step = _pow2(torch.where(m * 128 < 127.5, k - 7, k - 6).clamp(min=-126))[:, None]
+    return (torch.round(full / step) * step).reshape(T, -1)[:, :C]
+
+
+def _read64(s, name, C):
+    q = s["codes" + name].double()
+    e = s["exps" + name].long().repeat_interleave(32, 1)
+    return torch.where(e > 0, q * _pow2(e - 127), 0.0)[:, :C]
+
+
+def _act64(x, act):
+    if act == "gelu_tanh":
+        c = (2 / math.pi) ** 0.5
+        inner = c * (x + 0.044715 * x ** 3)
+        th = torch.tanh(inner)
+        return x * (1 + th) / 2, (1 + th) / 2 + x / 2 / torch.cosh(inner) ** 2 * \
+            c * (1 + 0.134145 * x ** 2)
+    if act == "gelu":
+        phi = torch.special.ndtr(x)
+        return x * phi, phi + x * torch.exp(-x * x / 2) / (2 * math.pi) ** 0.5
+    s = torch.sigmoid(x)
+    return x * s, s + x * s * torch.sigmoid(-x)
+
+
+def exact(c, seed):
+    s = prepare(c, seed)
+    d = {k: v.double() if isinstance(v, torch.Tensor) and v.is_floating_point() else v
+         for k, v in s.items()}
+    if c["op"] == "codes":
+        return dict(x=_code64(d["x"]))
+    if c["op"] == "glu":
+        gk = _code64(d["gate"])
+        value, slope = _act64(gk, c["act"])
+        first = _act64(d["gate"], c["act"])[0]
+        if not c["gated"]:
+            return dict(out=first, dgate=d["dout"] * slope, again=value)
+        uk = _code64(d["up"])
+        return dict(out=first * d["up"], dgate=slope * uk * d["dout"], dup=value * d["dout"],
+                    again=value * uk)
+    if c["op"] == "wgrad":
+        x = _read64(s, "", c["K"])
+        x = x * (1.0 if d["scale"] is None else d["scale"]) + \
+            (0.0 if d["shift"] is None else d["shift"])
+        out = dict(dw=torch.mm(d["dy"].t().contiguous(), x))
+        if c["bias"]:
+            out["dbias"] = d["dy"].sum(0)
+        return out
+    T, C, R = c["T"], c["C"], c["R"]
+    gate = torch.ones(1, 1, 1, dtype=torch.float64, device="cuda") if d["gate_values"] is None \
+        else d["gate_values"][:, None, :]
+
+    def scaled(x, name):
+        w, b = d[name + "_weight"], d[name + "_bias"]
+        return x * (1.0 if w is None else w) + (0.0 if b is None else b)
+
+    def unit(x, kind):
+        if kind == "none":
+            return x
+        mean = x.mean(1, keepdim=True) if kind == "layer" else 0.0
+        return (x - mean) / torch.sqrt(((x - mean) ** 2).mean(1, keepdim=True) + c_eps)
+
+    c_eps = s["eps"]
+    if c["op"] == "resnorm_fwd":
+        xb = unit(d["b"], c["post"])
+        branch = scaled(xb, "post").reshape(-1, R, C) if d["gate_values"] is not None else \
+            scaled(xb, "post")[None]
+        r_out = d["r"] + s["alpha"] * (gate * branch).reshape(T, C)
+        xn = unit(r_out, c["pre"])
+        # the codes of a computed value have no single right answer: a difference in
+        # the last bit of xhat moves those next to a tie by a whole step
+        kept = dict(xhat_b=None, xhat_n=None) if c["keep"] else {}
+        return dict(r_out=r_out, n=scaled(xn, "pre"), **kept)
+
+    def through(g, xhat, kind, stats):
+        """g^T d(xhat)/d(input) of a row: rstd (g - [mean g] - xhat mean(g xhat))."""
+        if kind == "none":
+            return g
+        flat = g.mean(1, keepdim=True) if kind == "layer" else 0.0
+        return stats[:, 1:] * (g - flat - xhat * (g * xhat).mean(1, keepdim=True))
+
+    if c["source"] == "codes":
+        xn, xb = _read64(s, "_n", C), _read64(s, "_b", C)
+    else:
+        xn = (d["r_out"] - d["pre_stats"][:, :1]) * d["pre_stats"][:, 1:]
+        xb = d["b"] if c["post"] == "none" else \
+            (d["b"] - d["post_stats"][:, :1]) * d["post_stats"][:, 1:]
+    dr = d["dr_out"] + through(d["dn"] * d["pre_weight"], xn, c["pre"], d["pre_stats"])
+    out = dict(dr=dr, dpre_weight=(d["dn"] * xn).sum(0))
+    if c["pre"] == "layer":
+        out["dpre_bias"] = d["dn"].sum(0)
+    rows = (s["alpha"] * dr).reshape(-1, R, C) if d["gate_values"] is not None else \
+        s["alpha"] * dr[None]
+    if d["gate_values"] is not None:
+        out["dgate"] = (rows * scaled(xb, "post").reshape(-1, R, C)).sum(1)
+    dp = (rows * gate).reshape(T, C)
+    if c["post"] != "none":
+        out["dpost_weight"] = (dp * xb).sum(0)
+        dp_x = dp * d["post_weight"]
+    else:
+        dp_x = dp
+    if c["post"] == "layer":
+        out["dpost_bias"] = dp.sum(0)
+    out["db"] = through(dp_x, xb, c["post"], d["post_stats"])
+    return out
