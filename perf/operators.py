@@ -68,13 +68,15 @@ def listed():
 
 
 def _log_int(rng, lo, hi):
-    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+    v = max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+    return v + 1 if v % 1536 == 0 else v
 
 
 def _ragged(rng, v):
     """A size near v: odd, a multiple of 8, or a multiple of 128."""
     m = rng.choice((1, 8, 128))
-    return max(1, v | 1) if m == 1 else max(m, v // m * m)
+    v = max(1, v | 1) if m == 1 else max(m, v // m * m)
+    return v + 8 if v % 1536 == 0 else v
 
 
 def draw(rng):
@@ -84,7 +86,7 @@ def draw(rng):
     C = _ragged(rng, _log_int(rng, 64, 8192))
     T = max(1, min(T, (48 << 20) // C))
     if op == "codes":
-        return dict(op=op, T=T, C=C, ld=C * rng.choice((1, 3)), dtype=dtype)
+        return dict(op=op, T=T, C=C, ld=C + rng.choice((0, 1)) * _ragged(rng, C), dtype=dtype)
     if op == "glu":
         return dict(op=op, T=T, F=C, dtype=dtype,
                     act=rng.choice(("silu", "gelu", "gelu_tanh")), gated=rng.random() < 0.8)
