@@ -343,6 +343,144 @@ iabn_status iabn_forward_train_noalloc(void *x_inout,
                                        iabn_act act, float act_param, float eps, float momentum,
                                        hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Residual blocks kept in 8 bits.  The same trade for the blocks of a language
+ * model (row norms, gated activations, linear layers): what a block keeps for its
+ * backward is one byte an element instead of the tensor.
+ *
+ * Tensors here are rows x cols of the storage dtype, the columns contiguous and the
+ * rows `ld` elements apart (ld >= cols), so a slice of a wider buffer is taken as it
+ * is.  Any alignment of one element is accepted; widths that are no multiple of 8
+ * cost one element-wise access a row.  rows and cols stay below 2^31; offsets are
+ * 64-bit.  An output may be exactly an input of the same call (same pointer and
+ * ld) unless said otherwise, and must not overlap one in any other way; two slices of
+ * one buffer (equal ld, disjoint columns) do not overlap.  rows == 0 or cols == 0 is
+ * a no-op that succeeds (gradients summed over no rows are written as zeros).
+ *
+ * Codes: a tensor [rows, cols] is kept as
+ *   codes  int8  [rows, cols rounded up to 32], 16-byte aligned, and
+ *   exps   uint8 [rows, that / 32], one for each group of 32 along the row;
+ *   value = q * 2^(E - 127), |q| <= 127, E the smallest exponent (1 to 248) under which
+ *   the group's largest magnitude rounds to at most 127; q to nearest, ties to even
+ *   (magnitudes of 127.5 * 2^121 and above, which have none, become 127 * 2^121).
+ *   E = 0: a group of zeros.  E = 255: a group that held an infinity or a NaN; all
+ *   of it reads NaN.  Padding codes are zero.  Values are exact in bf16 (not always in
+ *   f16: they round, or overflow to infinity, when unpacked to it).
+ */
+
+/* codes and exps of x [rows, cols].  Reads x once. */
+iabn_status iabn_codes_pack(const void *x, int64_t ldx, int64_t rows, int64_t cols,
+                            iabn_dtype dtype, int8_t *codes, uint8_t *exps, hipStream_t stream);
+
+/* y = scale_c * value + shift_c, rounded once; scale and shift fp32 [cols], either
+ * may be NULL (1 and 0). */
+iabn_status iabn_codes_unpack(const int8_t *codes, const uint8_t *exps, int64_t rows,
+                              int64_t cols, const float *scale, const float *shift, void *y,
+                              int64_t ldy, iabn_dtype dtype, hipStream_t stream);
+
+/* Activations of the gated unit: SiLU x*sigmoid(x), GELU x*Phi(x), and GELU with the
+ * tanh form of Phi. */
+typedef enum iabn_glu_act { IABN_GLU_SILU = 0, IABN_GLU_GELU = 1, IABN_GLU_GELU_TANH = 2 } iabn_glu_act;
+
+/* out = act(gate) * up, or act(gate) without up (NULL), from the tensors as they are;
+ * and their codes for the backward: codes_gate / exps_gate with codes_up / exps_up
+ * (no codes_up without up), or all NULL (inference).  out may be exactly gate or up. */
+iabn_status iabn_glu_forward(const void *gate, int64_t ldgate, const void *up, int64_t ldup,
+                             void *out, int64_t ldout, int64_t rows, int64_t cols,
+                             iabn_dtype dtype, iabn_glu_act act, int8_t *codes_gate,
+                             uint8_t *exps_gate, int8_t *codes_up, uint8_t *exps_up,
+                             hipStream_t stream);
+
+/* Backward from the codes, g' and u' their values (u' = 1 without codes_up):
+ *   dgate = dout * u' * act'(g'), dup = dout * act(g') (with codes_up),
+ *   out   = act(g') * u', when not NULL: the next layer's input rebuilt.
+ * dgate, dup and out may each be exactly dout. */
+iabn_status iabn_glu_backward(const int8_t *codes_gate, const uint8_t *exps_gate,
+                              const int8_t *codes_up, const uint8_t *exps_up, const void *dout,
+                              int64_t lddout, void *dgate, int64_t lddgate, void *dup,
+                              int64_t lddup, void *out, int64_t ldout, int64_t rows, int64_t cols,
+                              iabn_dtype dtype, iabn_glu_act act, hipStream_t stream);
+
+/* Bytes of workspace of iabn_linear_wgrad; 0 when it needs none (and for invalid
+ * arguments).  Depends on the arguments and the device's CU count. */
+size_t iabn_linear_wgrad_workspace_size(int64_t rows, int64_t n, int64_t k, iabn_dtype dtype);
+
+/* Weight gradient of y = x W^T + bias, W [n, k], from the codes of x [rows, k]:
+ *   dw = (dw +) dy^T (scale * x + shift), dbias = (dbias +) sum over rows of dy,
+ * the bracketed terms with accumulate != 0.  dy [rows, n] of `dtype`; dw [n, k], rows
+ * lddw apart, of dw_dtype; scale, shift fp32 [k] or NULL; dbias fp32 [n] or NULL.
+ * Sums are fp32; the products are exact (codes are exact in bf16, and f16 and f32
+ * values of dy enter as two and three bf16 parts).  workspace: device, 16-byte
+ * aligned, iabn_linear_wgrad_workspace_size bytes; it carries no status word. */
+iabn_status iabn_linear_wgrad(const void *dy, int64_t lddy, iabn_dtype dtype, const int8_t *codes,
+                              const uint8_t *exps, const float *scale, const float *shift,
+                              void *dw, int64_t lddw, iabn_dtype dw_dtype, float *dbias,
+                              int accumulate, int64_t rows, int64_t n, int64_t k,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Row norms: RMS x * rstd, layer (x - mean) * rstd, rstd = 1/sqrt(mean of squares of
+ * what is scaled + eps). */
+typedef enum iabn_norm { IABN_NORM_NONE = 0, IABN_NORM_RMS = 1, IABN_NORM_LAYER = 2 } iabn_norm;
+
+/* The boundary between two residual blocks: the block's output b goes through the
+ * post-norm, its gate and the residual scale into the residual stream r, and the
+ * pre-norm makes the next block's input of it:
+ *   r' = r + alpha * g * post(b),   n = pre(r'),   norm(x) = xhat * weight + bias.
+ * weights and biases are fp32 [cols], NULL for 1 and 0.  gate: NULL, or
+ * [rows / rows_per_gate, cols] contiguous of gate_dtype (f32 or the storage dtype),
+ * each gate row for rows_per_gate (a divisor of rows) consecutive rows: rows for a
+ * learned vector, a sample's rows, or 1.  rows_per_gate is ignored without a gate.
+ * cols <= 16384. */
+typedef struct iabn_resnorm {
+    int64_t rows, cols;
+    iabn_dtype dtype;
+    iabn_norm post, pre;
+    const float *post_weight, *post_bias, *pre_weight, *pre_bias;
+    float alpha, eps;
+    const void *gate;
+    iabn_dtype gate_dtype;
+    int64_t rows_per_gate;
+} iabn_resnorm;
+
+/* Forward.  b NULL: r' = r (the first norm of a network).  r_out NULL: r' is not
+ * written; n is written unless pre is none.  n is formed from the unrounded r'.
+ * post_stats, pre_stats: fp32 [rows, 2], mean and rstd, or NULL.  codes_b / exps_b:
+ * codes of post's xhat (of b itself when post is none), codes_n / exps_n: codes of
+ * pre's xhat; NULL when the backward will read the tensors themselves.  r_out and n
+ * may each be exactly r or b, but not one another. */
+iabn_status iabn_resnorm_forward(const iabn_resnorm *layer, const void *r, int64_t ldr,
+                                 const void *b, int64_t ldb, void *r_out, int64_t ldr_out,
+                                 void *n, int64_t ldn, float *post_stats, float *pre_stats,
+                                 int8_t *codes_b, uint8_t *exps_b, int8_t *codes_n,
+                                 uint8_t *exps_n, hipStream_t stream);
+
+/* Bytes of workspace of iabn_resnorm_backward (0 for an empty problem and invalid
+ * arguments); rows_per_gate as in the layer, any value >= 1 without a gate. */
+size_t iabn_resnorm_workspace_size(int64_t rows, int64_t cols, int64_t rows_per_gate);
+
+/* Backward, from dr_out (gradient of r'; NULL: zero) and dn (of n; NULL: zero), and
+ * either the stored r_out and b or the codes (not a mixture), with the forward's
+ * statistics:
+ *   D  = dr_out + rstd (q - [<q>] - xhat <q xhat>), q = dn * pre_weight   -> dr
+ *   dz = alpha * D; dgate = sum dz * post(b); h = g * dz * post_weight
+ *   db = rstd_b (h - [<h>] - xhat_b <h xhat_b>)       [.]: layer norms only
+ * dr may be NULL; db NULL: the branch gets no gradients (and dpost_*, dgate must be
+ * NULL).  dpost_*, dpre_* fp32 [cols], dgate of gate_dtype shaped as gate; each may be
+ * NULL.  b (codes_b) is needed with db for a post-norm or dgate only.  dr and db may be
+ * exactly dr_out or dn, but not one another, and must not overlap what was saved.
+ * workspace: device, 16-byte aligned; it carries no status word.  Sums over rows are
+ * fp32 within a block of rows and finished in fp64, in a fixed order. */
+iabn_status iabn_resnorm_backward(const iabn_resnorm *layer, const void *dr_out,
+                                  int64_t lddr_out, const void *dn, int64_t lddn,
+                                  const void *r_out, int64_t ldr_out, const void *b, int64_t ldb,
+                                  const int8_t *codes_n, const uint8_t *exps_n,
+                                  const int8_t *codes_b, const uint8_t *exps_b,
+                                  const float *post_stats, const float *pre_stats, void *dr,
+                                  int64_t lddr, void *db, int64_t lddb, float *dpost_weight,
+                                  float *dpost_bias, float *dpre_weight, float *dpre_bias,
+                                  void *dgate, void *workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+
 /* Describes, as a short text, the kernels that iabn_forward_train and
  * iabn_backward launch for this problem when every tensor pointer is 16-byte
  * aligned (aligned16 != 0) or not, e.g.

@@ -325,3 +325,11 @@ def shape_of(t: torch.Tensor, layout) -> tuple:
     else:
         N, H, W, C = t.shape
     return int(N), int(C), int(H), int(W)
+
+
+# the residual-block operators (block.py binds them on the names above)
+from .block import (ResNormSpec, code_cols, codes_empty, iabn_codes_pack,  # noqa: E402,F401
+                    iabn_codes_unpack, iabn_glu_backward, iabn_glu_forward, iabn_linear_wgrad,
+                    iabn_linear_wgrad_workspace_size, iabn_resnorm_backward,
+                    iabn_resnorm_forward, iabn_resnorm_workspace_size, linear_wgrad_workspace,
+                    resnorm_workspace)

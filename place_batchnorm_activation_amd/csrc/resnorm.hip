@@ -1,0 +1,727 @@
+// The boundary between two residual blocks: post-norm of the block's output, its
+// gate and residual scale, the residual sum, and the next block's pre-norm.
+//
+//   forward, a row of C columns:
+//     p = post(b),  r' = r + alpha * g * p,  n = pre(r')
+//     norm(x) = xhat * w + beta,  xhat = (x - mean) * rstd; RMS norms take mean 0,
+//     rstd = 1/sqrt(mean((x - mean)^2) + eps)
+//   backward, from dr' and dn, with <.> the mean over the row:
+//     q  = dn * w_pre
+//     D  = dr' + rstd_pre * (q - [<q>] - xn * <q xn>)           = dr
+//     dz = alpha * D,  dg = sum dz * p,  h = g * dz * w_post
+//     db = rstd_post * (h - [<h>] - xb * <h xb>)                [layer norms only]
+//     dw_pre = sum dn * xn, dbeta_pre = sum dn, dw_post = sum g dz xb, dbeta_post = sum g dz
+//   xn, xb come from the stored tensors and their statistics, or from 8-bit codes of
+//   xn and xb themselves (rows.hpp), which stand in for both tensors.
+//
+// The work is a few operations an element on 8 to 12 bytes of traffic: HBM bounds
+// it, so each kernel reads every tensor once and holds the row in registers across
+// its reductions.  n is formed from the unrounded r'.  Statistics, sums and
+// gradients of the vectors are fp32 (two passes over the registers for a layer
+// norm's variance, so that no digits cancel); the sums over row blocks are finished
+// in fp64, in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include "block.hpp"
+#include "rows.hpp"
+
+namespace iabn {
+
+namespace {
+
+// Sum over the wave, in every lane: shifts within rows of 16 lanes, then broadcasts of
+// a row's last lane into the next ones; lane 63 ends with the total.
+__device__ __forceinline__ float wave_total(float v)
+{
+    auto step = [&](auto ctrl, auto rows) {
+        v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v),
+                                                         decltype(ctrl)::value,
+                                                         decltype(rows)::value, 0xF, false));
+    };
+    using std::integral_constant;
+    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});   // row_shr:1
+    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});   // row_shr:2
+    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});   // row_shr:4
+    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});   // row_shr:8
+    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});   // row_bcast:15
+    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});   // row_bcast:31
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+
+// Sums over the TPR threads that hold a row.  Wider rows exchange wave totals
+// through `slots` (kSlots x 2 x waves floats): consecutive calls take consecutive
+// slots, so that one barrier a call suffices.
+constexpr int kSlots = 4;
+
+template <int TPR>
+struct RowSum {
+    static constexpr int kWaves = TPR / kWave;
+    float (*slots)[2][kWaves];
+    int at = 0;
+
+    __device__ __forceinline__ void operator()(float& a, float& b)
+    {
+        a = wave_total(a);
+        b = wave_total(b);
+        if constexpr (kWaves > 1) {
+            float (*s)[kWaves] = slots[at];
+            at = (at + 1) % kSlots;
+            const int w = threadIdx.x / kWave;
+            if (threadIdx.x % kWave == 0) {
+                s[0][w] = a;
+                s[1][w] = b;
+            }
+            __syncthreads();
+            a = b = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                a += s[0][i];
+                b += s[1][i];
+            }
+        }
+    }
+    __device__ __forceinline__ void operator()(float& a)
+    {
+        float b = 0.f;
+        (*this)(a, b);
+    }
+};
+
+// xhat of a row held as NV vectors a thread, in place, and its statistics.
+template <int NV, class SUM>
+__device__ __forceinline__ void normalise(float (&x)[NV][8], const int (&col)[NV], int C, bool layer,
+                                          float inv_c, float eps, SUM& sum, float& mean,
+                                          float& rstd)
+{
+    mean = 0.f;
+    if (layer) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mean += x[k][e];
+        sum(mean);
+        mean *= inv_c;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[k][e] = col[k] + e < C ? x[k][e] - mean : 0.f;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[k][e], x[k][e], s);
+    sum(s);
+    rstd = 1.f / sqrtf(fmaf(s, inv_c, eps));
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[k][e] *= rstd;
+}
+
+// Eight gate values of row `row` (gate rows cover R rows each).
+template <int DT>
+__device__ __forceinline__ void load_gate(const void* gate, bool f32, int64_t grow, int64_t C,
+                                          uint32_t c, float (&g)[8])
+{
+    if (f32) widen8<kF32>(load8<kF32>(row_ptr<kF32>(gate, grow, C), c, int(C)), g);
+    else widen8<DT>(load8<DT>(row_ptr<DT>(gate, grow, C), c, int(C)), g);
+}
+
+// TPR threads a row, NV vectors a thread.
+template <int DT, int TPR, int NV>
+__global__ __launch_bounds__((TPR > kThreads ? TPR : kThreads)) void k_resnorm_fwd(ResnormFwd a,
+                                                                                   FastDiv dr)
+{
+    constexpr int NT = TPR > kThreads ? TPR : kThreads;
+    constexpr int RPW = NT / TPR;                     // rows a workgroup holds
+    __shared__ float slots[kSlots][2][TPR / kWave];
+    RowSum<TPR> sum{slots};
+    const int t = threadIdx.x % TPR;
+    const int C = int(a.C);
+    const float inv_c = 1.f / float(a.C);
+    const int64_t Cp = code_pitch(a.C);
+    int col[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        col[k] = (t + k * TPR) * kRowV;
+    }
+    const int64_t step = int64_t(gridDim.x) * RPW;
+    // uniform over a wave (and a barrier's workgroup)
+    const int sub = RPW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
+    for (int64_t row = int64_t(blockIdx.x) * RPW + sub; row < a.T; row += step) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) asm volatile("" : "+v"(col[k]));    // as in the backward
+        Raw8<DT> rr[NV];
+        float x[NV][8];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) rr[k] = load8<DT>(row_ptr<DT>(a.r, row, a.ldr), col[k], C);
+        float mean, rstd;
+        if (a.b) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                widen8<DT>(load8<DT>(row_ptr<DT>(a.b, row, a.ldb), col[k], C), x[k]);
+            if (a.post != kNormNone) {
+                normalise<NV>(x, col, C, a.post == kNormLayer, inv_c, a.eps, sum, mean, rstd);
+                if (a.post_stats && t == 0) {
+                    a.post_stats[2 * row] = mean;
+                    a.post_stats[2 * row + 1] = rstd;
+                }
+            }
+            const int64_t grow = a.gate ? fast_div(uint32_t(row), dr) : 0;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (a.codes_b) {
+                    uint32_t E;
+                    const uint2 q = encode8(x[k], E);
+                    store_codes(a.codes_b + row * Cp, a.exps_b + row * (Cp / kGroup), Cp,
+                                col[k], q, E);
+                }
+                float v[8];
+                if (a.post != kNormNone) {
+                    float w[8], o[8];
+                    load_cols(a.post_w, col[k], C, 1.f, w);
+                    load_cols(a.post_b, col[k], C, 0.f, o);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[k][e] = fmaf(x[k][e], w[e], o[e]);
+                }
+                if (a.gate) {
+                    float g[8];
+                    load_gate<DT>(a.gate, a.gate_f32, grow, a.C, col[k], g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[k][e] *= g[e];
+                }
+                widen8<DT>(rr[k], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[k][e] = fmaf(a.alpha, x[k][e], v[e]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) widen8<DT>(rr[k], x[k]);
+        }
+        if (a.r_out) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) store8<DT>(row_ptr<DT>(a.r_out, row, a.ldro), col[k], C, x[k]);
+        }
+        if (a.pre == kNormNone) continue;
+        normalise<NV>(x, col, C, a.pre == kNormLayer, inv_c, a.eps, sum, mean, rstd);
+        if (a.pre_stats && t == 0) {
+            a.pre_stats[2 * row] = mean;
+            a.pre_stats[2 * row + 1] = rstd;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (a.codes_n) {
+                uint32_t E;
+                const uint2 q = encode8(x[k], E);
+                store_codes(a.codes_n + row * Cp, a.exps_n + row * (Cp / kGroup), Cp,
+                                col[k], q, E);
+            }
+            float w[8], o[8];
+            load_cols(a.pre_w, col[k], C, 1.f, w);
+            load_cols(a.pre_b, col[k], C, 0.f, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[k][e] = fmaf(x[k][e], w[e], o[e]);
+            store8<DT>(row_ptr<DT>(a.n, row, a.ldn), col[k], C, x[k]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+
+// A saved vector: the stored tensor's elements, or codes and exponent.
+template <int DT, bool CODES>
+struct Saved {
+    Raw8<DT> raw;
+    __device__ __forceinline__ void load(const void* x, int64_t ld, const int8_t*, const uint8_t*,
+                                         int64_t row, int64_t, uint32_t c, int C)
+    {
+        raw = load8<DT>(row_ptr<DT>(x, row, ld), c, C);
+    }
+    __device__ __forceinline__ void xhat(float mean, float rstd, float (&v)[8]) const
+    {
+        widen8<DT>(raw, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * rstd;
+    }
+};
+
+template <int DT>
+struct Saved<DT, true> {
+    uint2 q;
+    uint32_t E;
+    __device__ __forceinline__ void load(const void*, int64_t, const int8_t* codes,
+                                         const uint8_t* exps, int64_t row, int64_t Cp,
+                                         uint32_t c, int)
+    {
+        q = make_uint2(0u, 0u);
+        E = 0;
+        if (c < Cp) {
+            q = *reinterpret_cast<const uint2*>(codes + row * Cp + c);
+            E = (exps + row * (Cp / kGroup))[c / kGroup];
+        }
+    }
+    __device__ __forceinline__ void xhat(float, float, float (&v)[8]) const { decode8(q, E, v); }
+};
+
+// How the rows are dealt: every workgroup walks rows of whole gate groups
+// (cpg == 1: gpw groups each), or a part of one group's rows (cpg > 1 workgroups
+// a group, rc rows each), so that no workgroup holds a share of two gate sums.
+// Without a gate all rows are one group.
+struct RowDeal {
+    int64_t R, cpg, rc, gpw, grid;
+};
+
+RowDeal deal_rows(int64_t T, int64_t R, int64_t target)
+{
+    RowDeal d;
+    d.R = R;
+    const int64_t per = max64(1, ceil_div(T, target));
+    if (R >= 2 * per) {
+        d.cpg = ceil_div(R, per);
+        d.rc = ceil_div(R, d.cpg);
+        d.cpg = ceil_div(R, d.rc);
+        d.gpw = 1;
+        d.grid = T / R * d.cpg;
+    } else {
+        d.cpg = 1;
+        d.rc = R;
+        d.gpw = max64(1, per / R);
+        d.grid = ceil_div(T / R, d.gpw);
+    }
+    return d;
+}
+
+// The sums over rows that a call needs, in the order of their workspace sections.
+enum { kSumPreW = 0, kSumPreB, kSumPostW, kSumPostB, kSumGate, kSums };
+
+struct SumSlots {
+    int at[kSums];       // section of each sum, or -1
+    int count;
+};
+
+SumSlots sum_slots(const ResnormBwd& a, int64_t cpg)
+{
+    SumSlots s;
+    s.count = 0;
+    const bool want[kSums] = {a.dpre_w != nullptr, a.dpre_b != nullptr, a.dpost_w != nullptr,
+                              a.dpost_b != nullptr, a.dgate != nullptr && cpg > 1};
+    for (int i = 0; i < kSums; ++i) s.at[i] = want[i] ? s.count++ : -1;
+    return s;
+}
+
+// NT threads hold a row, NV vectors each.
+//
+// WIDE (4 vectors a thread): registers would not hold five sums of 32 columns next
+// to the row.  The phases then load the row's vectors again, from cache, instead
+// of keeping them, and the sums of the weights lie in LDS, each in its thread's
+// own slots.
+template <int DT, int NT, int NV, bool CODES, bool BIAS, bool GATE, bool WIDE>
+__global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, SumSlots ss,
+                                                    float* part)
+{
+    __shared__ float slots[kSlots][2][NT / kWave];
+    RowSum<NT> sum{slots};
+    const int C = int(a.C);
+    const float inv_c = 1.f / float(a.C);
+    const int64_t Cp = code_pitch(a.C);
+    const bool has_b = a.db != nullptr;
+    const bool pre = a.pre != kNormNone && a.dn;
+    const bool read_b = has_b && (a.post != kNormNone || (GATE && a.dgate));
+    int col[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        col[k] = (int(threadIdx.x) + k * NT) * kRowV;
+    }
+    // sums: 0 pre weight, 1 post weight, 2 pre bias, 3 post bias, 4 gate
+    constexpr int kInLds = WIDE ? 2 : 0, kInRegs = 5 - kInLds;
+    float s_v[kInRegs][NV][8];
+    __shared__ float4 s_lds[WIDE ? 4 * NV : 1][WIDE ? NT : 1];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int s = 0; s < kInRegs; ++s)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_v[s][k][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * kInLds; ++i)
+            s_lds[i * NV + k][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // adds to sum s of vector k
+    auto add = [&](auto s_, int k, const float (&v)[8]) {
+        constexpr int s = decltype(s_)::value;
+        if constexpr (s >= kInLds) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_v[s - kInLds][k][e] += v[e];
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4& q = s_lds[(2 * s + h) * NV + k][threadIdx.x];
+                q = make_float4(q.x + v[4 * h], q.y + v[4 * h + 1], q.z + v[4 * h + 2],
+                                q.w + v[4 * h + 3]);
+            }
+        }
+    };
+    // sum s of vector k
+    auto get = [&](auto s_, int k, float (&v)[8]) {
+        constexpr int s = decltype(s_)::value;
+        if constexpr (s >= kInLds) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = s_v[s - kInLds][k][e];
+        } else {
+            const float4 q0 = s_lds[2 * s * NV + k][threadIdx.x];
+            const float4 q1 = s_lds[(2 * s + 1) * NV + k][threadIdx.x];
+            v[0] = q0.x; v[1] = q0.y; v[2] = q0.z; v[3] = q0.w;
+            v[4] = q1.x; v[5] = q1.y; v[6] = q1.z; v[7] = q1.w;
+        }
+    };
+    using std::integral_constant;
+    constexpr integral_constant<int, 0> kPreW{};
+    constexpr integral_constant<int, 1> kPostW{};
+    constexpr integral_constant<int, 2> kPreB{};
+    constexpr integral_constant<int, 3> kPostB{};
+    constexpr integral_constant<int, 4> kGateS{};
+    // keeps the loads of one vector from moving over another's work, which would
+    // hold all of them in registers at once
+    auto fence = [&](int k) {
+        if constexpr (WIDE) asm volatile("" : "+v"(col[k]) : : "memory");
+    };
+
+    const int64_t group0 = int64_t(blockIdx.x) / d.cpg * d.gpw;
+    const int64_t row0 = group0 * d.R + int64_t(blockIdx.x) % d.cpg * d.rc;
+    const int64_t row1 = d.cpg > 1 ? dmin(row0 + d.rc, (group0 + 1) * d.R)
+                                   : dmin(row0 + d.gpw * d.R, a.T);
+    int64_t grow = group0, in_group = 0;       // gate row, rows of it seen (cpg == 1)
+
+    for (int64_t row = row0; row < row1; ++row) {
+        // everything that follows from the columns (addresses, masks of a ragged
+        // end) is formed anew in each row: held over the loop it takes the registers
+        // that the row needs
+#pragma unroll
+        for (int k = 0; k < NV; ++k) asm volatile("" : "+v"(col[k]));
+        Raw8<DT> dn[NV], dro[NV];
+        Saved<DT, CODES> sn[NV], sb[NV];
+        auto load_pre = [&](int k) {
+            dro[k] = Raw8<DT>{};
+            if (a.dr_out) dro[k] = load8<DT>(row_ptr<DT>(a.dr_out, row, a.lddro), col[k], C);
+            if (pre) {
+                dn[k] = load8<DT>(row_ptr<DT>(a.dn, row, a.lddn), col[k], C);
+                sn[k].load(a.r_out, a.ldro, a.codes_n, a.exps_n, row, Cp, col[k], C);
+            }
+        };
+        auto load_post = [&](int k) {
+            if (read_b) sb[k].load(a.b, a.ldb, a.codes_b, a.exps_b, row, Cp, col[k], C);
+        };
+        if constexpr (!WIDE) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                load_pre(k);
+                load_post(k);
+            }
+        }
+        float mn = 0.f, rn = 0.f, mb = 0.f, rb = 1.f;
+        if (pre) {
+            mn = a.pre_stats[2 * row];
+            rn = a.pre_stats[2 * row + 1];
+        }
+        if (has_b && a.post != kNormNone) {
+            mb = a.post_stats[2 * row];
+            rb = a.post_stats[2 * row + 1];
+        }
+
+        // <q xn>, <q>, and the sums of the pre-norm's vectors
+        float c1 = 0.f, c0 = 0.f;
+        if (pre) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                fence(k);
+                if constexpr (WIDE) load_pre(k);
+                float g[8], x[8], w[8];
+                widen8<DT>(dn[k], g);
+                sn[k].xhat(mn, rn, x);
+                load_cols(a.pre_w, col[k], C, 1.f, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    c0 = fmaf(g[e], w[e], c0);
+                    x[e] *= g[e];
+                    c1 = fmaf(x[e], w[e], c1);
+                }
+                add(kPreW, k, x);
+                if constexpr (BIAS) add(kPreB, k, g);
+            }
+            sum(c1, c0);
+            c1 *= inv_c;
+            c0 = a.pre == kNormLayer ? c0 * inv_c : 0.f;
+        }
+
+        // D, and dz = alpha*g*D with its sums
+        float D[NV][8];
+        float e1 = 0.f, e0 = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            fence(k);
+            if constexpr (WIDE) load_pre(k);
+            widen8<DT>(dro[k], D[k]);
+            if (pre) {
+                float g[8], x[8], w[8];
+                widen8<DT>(dn[k], g);
+                sn[k].xhat(mn, rn, x);
+                load_cols(a.pre_w, col[k], C, 1.f, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    D[k][e] = fmaf(rn, fmaf(g[e], w[e], -c0) - x[e] * c1, D[k][e]);
+            }
+            if (a.dr) store8<DT>(row_ptr<DT>(a.dr, row, a.lddr), col[k], C, D[k]);
+            if (!has_b) continue;
+            if constexpr (WIDE) load_post(k);
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, w[8];
+            if (read_b) sb[k].xhat(mb, rb, x);
+            if (a.post != kNormNone) load_cols(a.post_w, col[k], C, 1.f, w);
+            if constexpr (GATE) {
+                float g[8];
+                load_gate<DT>(a.gate, a.gate_f32, grow, a.C, col[k], g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) D[k][e] *= a.alpha;
+                float p[8];
+                load_cols(a.post != kNormNone ? a.post_b : nullptr, col[k], C, 0.f, p);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    p[e] = D[k][e] * (a.post != kNormNone ? fmaf(x[e], w[e], p[e]) : x[e]);
+                add(kGateS, k, p);
+                if (a.dgate && d.R == 1) {
+                    if (a.gate_f32) store8<kF32>(row_ptr<kF32>(a.dgate, row, a.C), col[k], C, p);
+                    else store8<DT>(row_ptr<DT>(a.dgate, row, a.C), col[k], C, p);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) D[k][e] *= g[e];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) D[k][e] *= a.alpha;
+            }
+            if (a.post != kNormNone) {
+                if constexpr (BIAS) add(kPostB, k, D[k]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] *= D[k][e];
+                    e1 = fmaf(x[e], w[e], e1);
+                    D[k][e] *= w[e];
+                    e0 += D[k][e];
+                }
+                add(kPostW, k, x);
+            }
+        }
+        if constexpr (GATE) {
+            // a whole group's gate sum is done: write it and start the next
+            if (d.cpg == 1 && ++in_group == d.R) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    float v[8];
+                    get(kGateS, k, v);
+                    if (a.dgate && d.R > 1) {
+                        if (a.gate_f32) store8<kF32>(row_ptr<kF32>(a.dgate, grow, a.C), col[k], C, v);
+                        else store8<DT>(row_ptr<DT>(a.dgate, grow, a.C), col[k], C, v);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s_v[kInRegs - 1][k][e] = 0.f;
+                }
+                in_group = 0;
+                ++grow;
+            }
+        }
+        if (!has_b) continue;
+        if (a.post != kNormNone) {
+            sum(e1, e0);
+            e1 *= inv_c;
+            e0 = a.post == kNormLayer ? e0 * inv_c : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            fence(k);
+            if (a.post != kNormNone) {
+                float x[8];
+                if constexpr (WIDE) load_post(k);
+                sb[k].xhat(mb, rb, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) D[k][e] = rb * (D[k][e] - e0 - x[e] * e1);
+            }
+            store8<DT>(row_ptr<DT>(a.db, row, a.lddb), col[k], C, D[k]);
+        }
+    }
+
+    // this workgroup's share of the sums: section s, workgroup, column
+    auto put = [&](int section, auto s_, int k) {
+        if (section < 0) return;
+        float v[8];
+        get(s_, k, v);
+        store8<kF32>(row_ptr<kF32>(part, int64_t(section) * d.grid + blockIdx.x, Cp), col[k], C, v);
+    };
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        put(ss.at[kSumPreW], kPreW, k);
+        put(ss.at[kSumPostW], kPostW, k);
+        if constexpr (BIAS) {
+            put(ss.at[kSumPreB], kPreB, k);
+            put(ss.at[kSumPostB], kPostB, k);
+        }
+        if constexpr (GATE) put(ss.at[kSumGate], kGateS, k);
+    }
+}
+
+// Adds the workgroups' shares in fp64, in their order: blockIdx.y below ss.count
+// (without the gate) one vector's sum over all of them, above it one gate row's over
+// its cpg.
+constexpr int kFinCols = 64, kFinRows = 16;
+
+template <int DT>
+__global__ __launch_bounds__(kFinCols* kFinRows) void k_resnorm_fin(ResnormBwd a, RowDeal d,
+                                                                    SumSlots ss,
+                                                                    const float* part)
+{
+    const int64_t Cp = code_pitch(a.C);
+    const int64_t c = int64_t(blockIdx.x) * kFinCols + threadIdx.x % kFinCols;
+    const int ph = threadIdx.x / kFinCols;
+    const bool gate = ss.at[kSumGate] >= 0;
+    const int vectors = ss.count - (gate ? 1 : 0);
+    const int y = blockIdx.y;
+    int64_t w0 = 0, w1 = d.grid;
+    int s = y;
+    if (y >= vectors) {
+        s = ss.at[kSumGate];
+        w0 = (y - vectors) * d.cpg;
+        w1 = w0 + d.cpg;
+    }
+    double v = 0.0;
+    if (c < a.C)
+        for (int64_t w = w0 + ph; w < w1; w += kFinRows)
+            v += double(part[(int64_t(s) * d.grid + w) * Cp + c]);
+    __shared__ double sh[kFinRows][kFinCols];
+    sh[ph][threadIdx.x % kFinCols] = v;
+    __syncthreads();
+    if (ph != 0 || c >= a.C) return;
+    for (int i = 1; i < kFinRows; ++i) v += sh[i][threadIdx.x % kFinCols];
+    const float f = float(v);
+    if (y >= vectors) {
+        const int64_t i = int64_t(y - vectors) * a.C + c;
+        if (a.gate_f32) static_cast<float*>(a.dgate)[i] = f;
+        else if constexpr (DT == kF32) static_cast<float*>(a.dgate)[i] = f;
+        else static_cast<uint16_t*>(a.dgate)[i] = pack1<DT>(f);
+    } else if (s == ss.at[kSumPreW]) a.dpre_w[c] = f;
+    else if (s == ss.at[kSumPreB]) a.dpre_b[c] = f;
+    else if (s == ss.at[kSumPostW]) a.dpost_w[c] = f;
+    else a.dpost_b[c] = f;
+}
+
+// Threads and vectors that hold a row of the backward.
+struct BwdShape {
+    int nt, nv;
+};
+
+BwdShape bwd_shape(int64_t C)
+{
+    const int64_t v = code_pitch(C) / kRowV;
+    if (v <= 64) return {64, 1};
+    if (v <= 128) return {64, 2};
+    if (v <= 256) return {128, 2};
+    if (v <= 512) return {256, 2};
+    if (v <= 1024) return {512, 2};
+    return {512, 4};
+}
+
+// Workgroups the row blocks are dealt to: 8 waves a CU (512 threads), and one
+// workgroup where a row takes more.
+int64_t bwd_target(int64_t C, int64_t cus)
+{
+    return cus * max64(1, 512 / bwd_shape(C).nt);
+}
+
+}  // namespace
+
+size_t resnorm_workspace_bytes(int64_t T, int64_t C, int64_t R, int64_t cus)
+{
+    if (T <= 0 || C <= 0) return 0;
+    const RowDeal d = deal_rows(T, R, bwd_target(C, cus));
+    return size_t(kSums) * size_t(d.grid) * size_t(code_pitch(C)) * 4;
+}
+
+void launch_resnorm_forward(const ResnormFwd& a, int dtype, int64_t cus, hipStream_t s)
+{
+    const int64_t v = code_pitch(a.C) / kRowV;
+    const FastDiv dr = make_fast_div(uint32_t(a.R));
+    with_dtype(dtype, [&](auto dt) {
+        auto go = [&](auto tpr, auto nv) {
+            constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+            constexpr int NT = TPR > kThreads ? TPR : kThreads;
+            const int64_t wgs = ceil_div(a.T, NT / TPR);
+            const dim3 grid(unsigned(min64(wgs, cus * (2048 / NT))));
+            hipLaunchKernelGGL((k_resnorm_fwd<decltype(dt)::value, TPR, NV>), grid, dim3(NT), 0,
+                               s, a, dr);
+        };
+        using std::integral_constant;
+        if (v <= 64) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+        else if (v <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+        else if (v <= 256) go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+        else if (v <= 512) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+        else if (v <= 1024) go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+        else go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    });
+}
+
+void launch_resnorm_backward(const ResnormBwd& a, int dtype, int64_t cus, void* ws,
+                             hipStream_t s)
+{
+    RowDeal d{a.R, 1, a.R, 1, 0};
+    if (a.T > 0) d = deal_rows(a.T, a.R, bwd_target(a.C, cus));
+    const SumSlots ss = sum_slots(a, d.cpg);
+    float* part = static_cast<float*>(ws);
+    const bool codes = a.codes_n != nullptr || a.codes_b != nullptr;
+    const bool bias = a.dpre_b != nullptr || a.dpost_b != nullptr;
+    const bool gate = a.gate != nullptr && a.db != nullptr;
+    const BwdShape sh = bwd_shape(a.C);
+    with_dtype(dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        using std::integral_constant;
+        using Y = std::true_type;
+        using N = std::false_type;
+        auto run = [&](auto nt, auto nv, auto cd, auto bi, auto ga) {
+            if (d.grid > 0)
+                hipLaunchKernelGGL(
+                    (k_resnorm_bwd<DT, decltype(nt)::value, decltype(nv)::value,
+                                   decltype(cd)::value, decltype(bi)::value, decltype(ga)::value,
+                                   (decltype(nv)::value > 2)>),
+                    dim3(unsigned(d.grid)), dim3(decltype(nt)::value), 0, s, a, d, ss, part);
+        };
+        auto on = [](bool v, auto&& f) {
+            if (v) f(Y{});
+            else f(N{});
+        };
+        auto flags = [&](auto nt, auto nv) {
+            on(codes, [&](auto cd) {
+                on(bias, [&](auto bi) {
+                    on(gate, [&](auto ga) { run(nt, nv, cd, bi, ga); });
+                });
+            });
+        };
+        using I64 = integral_constant<int, 64>;
+        using I128 = integral_constant<int, 128>;
+        using I256 = integral_constant<int, 256>;
+        using I512 = integral_constant<int, 512>;
+        using I1 = integral_constant<int, 1>;
+        using I2 = integral_constant<int, 2>;
+        using I4 = integral_constant<int, 4>;
+        if (sh.nt == 64 && sh.nv == 1) flags(I64{}, I1{});
+        else if (sh.nt == 64) flags(I64{}, I2{});
+        else if (sh.nt == 128) flags(I128{}, I2{});
+        else if (sh.nt == 256) flags(I256{}, I2{});
+        else if (sh.nv == 2) flags(I512{}, I2{});
+        else flags(I512{}, I4{});
+        const int vectors = ss.count - (ss.at[kSumGate] >= 0 ? 1 : 0);
+        const int64_t gates = ss.at[kSumGate] >= 0 ? a.T / a.R : 0;
+        if (vectors + gates > 0)
+            hipLaunchKernelGGL((k_resnorm_fin<DT>),
+                               dim3(unsigned(ceil_div(a.C, kFinCols)), unsigned(vectors + gates)),
+                               dim3(kFinCols * kFinRows), 0, s, a, d, ss, part);
+    });
+}
+
+}  // namespace iabn
