@@ -299,6 +299,7 @@ iabn_status iabn_linear_wgrad(const void* dy, int64_t lddy, iabn_dtype dtype, co
     if (n == 0 || k == 0) return IABN_OK;
     // tiles of 128 x 128 in 31 bits of workgroups
     if (double(ceil_div(n, 128)) * double(ceil_div(k, 128)) > 2.0e9) return IABN_ERR_UNSUPPORTED;
+    if (lddy >= kWgradMaxLd || k >= kWgradMaxLd) return IABN_ERR_UNSUPPORTED;
     const Rows out{dw, lddw, n, k, esize(dw_dtype)};
     const Rows in{dy, lddy, rows, n, esize(dtype)};
     IABN_TRY(check_rows(out));

@@ -67,7 +67,8 @@ struct GluBwd {
 void launch_glu_forward(const GluFwd& a, int64_t T, int64_t F, int dtype, int act, hipStream_t s);
 void launch_glu_backward(const GluBwd& a, int64_t T, int64_t F, int dtype, int act, hipStream_t s);
 
-// wgrad.hip
+// wgrad.hip: lanes reach up to 16 rows of dy and of the codes in 32 bits of bytes
+constexpr int64_t kWgradMaxLd = int64_t(1) << 26;
 struct WgradArgs {
     const void* dy;
     int64_t lddy;

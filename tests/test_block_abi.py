@@ -88,6 +88,7 @@ def test_wgrad_validation():
     assert wgrad(dw=4 * M + 2) == MISALIGNED and wgrad(s=M + 1) == MISALIGNED
     assert wgrad(c=2 * M + 4) == MISALIGNED and wgrad(db=M + 2) == MISALIGNED
     assert wgrad(dw=M) == INVALID and wgrad(dw=2 * M) == INVALID
+    assert wgrad(ldd=1 << 26) == UNSUPPORTED and wgrad(K=1 << 26, ldw=1 << 26) == UNSUPPORTED
     big = dict(T=100000, N=64, K=48)
     need = lib.iabn_linear_wgrad_workspace_size(100000, 64, 48, BF16)
     assert need > 0

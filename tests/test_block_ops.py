@@ -315,6 +315,15 @@ def test_linear_wgrad(T, N, K, dtype, affine):
         assert torch.equal(low, dw2.to(dt))
 
 
+@pytest.mark.parametrize("T,N,K", [(70, 2048, 2048), (200, 2053, 2090), (64, 4096, 1030),
+                                   (5, 1100, 4100)])
+@pytest.mark.parametrize("affine", ["scale", "shift"])
+def test_linear_wgrad_large_tiles(T, N, K, affine):
+    """Outputs of many tiles, whole and ragged; the sum over t is short, so that the
+    float64 form stays quick."""
+    test_linear_wgrad(T, N, K, torch.bfloat16, affine)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 def test_linear_wgrad_of_no_rows(dtype):
     dy = torch.empty(0, 6, device="cuda", dtype=dtype)
