@@ -40,6 +40,15 @@ inline void each_row_block(int64_t T, int64_t vectors_per_row, int64_t vectors_p
     }
 }
 
+// Calls f(std::true_type) when rows of C columns are whole vectors of 8, else
+// f(std::false_type).
+template <class F>
+inline void with_whole(int64_t C, F&& f)
+{
+    if (C % 8 == 0) f(std::true_type{});
+    else f(std::false_type{});
+}
+
 // codes.hip
 void launch_codes_pack(const void* x, int64_t ldx, int64_t T, int64_t C, int dtype, int8_t* codes,
                        uint8_t* exps, hipStream_t s);

@@ -16,7 +16,7 @@ namespace iabn {
 
 namespace {
 
-template <int DT>
+template <int DT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_codes_pack(const void* __restrict__ x, int64_t ldx,
                                                          int64_t row0, uint32_t nvec, uint32_t vpr,
                                                          FastDiv dv, int C,
@@ -29,13 +29,13 @@ __global__ __launch_bounds__(kThreads) void k_codes_pack(const void* __restrict_
     const int64_t row = row0 + r;
     const uint32_t c = (i - r * vpr) * kRowV, Cp = vpr * kRowV;
     float v[8];
-    widen8<DT>(load8<DT>(row_ptr<DT>(x, row, ldx), c, C), v);
+    widen8<DT>(load8<DT, WHOLE>(row_ptr<DT>(x, row, ldx), c, C), v);
     uint32_t E;
     const uint2 q = encode8(v, E);
     store_codes(codes + row * Cp, exps + row * (Cp / kGroup), Cp, c, q, E);
 }
 
-template <int DT>
+template <int DT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_codes_unpack(
     const int8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t row0,
     uint32_t nvec, uint32_t vpr, FastDiv dv, int C, const float* __restrict__ scale,
@@ -52,12 +52,12 @@ __global__ __launch_bounds__(kThreads) void k_codes_unpack(
             exps[row * (Cp / kGroup) + c / kGroup], v);
     if (scale || shift) {                   // uniform over the launch
         float a[8], b[8];
-        load_cols(scale, c, C, 1.f, a);
-        load_cols(shift, c, C, 0.f, b);
+        load_cols<WHOLE>(scale, c, C, 1.f, a);
+        load_cols<WHOLE>(shift, c, C, 0.f, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], a[e], b[e]);
     }
-    store8<DT>(row_ptr<DT>(y, row, ldy), c, C, v);
+    store8<DT, WHOLE>(row_ptr<DT>(y, row, ldy), c, C, v);
 }
 
 }  // namespace
@@ -67,12 +67,12 @@ void launch_codes_pack(const void* x, int64_t ldx, int64_t T, int64_t C, int dty
 {
     const int64_t vpr = code_pitch(C) / kRowV;
     const FastDiv dv = make_fast_div(uint32_t(vpr));
-    with_dtype(dtype, [&](auto d) {
+    with_dtype(dtype, [&](auto d) { with_whole(C, [&](auto whole) {
         each_row_block(T, vpr, kThreads, [&](int64_t row0, uint32_t nvec, dim3 grid) {
-            hipLaunchKernelGGL((k_codes_pack<decltype(d)::value>), grid, dim3(kThreads), 0, s, x,
+            hipLaunchKernelGGL((k_codes_pack<decltype(d)::value, decltype(whole)::value>), grid, dim3(kThreads), 0, s, x,
                                ldx, row0, nvec, uint32_t(vpr), dv, int(C), codes, exps);
         });
-    });
+    }); });
 }
 
 void launch_codes_unpack(const int8_t* codes, const uint8_t* exps, int64_t T, int64_t C,
@@ -81,13 +81,13 @@ void launch_codes_unpack(const int8_t* codes, const uint8_t* exps, int64_t T, in
 {
     const int64_t vpr = code_pitch(C) / kRowV;
     const FastDiv dv = make_fast_div(uint32_t(vpr));
-    with_dtype(dtype, [&](auto d) {
+    with_dtype(dtype, [&](auto d) { with_whole(C, [&](auto whole) {
         each_row_block(T, vpr, kThreads, [&](int64_t row0, uint32_t nvec, dim3 grid) {
-            hipLaunchKernelGGL((k_codes_unpack<decltype(d)::value>), grid, dim3(kThreads), 0, s,
+            hipLaunchKernelGGL((k_codes_unpack<decltype(d)::value, decltype(whole)::value>), grid, dim3(kThreads), 0, s,
                                codes, exps, row0, nvec, uint32_t(vpr), dv, int(C), scale, shift, y,
                                ldy);
         });
-    });
+    }); });
 }
 
 }  // namespace iabn

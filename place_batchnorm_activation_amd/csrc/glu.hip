@@ -63,7 +63,7 @@ __device__ __forceinline__ void glu_act(float x, float& f, float& d)
     }
 }
 
-template <int DT, int ACT>
+template <int DT, int ACT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_glu_fwd(GluFwd a, int64_t row0, uint32_t nvec,
                                                       uint32_t vpr, FastDiv dv, int F)
 {
@@ -73,9 +73,9 @@ __global__ __launch_bounds__(kThreads) void k_glu_fwd(GluFwd a, int64_t row0, ui
     const int64_t row = row0 + r;
     const uint32_t c = (i - r * vpr) * kRowV, Fp = vpr * kRowV;
     float g[8], u[8];
-    const Raw8<DT> rg = load8<DT>(row_ptr<DT>(a.gate, row, a.ldg), c, F);
+    const Raw8<DT> rg = load8<DT, WHOLE>(row_ptr<DT>(a.gate, row, a.ldg), c, F);
     if (a.up) {
-        const Raw8<DT> ru = load8<DT>(row_ptr<DT>(a.up, row, a.ldu), c, F);
+        const Raw8<DT> ru = load8<DT, WHOLE>(row_ptr<DT>(a.up, row, a.ldu), c, F);
         widen8<DT>(ru, u);
     }
     widen8<DT>(rg, g);
@@ -94,10 +94,10 @@ __global__ __launch_bounds__(kThreads) void k_glu_fwd(GluFwd a, int64_t row0, ui
         glu_act<ACT>(g[e], f, d);
         g[e] = a.up ? f * u[e] : f;
     }
-    store8<DT>(row_ptr<DT>(a.out, row, a.ldo), c, F, g);
+    store8<DT, WHOLE>(row_ptr<DT>(a.out, row, a.ldo), c, F, g);
 }
 
-template <int DT, int ACT>
+template <int DT, int ACT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_glu_bwd(GluBwd a, int64_t row0, uint32_t nvec,
                                                       uint32_t vpr, FastDiv dv, int F)
 {
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(kThreads) void k_glu_bwd(GluBwd a, int64_t row0, ui
     const int64_t row = row0 + r;
     const uint32_t c = (i - r * vpr) * kRowV, Fp = vpr * kRowV;
     if (c >= uint32_t(F)) return;
-    const Raw8<DT> ro = load8<DT>(row_ptr<DT>(a.dout, row, a.lddo), c, F);
+    const Raw8<DT> ro = load8<DT, WHOLE>(row_ptr<DT>(a.dout, row, a.lddo), c, F);
     float g[8], u[8], o[8];
     decode8(*reinterpret_cast<const uint2*>(a.codes_g + row * Fp + c),
             a.exps_g[row * (Fp / kGroup) + c / kGroup], g);
@@ -124,9 +124,9 @@ __global__ __launch_bounds__(kThreads) void k_glu_bwd(GluBwd a, int64_t row0, ui
         dg[e] = a.codes_u ? o[e] * u[e] * d : o[e] * d;
         o[e] = a.codes_u ? f * u[e] : f;
     }
-    store8<DT>(row_ptr<DT>(a.dgate, row, a.lddg), c, F, dg);
-    if (a.codes_u) store8<DT>(row_ptr<DT>(a.dup, row, a.lddu), c, F, du);
-    if (a.out) store8<DT>(row_ptr<DT>(a.out, row, a.ldo), c, F, o);
+    store8<DT, WHOLE>(row_ptr<DT>(a.dgate, row, a.lddg), c, F, dg);
+    if (a.codes_u) store8<DT, WHOLE>(row_ptr<DT>(a.dup, row, a.lddu), c, F, du);
+    if (a.out) store8<DT, WHOLE>(row_ptr<DT>(a.out, row, a.ldo), c, F, o);
 }
 
 template <class F>
@@ -146,12 +146,12 @@ void launch_glu_forward(const GluFwd& a, int64_t T, int64_t F, int dtype, int ac
     const int64_t vpr = code_pitch(F) / kRowV;
     const FastDiv dv = make_fast_div(uint32_t(vpr));
     with_dtype(dtype, [&](auto d) {
-        with_glu_act(act, [&](auto ac) {
+        with_glu_act(act, [&](auto ac) { with_whole(F, [&](auto whole) {
             each_row_block(T, vpr, kThreads, [&](int64_t row0, uint32_t nvec, dim3 grid) {
-                hipLaunchKernelGGL((k_glu_fwd<decltype(d)::value, decltype(ac)::value>), grid,
+                hipLaunchKernelGGL((k_glu_fwd<decltype(d)::value, decltype(ac)::value, decltype(whole)::value>), grid,
                                    dim3(kThreads), 0, s, a, row0, nvec, uint32_t(vpr), dv, int(F));
             });
-        });
+        }); });
     });
 }
 
@@ -160,12 +160,12 @@ void launch_glu_backward(const GluBwd& a, int64_t T, int64_t F, int dtype, int a
     const int64_t vpr = code_pitch(F) / kRowV;
     const FastDiv dv = make_fast_div(uint32_t(vpr));
     with_dtype(dtype, [&](auto d) {
-        with_glu_act(act, [&](auto ac) {
+        with_glu_act(act, [&](auto ac) { with_whole(F, [&](auto whole) {
             each_row_block(T, vpr, kThreads, [&](int64_t row0, uint32_t nvec, dim3 grid) {
-                hipLaunchKernelGGL((k_glu_bwd<decltype(d)::value, decltype(ac)::value>), grid,
+                hipLaunchKernelGGL((k_glu_bwd<decltype(d)::value, decltype(ac)::value, decltype(whole)::value>), grid,
                                    dim3(kThreads), 0, s, a, row0, nvec, uint32_t(vpr), dv, int(F));
             });
-        });
+        }); });
     });
 }
 

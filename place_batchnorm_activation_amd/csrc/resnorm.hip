@@ -119,17 +119,20 @@ __device__ __forceinline__ void normalise(float (&x)[NV][8], const int (&col)[NV
         for (int e = 0; e < 8; ++e) x[k][e] *= rstd;
 }
 
-// Eight gate values of row `row` (gate rows cover R rows each).
-template <int DT>
+// Eight gate values of gate row `grow` (1 without a gate).
+template <int DT, bool WHOLE>
 __device__ __forceinline__ void load_gate(const void* gate, bool f32, int64_t grow, int64_t C,
                                           uint32_t c, float (&g)[8])
 {
-    if (f32) widen8<kF32>(load8<kF32>(row_ptr<kF32>(gate, grow, C), c, int(C)), g);
-    else widen8<DT>(load8<DT>(row_ptr<DT>(gate, grow, C), c, int(C)), g);
+    if (!gate) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = 1.f;
+    } else if (f32) widen8<kF32>(load8<kF32, WHOLE>(row_ptr<kF32>(gate, grow, C), c, int(C)), g);
+    else widen8<DT>(load8<DT, WHOLE>(row_ptr<DT>(gate, grow, C), c, int(C)), g);
 }
 
 // TPR threads a row, NV vectors a thread.
-template <int DT, int TPR, int NV>
+template <int DT, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__((TPR > kThreads ? TPR : kThreads)) void k_resnorm_fwd(ResnormFwd a,
                                                                                    FastDiv dr)
 {
@@ -155,12 +158,12 @@ __global__ __launch_bounds__((TPR > kThreads ? TPR : kThreads)) void k_resnorm_f
         Raw8<DT> rr[NV];
         float x[NV][8];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) rr[k] = load8<DT>(row_ptr<DT>(a.r, row, a.ldr), col[k], C);
+        for (int k = 0; k < NV; ++k) rr[k] = load8<DT, WHOLE>(row_ptr<DT>(a.r, row, a.ldr), col[k], C);
         float mean, rstd;
         if (a.b) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                widen8<DT>(load8<DT>(row_ptr<DT>(a.b, row, a.ldb), col[k], C), x[k]);
+                widen8<DT>(load8<DT, WHOLE>(row_ptr<DT>(a.b, row, a.ldb), col[k], C), x[k]);
             if (a.post != kNormNone) {
                 normalise<NV>(x, col, C, a.post == kNormLayer, inv_c, a.eps, sum, mean, rstd);
                 if (a.post_stats && t == 0) {
@@ -180,14 +183,14 @@ __global__ __launch_bounds__((TPR > kThreads ? TPR : kThreads)) void k_resnorm_f
                 float v[8];
                 if (a.post != kNormNone) {
                     float w[8], o[8];
-                    load_cols(a.post_w, col[k], C, 1.f, w);
-                    load_cols(a.post_b, col[k], C, 0.f, o);
+                    load_cols<WHOLE>(a.post_w, col[k], C, 1.f, w);
+                    load_cols<WHOLE>(a.post_b, col[k], C, 0.f, o);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[k][e] = fmaf(x[k][e], w[e], o[e]);
                 }
                 if (a.gate) {
                     float g[8];
-                    load_gate<DT>(a.gate, a.gate_f32, grow, a.C, col[k], g);
+                    load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, col[k], g);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[k][e] *= g[e];
                 }
@@ -201,7 +204,7 @@ __global__ __launch_bounds__((TPR > kThreads ? TPR : kThreads)) void k_resnorm_f
         }
         if (a.r_out) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) store8<DT>(row_ptr<DT>(a.r_out, row, a.ldro), col[k], C, x[k]);
+            for (int k = 0; k < NV; ++k) store8<DT, WHOLE>(row_ptr<DT>(a.r_out, row, a.ldro), col[k], C, x[k]);
         }
         if (a.pre == kNormNone) continue;
         normalise<NV>(x, col, C, a.pre == kNormLayer, inv_c, a.eps, sum, mean, rstd);
@@ -218,11 +221,11 @@ __global__ __launch_bounds__((TPR > kThreads ? TPR : kThreads)) void k_resnorm_f
                                 col[k], q, E);
             }
             float w[8], o[8];
-            load_cols(a.pre_w, col[k], C, 1.f, w);
-            load_cols(a.pre_b, col[k], C, 0.f, o);
+            load_cols<WHOLE>(a.pre_w, col[k], C, 1.f, w);
+            load_cols<WHOLE>(a.pre_b, col[k], C, 0.f, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[k][e] = fmaf(x[k][e], w[e], o[e]);
-            store8<DT>(row_ptr<DT>(a.n, row, a.ldn), col[k], C, x[k]);
+            store8<DT, WHOLE>(row_ptr<DT>(a.n, row, a.ldn), col[k], C, x[k]);
         }
     }
 }
@@ -231,13 +234,13 @@ __global__ __launch_bounds__((TPR > kThreads ? TPR : kThreads)) void k_resnorm_f
 // backward
 
 // A saved vector: the stored tensor's elements, or codes and exponent.
-template <int DT, bool CODES>
+template <int DT, bool CODES, bool WHOLE>
 struct Saved {
     Raw8<DT> raw;
     __device__ __forceinline__ void load(const void* x, int64_t ld, const int8_t*, const uint8_t*,
                                          int64_t row, int64_t, uint32_t c, int C)
     {
-        raw = load8<DT>(row_ptr<DT>(x, row, ld), c, C);
+        raw = load8<DT, WHOLE>(row_ptr<DT>(x, row, ld), c, C);
     }
     __device__ __forceinline__ void xhat(float mean, float rstd, float (&v)[8]) const
     {
@@ -247,8 +250,8 @@ struct Saved {
     }
 };
 
-template <int DT>
-struct Saved<DT, true> {
+template <int DT, bool WHOLE>
+struct Saved<DT, true, WHOLE> {
     uint2 q;
     uint32_t E;
     __device__ __forceinline__ void load(const void*, int64_t, const int8_t* codes,
@@ -313,14 +316,16 @@ SumSlots sum_slots(const ResnormBwd& a, int64_t cpg)
 
 // NT threads hold a row, NV vectors each.
 //
-// WIDE (4 vectors a thread): registers would not hold five sums of 32 columns next
-// to the row.  The phases then load the row's vectors again, from cache, instead
-// of keeping them, and the sums of the weights lie in LDS, each in its thread's
-// own slots.
-template <int DT, int NT, int NV, bool CODES, bool BIAS, bool GATE, bool WIDE>
+// NV = 1: the next row is read while this one is worked on, and the vectors that all
+// rows use stay in registers.  NV = 2: a row's raw vectors stay in registers over its
+// phases.  NV = 4 (WIDE): they would not fit next to five sums of 32 columns; every phase
+// reads them again, from cache, and the sums of the weights lie in LDS, each in its
+// thread's own slots.
+template <int DT, int NT, int NV, bool CODES, bool BIAS, bool GATE, bool WHOLE>
 __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, SumSlots ss,
                                                     float* part)
 {
+    constexpr bool AHEAD = NV == 1, WIDE = NV == 4;
     __shared__ float slots[kSlots][2][NT / kWave];
     RowSum<NT> sum{slots};
     const int C = int(a.C);
@@ -394,41 +399,95 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
                                    : dmin(row0 + d.gpw * d.R, a.T);
     int64_t grow = group0, in_group = 0;       // gate row, rows of it seen (cpg == 1)
 
+    // what a row reads
+    struct RowIn {
+        Raw8<DT> dn[NV], dro[NV];
+        Saved<DT, CODES, WHOLE> sn[NV], sb[NV];
+        float mn, rn, mb, rb;
+    };
+    auto load_pre = [&](int64_t row, int k, RowIn& q) {
+        q.dro[k] = Raw8<DT>{};
+        if (a.dr_out) q.dro[k] = load8<DT, WHOLE>(row_ptr<DT>(a.dr_out, row, a.lddro), col[k], C);
+        if (pre) {
+            q.dn[k] = load8<DT, WHOLE>(row_ptr<DT>(a.dn, row, a.lddn), col[k], C);
+            q.sn[k].load(a.r_out, a.ldro, a.codes_n, a.exps_n, row, Cp, col[k], C);
+        }
+    };
+    auto load_post = [&](int64_t row, int k, RowIn& q) {
+        if (read_b) q.sb[k].load(a.b, a.ldb, a.codes_b, a.exps_b, row, Cp, col[k], C);
+    };
+    auto load_row = [&](int64_t row, RowIn& q) {
+        q.mn = q.rn = q.mb = 0.f;
+        q.rb = 1.f;
+        if (pre) {
+            q.mn = a.pre_stats[2 * row];
+            q.rn = a.pre_stats[2 * row + 1];
+        }
+        if (has_b && a.post != kNormNone) {
+            q.mb = a.post_stats[2 * row];
+            q.rb = a.post_stats[2 * row + 1];
+        }
+        if constexpr (!WIDE) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                load_pre(row, k, q);
+                load_post(row, k, q);
+            }
+        }
+    };
+    // the vectors that every row uses (rows of more vectors read them again each time)
+    float w_n[NV][8], w_b[NV][8], w_g[NV][8];
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            load_cols<WHOLE>(a.pre_w, col[k], C, 1.f, w_n[k]);
+            if (a.post != kNormNone) load_cols<WHOLE>(a.post_w, col[k], C, 1.f, w_b[k]);
+            if constexpr (GATE) {
+                if (row0 < row1) load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, col[k], w_g[k]);
+            }
+        }
+    }
+    auto pre_weight = [&](int k, float (&w)[8]) {
+        if constexpr (!AHEAD) {
+            load_cols<WHOLE>(a.pre_w, col[k], C, 1.f, w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = w_n[k][e];
+        }
+    };
+    auto post_weight = [&](int k, float (&w)[8]) {
+        if constexpr (!AHEAD) {
+            load_cols<WHOLE>(a.post_w, col[k], C, 1.f, w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = w_b[k][e];
+        }
+    };
+    auto gate_row = [&](int k, float (&w)[8]) {
+        if constexpr (!GATE) {
+        } else if constexpr (!AHEAD) {
+            load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, col[k], w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = w_g[k][e];
+        }
+    };
+
+    RowIn now, ahead;
+    if (AHEAD && row0 < row1) load_row(row0, now);
     for (int64_t row = row0; row < row1; ++row) {
         // everything that follows from the columns (addresses, masks of a ragged
         // end) is formed anew in each row: held over the loop it takes the registers
         // that the row needs
 #pragma unroll
         for (int k = 0; k < NV; ++k) asm volatile("" : "+v"(col[k]));
-        Raw8<DT> dn[NV], dro[NV];
-        Saved<DT, CODES> sn[NV], sb[NV];
-        auto load_pre = [&](int k) {
-            dro[k] = Raw8<DT>{};
-            if (a.dr_out) dro[k] = load8<DT>(row_ptr<DT>(a.dr_out, row, a.lddro), col[k], C);
-            if (pre) {
-                dn[k] = load8<DT>(row_ptr<DT>(a.dn, row, a.lddn), col[k], C);
-                sn[k].load(a.r_out, a.ldro, a.codes_n, a.exps_n, row, Cp, col[k], C);
-            }
-        };
-        auto load_post = [&](int k) {
-            if (read_b) sb[k].load(a.b, a.ldb, a.codes_b, a.exps_b, row, Cp, col[k], C);
-        };
-        if constexpr (!WIDE) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                load_pre(k);
-                load_post(k);
-            }
-        }
-        float mn = 0.f, rn = 0.f, mb = 0.f, rb = 1.f;
-        if (pre) {
-            mn = a.pre_stats[2 * row];
-            rn = a.pre_stats[2 * row + 1];
-        }
-        if (has_b && a.post != kNormNone) {
-            mb = a.post_stats[2 * row];
-            rb = a.post_stats[2 * row + 1];
-        }
+        if constexpr (AHEAD) load_row(row + 1 < row1 ? row + 1 : row, ahead);
+        else load_row(row, now);
+        const float mn = now.mn, rn = now.rn, mb = now.mb, rb = now.rb;
+        auto& dn = now.dn;
+        auto& dro = now.dro;
+        auto& sn = now.sn;
+        auto& sb = now.sb;
 
         // <q xn>, <q>, and the sums of the pre-norm's vectors
         float c1 = 0.f, c0 = 0.f;
@@ -436,11 +495,11 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 fence(k);
-                if constexpr (WIDE) load_pre(k);
+                if constexpr (WIDE) load_pre(row, k, now);
                 float g[8], x[8], w[8];
                 widen8<DT>(dn[k], g);
                 sn[k].xhat(mn, rn, x);
-                load_cols(a.pre_w, col[k], C, 1.f, w);
+                pre_weight(k, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     c0 = fmaf(g[e], w[e], c0);
@@ -461,37 +520,37 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             fence(k);
-            if constexpr (WIDE) load_pre(k);
+            if constexpr (WIDE) load_pre(row, k, now);
             widen8<DT>(dro[k], D[k]);
             if (pre) {
                 float g[8], x[8], w[8];
                 widen8<DT>(dn[k], g);
                 sn[k].xhat(mn, rn, x);
-                load_cols(a.pre_w, col[k], C, 1.f, w);
+                pre_weight(k, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     D[k][e] = fmaf(rn, fmaf(g[e], w[e], -c0) - x[e] * c1, D[k][e]);
             }
-            if (a.dr) store8<DT>(row_ptr<DT>(a.dr, row, a.lddr), col[k], C, D[k]);
+            if (a.dr) store8<DT, WHOLE>(row_ptr<DT>(a.dr, row, a.lddr), col[k], C, D[k]);
             if (!has_b) continue;
-            if constexpr (WIDE) load_post(k);
+            if constexpr (WIDE) load_post(row, k, now);
             float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, w[8];
             if (read_b) sb[k].xhat(mb, rb, x);
-            if (a.post != kNormNone) load_cols(a.post_w, col[k], C, 1.f, w);
+            if (a.post != kNormNone) post_weight(k, w);
             if constexpr (GATE) {
                 float g[8];
-                load_gate<DT>(a.gate, a.gate_f32, grow, a.C, col[k], g);
+                gate_row(k, g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) D[k][e] *= a.alpha;
                 float p[8];
-                load_cols(a.post != kNormNone ? a.post_b : nullptr, col[k], C, 0.f, p);
+                load_cols<WHOLE>(a.post != kNormNone ? a.post_b : nullptr, col[k], C, 0.f, p);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     p[e] = D[k][e] * (a.post != kNormNone ? fmaf(x[e], w[e], p[e]) : x[e]);
                 add(kGateS, k, p);
                 if (a.dgate && d.R == 1) {
-                    if (a.gate_f32) store8<kF32>(row_ptr<kF32>(a.dgate, row, a.C), col[k], C, p);
-                    else store8<DT>(row_ptr<DT>(a.dgate, row, a.C), col[k], C, p);
+                    if (a.gate_f32) store8<kF32, WHOLE>(row_ptr<kF32>(a.dgate, row, a.C), col[k], C, p);
+                    else store8<DT, WHOLE>(row_ptr<DT>(a.dgate, row, a.C), col[k], C, p);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) D[k][e] *= g[e];
@@ -519,17 +578,27 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
                     float v[8];
                     get(kGateS, k, v);
                     if (a.dgate && d.R > 1) {
-                        if (a.gate_f32) store8<kF32>(row_ptr<kF32>(a.dgate, grow, a.C), col[k], C, v);
-                        else store8<DT>(row_ptr<DT>(a.dgate, grow, a.C), col[k], C, v);
+                        if (a.gate_f32) store8<kF32, WHOLE>(row_ptr<kF32>(a.dgate, grow, a.C), col[k], C, v);
+                        else store8<DT, WHOLE>(row_ptr<DT>(a.dgate, grow, a.C), col[k], C, v);
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) s_v[kInRegs - 1][k][e] = 0.f;
                 }
                 in_group = 0;
                 ++grow;
+                if constexpr (AHEAD) {
+                    if (row + 1 < row1) {
+#pragma unroll
+                        for (int k = 0; k < NV; ++k)
+                            load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, col[k], w_g[k]);
+                    }
+                }
             }
         }
-        if (!has_b) continue;
+        if (!has_b) {
+            if constexpr (AHEAD) now = ahead;
+            continue;
+        }
         if (a.post != kNormNone) {
             sum(e1, e0);
             e1 *= inv_c;
@@ -540,13 +609,14 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
             fence(k);
             if (a.post != kNormNone) {
                 float x[8];
-                if constexpr (WIDE) load_post(k);
+                if constexpr (WIDE) load_post(row, k, now);
                 sb[k].xhat(mb, rb, x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) D[k][e] = rb * (D[k][e] - e0 - x[e] * e1);
             }
-            store8<DT>(row_ptr<DT>(a.db, row, a.lddb), col[k], C, D[k]);
+            store8<DT, WHOLE>(row_ptr<DT>(a.db, row, a.lddb), col[k], C, D[k]);
         }
+        if constexpr (AHEAD) now = ahead;
     }
 
     // this workgroup's share of the sums: section s, workgroup, column
@@ -554,7 +624,7 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
         if (section < 0) return;
         float v[8];
         get(s_, k, v);
-        store8<kF32>(row_ptr<kF32>(part, int64_t(section) * d.grid + blockIdx.x, Cp), col[k], C, v);
+        store8<kF32, true>(row_ptr<kF32>(part, int64_t(section) * d.grid + blockIdx.x, Cp), col[k], int(Cp), v);
     };
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -593,6 +663,7 @@ __global__ __launch_bounds__(kFinCols* kFinRows) void k_resnorm_fin(ResnormBwd a
     }
     double v = 0.0;
     if (c < a.C)
+#pragma unroll 8
         for (int64_t w = w0 + ph; w < w1; w += kFinRows)
             v += double(part[(int64_t(s) * d.grid + w) * Cp + c]);
     __shared__ double sh[kFinRows][kFinCols];
@@ -621,18 +692,17 @@ BwdShape bwd_shape(int64_t C)
 {
     const int64_t v = code_pitch(C) / kRowV;
     if (v <= 64) return {64, 1};
-    if (v <= 128) return {64, 2};
-    if (v <= 256) return {128, 2};
-    if (v <= 512) return {256, 2};
+    if (v <= 128) return {128, 1};
+    if (v <= 256) return {256, 1};
+    if (v <= 512) return {512, 1};
     if (v <= 1024) return {512, 2};
     return {512, 4};
 }
 
-// Workgroups the row blocks are dealt to: 8 waves a CU (512 threads), and one
-// workgroup where a row takes more.
+// Workgroups the row blocks are dealt to: 16 waves a CU.
 int64_t bwd_target(int64_t C, int64_t cus)
 {
-    return cus * max64(1, 512 / bwd_shape(C).nt);
+    return cus * max64(1, 1024 / bwd_shape(C).nt);
 }
 
 }  // namespace
@@ -654,8 +724,11 @@ void launch_resnorm_forward(const ResnormFwd& a, int dtype, int64_t cus, hipStre
             constexpr int NT = TPR > kThreads ? TPR : kThreads;
             const int64_t wgs = ceil_div(a.T, NT / TPR);
             const dim3 grid(unsigned(min64(wgs, cus * (2048 / NT))));
-            hipLaunchKernelGGL((k_resnorm_fwd<decltype(dt)::value, TPR, NV>), grid, dim3(NT), 0,
-                               s, a, dr);
+            with_whole(a.C, [&](auto whole) {
+                hipLaunchKernelGGL((k_resnorm_fwd<decltype(dt)::value, TPR, NV,
+                                                  decltype(whole)::value>),
+                                   grid, dim3(NT), 0, s, a, dr);
+            });
         };
         using std::integral_constant;
         if (v <= 64) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
@@ -683,12 +756,12 @@ void launch_resnorm_backward(const ResnormBwd& a, int dtype, int64_t cus, void* 
         using std::integral_constant;
         using Y = std::true_type;
         using N = std::false_type;
-        auto run = [&](auto nt, auto nv, auto cd, auto bi, auto ga) {
+        auto run = [&](auto nt, auto nv, auto cd, auto bi, auto ga, auto whole) {
             if (d.grid > 0)
                 hipLaunchKernelGGL(
                     (k_resnorm_bwd<DT, decltype(nt)::value, decltype(nv)::value,
-                                   decltype(cd)::value, decltype(bi)::value, decltype(ga)::value,
-                                   (decltype(nv)::value > 2)>),
+                                   decltype(cd)::value, decltype(bi)::value,
+                                   decltype(ga)::value, decltype(whole)::value>),
                     dim3(unsigned(d.grid)), dim3(decltype(nt)::value), 0, s, a, d, ss, part);
         };
         auto on = [](bool v, auto&& f) {
@@ -697,8 +770,13 @@ void launch_resnorm_backward(const ResnormBwd& a, int dtype, int64_t cus, void* 
         };
         auto flags = [&](auto nt, auto nv) {
             on(codes, [&](auto cd) {
+                // ragged rows take the kernel with every sum, whether wanted or not
+                if (a.C % kRowV != 0) {
+                    run(nt, nv, cd, Y{}, Y{}, N{});
+                    return;
+                }
                 on(bias, [&](auto bi) {
-                    on(gate, [&](auto ga) { run(nt, nv, cd, bi, ga); });
+                    on(gate, [&](auto ga) { run(nt, nv, cd, bi, ga, Y{}); });
                 });
             });
         };
@@ -709,10 +787,10 @@ void launch_resnorm_backward(const ResnormBwd& a, int dtype, int64_t cus, void* 
         using I1 = integral_constant<int, 1>;
         using I2 = integral_constant<int, 2>;
         using I4 = integral_constant<int, 4>;
-        if (sh.nt == 64 && sh.nv == 1) flags(I64{}, I1{});
-        else if (sh.nt == 64) flags(I64{}, I2{});
-        else if (sh.nt == 128) flags(I128{}, I2{});
-        else if (sh.nt == 256) flags(I256{}, I2{});
+        if (sh.nt == 64) flags(I64{}, I1{});
+        else if (sh.nt == 128) flags(I128{}, I1{});
+        else if (sh.nt == 256) flags(I256{}, I1{});
+        else if (sh.nv == 1) flags(I512{}, I1{});
         else if (sh.nv == 2) flags(I512{}, I2{});
         else flags(I512{}, I4{});
         const int vectors = ss.count - (ss.at[kSumGate] >= 0 ? 1 : 0);

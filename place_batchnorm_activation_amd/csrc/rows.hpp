@@ -60,16 +60,12 @@ __device__ __forceinline__ const char* row_ptr(const void* base, int64_t row, in
     return static_cast<const char*>(base) + row * ld * (DT == kF32 ? 4 : 2);
 }
 
-// v moved down by s elements (0 < s), zeros from above.
+// v moved down by s elements (0 < s < 8), zeros from above.
 template <int DT>
 __device__ __forceinline__ void shift_down(uint32_t (&w)[DT == kF32 ? 8 : 4], uint32_t s)
 {
     constexpr int N = DT == kF32 ? 8 : 4;
     uint32_t words = DT == kF32 ? s : s >> 1;      // whole words first, then half a word
-    if (s >= 8) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = 0u;
-    }
 #pragma unroll
     for (int b = 1; b < N; b *= 2)
 #pragma unroll
@@ -85,20 +81,33 @@ __device__ __forceinline__ void shift_down(uint32_t (&w)[DT == kF32 ? 8 : 4], ui
 }
 
 // Eight elements from column c of a row of C columns on; those past its end read as
-// zero.  The vector that holds the end is the row's last eight elements moved down,
-// so every load is one wide access without a branch; rows of fewer than eight columns
-// are read one by one.
-template <int DT>
+// zero.  WHOLE: C is a multiple of 8, and a vector is in the row or past it.  Otherwise
+// the vector that holds the end is the row's last eight elements moved down, so
+// every load is one wide access; rows of fewer than eight columns are read one by one.
+// (The ragged form takes dozens of vector instructions a load, which bounds kernels of
+// several loads a row: 16640 x 1152 in resnorm's backward took 167 us with it.)
+template <int DT, bool WHOLE>
 __device__ __forceinline__ Raw8<DT> load8(const char* row, uint32_t c, int C)
 {
     constexpr int N = DT == kF32 ? 8 : 4, es = DT == kF32 ? 4 : 2;
     Raw8<DT> r;
+#pragma unroll
+    for (int h = 0; h < N / 4; ++h) r.q[h] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (WHOLE) {
+        if (c < uint32_t(C)) {
+#pragma unroll
+            for (int h = 0; h < N / 4; ++h) r.q[h] = load16_any(row + c * es + 16 * h);
+        }
+        return r;
+    }
     uint32_t w[N];
     if (C >= kRowV) {
         const uint32_t last = uint32_t(C) - kRowV, at = c < last ? c : last;
+        if (c < uint32_t(C)) {
 #pragma unroll
-        for (int h = 0; h < N / 4; ++h) r.q[h] = load16_any(row + at * es + 16 * h);
-        if (c > last) {
+            for (int h = 0; h < N / 4; ++h) r.q[h] = load16_any(row + at * es + 16 * h);
+        }
+        if (c > last && c < uint32_t(C)) {
 #pragma unroll
             for (int h = 0; h < N / 4; ++h) {
                 w[4 * h] = r.q[h].x; w[4 * h + 1] = r.q[h].y;
@@ -109,20 +118,19 @@ __device__ __forceinline__ Raw8<DT> load8(const char* row, uint32_t c, int C)
             for (int h = 0; h < N / 4; ++h)
                 r.q[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
         }
-    } else {
+    } else if (c == 0) {
 #pragma unroll
         for (int i = 0; i < N; ++i) w[i] = 0u;
-        if (c == 0)
 #pragma unroll 1
-            for (int e = C - 1; e >= 0; --e) {
+        for (int e = C - 1; e >= 0; --e) {
 #pragma unroll
-                for (int i = N - 1; i >= 0; --i) {
-                    const uint32_t dn = i > 0 ? w[i - 1] : 0u;
-                    w[i] = DT == kF32 ? dn : __builtin_amdgcn_alignbyte(w[i], dn, 2);
-                }
-                if constexpr (DT == kF32) w[0] = reinterpret_cast<const uint32_t*>(row)[e];
-                else w[0] |= reinterpret_cast<const uint16_t*>(row)[e];
+            for (int i = N - 1; i >= 0; --i) {
+                const uint32_t dn = i > 0 ? w[i - 1] : 0u;
+                w[i] = DT == kF32 ? dn : __builtin_amdgcn_alignbyte(w[i], dn, 2);
             }
+            if constexpr (DT == kF32) w[0] = reinterpret_cast<const uint32_t*>(row)[e];
+            else w[0] |= reinterpret_cast<const uint16_t*>(row)[e];
+        }
 #pragma unroll
         for (int h = 0; h < N / 4; ++h)
             r.q[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
@@ -144,8 +152,8 @@ __device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8])
 }
 
 // Eight values at column c of a row of C columns, rounded once to the storage dtype;
-// those past its end are not written (four, two and one of the rest).
-template <int DT>
+// those past its end are not written (WHOLE as above; else four, two and one of the rest).
+template <int DT, bool WHOLE>
 __device__ __forceinline__ void store8(const char* row, uint32_t c, int C, const float (&v)[8])
 {
     constexpr int es = DT == kF32 ? 4 : 2;
@@ -164,6 +172,7 @@ __device__ __forceinline__ void store8(const char* row, uint32_t c, int C, const
             const u32x4_any_t a = {q.x, q.y, q.z, q.w};
             *reinterpret_cast<u32x4_any_t*>(p) = a;
         }
+    } else if constexpr (WHOLE) {
     } else if constexpr (DT == kF32) {
         if (nv & 4) {
             const u32x4_any_t a = {__float_as_uint(v[0]), __float_as_uint(v[1]),
@@ -196,11 +205,12 @@ __device__ __forceinline__ void store8(const char* row, uint32_t c, int C, const
 }
 
 // Eight of a per-column vector of C fp32 values (null: `none`); zero past its end.
+template <bool WHOLE>
 __device__ __forceinline__ void load_cols(const float* p, uint32_t c, int C, float none,
                                           float (&v)[8])
 {
     if (p) {
-        widen8<kF32>(load8<kF32>(reinterpret_cast<const char*>(p), c, C), v);
+        widen8<kF32>(load8<kF32, WHOLE>(reinterpret_cast<const char*>(p), c, C), v);
     } else {
         const int nv = valid8(int(c), C);
 #pragma unroll
