@@ -59,31 +59,40 @@ struct RowSum {
     float (*slots)[2][kWaves];
     int at = 0;
 
-    __device__ __forceinline__ void operator()(float& a, float& b)
+    template <int N>
+    __device__ __forceinline__ void add(float (&v)[N])
     {
-        a = wave_total(a);
-        b = wave_total(b);
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = wave_total(v[k]);
         if constexpr (kWaves > 1) {
             float (*s)[kWaves] = slots[at];
             at = (at + 1) % kSlots;
             const int w = threadIdx.x / kWave;
             if (threadIdx.x % kWave == 0) {
-                s[0][w] = a;
-                s[1][w] = b;
+#pragma unroll
+                for (int k = 0; k < N; ++k) s[k][w] = v[k];
             }
             __syncthreads();
-            a = b = 0.f;
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) {
-                a += s[0][i];
-                b += s[1][i];
+            for (int k = 0; k < N; ++k) {
+                v[k] = 0.f;
+#pragma unroll
+                for (int i = 0; i < kWaves; ++i) v[k] += s[k][i];
             }
         }
     }
+    __device__ __forceinline__ void operator()(float& a, float& b)
+    {
+        float v[2] = {a, b};
+        add(v);
+        a = v[0];
+        b = v[1];
+    }
     __device__ __forceinline__ void operator()(float& a)
     {
-        float b = 0.f;
-        (*this)(a, b);
+        float v[1] = {a};
+        add(v);
+        a = v[0];
     }
 };
 
@@ -316,16 +325,14 @@ SumSlots sum_slots(const ResnormBwd& a, int64_t cpg)
 
 // NT threads hold a row, NV vectors each.
 //
-// NV = 1: the next row is read while this one is worked on, and the vectors that all
-// rows use stay in registers.  NV = 2: a row's raw vectors stay in registers over its
-// phases.  NV = 4 (WIDE): they would not fit next to five sums of 32 columns; every phase
-// reads them again, from cache, and the sums of the weights lie in LDS, each in its
-// thread's own slots.
+// NV = 2: a row's raw vectors stay in registers over its phases.  NV = 4 (WIDE): they
+// would not fit next to five sums of 32 columns; every phase reads them again, from
+// cache, and the sums of the weights lie in LDS, each in its thread's own slots.
 template <int DT, int NT, int NV, bool CODES, bool BIAS, bool GATE, bool WHOLE>
 __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, SumSlots ss,
                                                     float* part)
 {
-    constexpr bool AHEAD = NV == 1, WIDE = NV == 4;
+    constexpr bool WIDE = NV == 4;
     __shared__ float slots[kSlots][2][NT / kWave];
     RowSum<NT> sum{slots};
     const int C = int(a.C);
@@ -435,54 +442,14 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
             }
         }
     };
-    // the vectors that every row uses (rows of more vectors read them again each time)
-    float w_n[NV][8], w_b[NV][8], w_g[NV][8];
-    if constexpr (AHEAD) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            load_cols<WHOLE>(a.pre_w, col[k], C, 1.f, w_n[k]);
-            if (a.post != kNormNone) load_cols<WHOLE>(a.post_w, col[k], C, 1.f, w_b[k]);
-            if constexpr (GATE) {
-                if (row0 < row1) load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, col[k], w_g[k]);
-            }
-        }
-    }
-    auto pre_weight = [&](int k, float (&w)[8]) {
-        if constexpr (!AHEAD) {
-            load_cols<WHOLE>(a.pre_w, col[k], C, 1.f, w);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = w_n[k][e];
-        }
-    };
-    auto post_weight = [&](int k, float (&w)[8]) {
-        if constexpr (!AHEAD) {
-            load_cols<WHOLE>(a.post_w, col[k], C, 1.f, w);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = w_b[k][e];
-        }
-    };
-    auto gate_row = [&](int k, float (&w)[8]) {
-        if constexpr (!GATE) {
-        } else if constexpr (!AHEAD) {
-            load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, col[k], w);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = w_g[k][e];
-        }
-    };
-
-    RowIn now, ahead;
-    if (AHEAD && row0 < row1) load_row(row0, now);
+    RowIn now;
     for (int64_t row = row0; row < row1; ++row) {
         // everything that follows from the columns (addresses, masks of a ragged
         // end) is formed anew in each row: held over the loop it takes the registers
         // that the row needs
 #pragma unroll
         for (int k = 0; k < NV; ++k) asm volatile("" : "+v"(col[k]));
-        if constexpr (AHEAD) load_row(row + 1 < row1 ? row + 1 : row, ahead);
-        else load_row(row, now);
+        load_row(row, now);
         const float mn = now.mn, rn = now.rn, mb = now.mb, rb = now.rb;
         auto& dn = now.dn;
         auto& dro = now.dro;
@@ -499,7 +466,7 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
                 float g[8], x[8], w[8];
                 widen8<DT>(dn[k], g);
                 sn[k].xhat(mn, rn, x);
-                pre_weight(k, w);
+                load_cols<WHOLE>(a.pre_w, col[k], C, 1.f, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     c0 = fmaf(g[e], w[e], c0);
@@ -526,7 +493,7 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
                 float g[8], x[8], w[8];
                 widen8<DT>(dn[k], g);
                 sn[k].xhat(mn, rn, x);
-                pre_weight(k, w);
+                load_cols<WHOLE>(a.pre_w, col[k], C, 1.f, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     D[k][e] = fmaf(rn, fmaf(g[e], w[e], -c0) - x[e] * c1, D[k][e]);
@@ -536,10 +503,10 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
             if constexpr (WIDE) load_post(row, k, now);
             float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, w[8];
             if (read_b) sb[k].xhat(mb, rb, x);
-            if (a.post != kNormNone) post_weight(k, w);
+            if (a.post != kNormNone) load_cols<WHOLE>(a.post_w, col[k], C, 1.f, w);
             if constexpr (GATE) {
                 float g[8];
-                gate_row(k, g);
+                load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, col[k], g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) D[k][e] *= a.alpha;
                 float p[8];
@@ -586,19 +553,9 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
                 }
                 in_group = 0;
                 ++grow;
-                if constexpr (AHEAD) {
-                    if (row + 1 < row1) {
-#pragma unroll
-                        for (int k = 0; k < NV; ++k)
-                            load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, col[k], w_g[k]);
-                    }
-                }
             }
         }
-        if (!has_b) {
-            if constexpr (AHEAD) now = ahead;
-            continue;
-        }
+        if (!has_b) continue;
         if (a.post != kNormNone) {
             sum(e1, e0);
             e1 *= inv_c;
@@ -616,7 +573,6 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
             }
             store8<DT, WHOLE>(row_ptr<DT>(a.db, row, a.lddb), col[k], C, D[k]);
         }
-        if constexpr (AHEAD) now = ahead;
     }
 
     // this workgroup's share of the sums: section s, workgroup, column
@@ -635,6 +591,256 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
             put(ss.at[kSumPostB], kPostB, k);
         }
         if constexpr (GATE) put(ss.at[kSumGate], kGateS, k);
+    }
+}
+
+// The same for rows of up to 4096 columns, one vector a thread: what all rows use stays
+// in registers, and each raw vector is replaced by the next row's as soon as it has been
+// used, so that a row's loads are in flight over the reductions of the one before.
+// FULL: layer norms, or biases; without it (RMS norms) the means of q and h and the
+// biases' sums are left out.  ALL: both norms, both gradients in and both out (what a
+// training step asks for), so that nothing in a row depends on a pointer being there.
+// VALU issue bounds this kernel as much as HBM: 16384 x 4096
+// bf16 from codes with a gate vector went from 149 us at 530 vector instructions a row and
+// thread to what the table below its launcher says.
+template <int DT, int NT, bool CODES, bool FULL, bool GATE, bool WHOLE, bool ALL>
+__global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d, SumSlots ss,
+                                                        float* part)
+{
+    constexpr int ES = DT == kF32 ? 4 : 2, M = FULL ? 2 : 1;
+    __shared__ float slots[kSlots][2][NT / kWave];
+    RowSum<NT> sum{slots};
+    const int C = int(a.C);
+    const float inv_c = 1.f / float(C);
+    const int64_t Cp = code_pitch(a.C);
+    const bool has_b = ALL || a.db != nullptr, post = ALL || a.post != kNormNone;
+    const bool pre = ALL || (a.pre != kNormNone && a.dn);
+    const bool read_b = ALL || (has_b && (post || (GATE && a.dgate)));
+    const uint32_t c = threadIdx.x * kRowV;
+    // WHOLE: threads past the row read its last vector again; their weights are zero,
+    // which keeps them out of the row's sums, and they write nothing
+    const bool in = c < uint32_t(C);
+    uint32_t at = WHOLE ? (in ? c : uint32_t(C) - kRowV) : c;
+
+    auto load = [&](const char* row) {
+        if constexpr (WHOLE) {
+            Raw8<DT> r;
+#pragma unroll
+            for (int h = 0; h < (DT == kF32 ? 2 : 1); ++h) r.q[h] = load16_any(row + at * ES + 16 * h);
+            return r;
+        } else {
+            return load8<DT, false>(row, c, C);
+        }
+    };
+    auto put_row = [&](const char* row, const float (&v)[8]) {
+        if constexpr (WHOLE) {
+            if (in) store8<DT, true>(row, at, C, v);
+        } else {
+            store8<DT, false>(row, c, C, v);
+        }
+    };
+    auto load_saved = [&](Saved<DT, CODES, WHOLE>& s, const char* x, const int8_t* codes,
+                          const uint8_t* exps) {
+        if constexpr (CODES) {
+            // (c, not `at`, of a ragged row; idle threads: the row's first codes)
+            const uint32_t k = WHOLE ? at : (in ? c : 0u);
+            s.q = *reinterpret_cast<const uint2*>(codes + k);
+            s.E = exps[k / kGroup];
+        } else {
+            s.raw = load(x);
+        }
+    };
+
+    const int64_t group0 = int64_t(blockIdx.x) / d.cpg * d.gpw;
+    const int64_t row0 = group0 * d.R + int64_t(blockIdx.x) % d.cpg * d.rc;
+    const int64_t row1 = d.cpg > 1 ? dmin(row0 + d.rc, (group0 + 1) * d.R)
+                                   : dmin(row0 + d.gpw * d.R, a.T);
+    int64_t grow = group0, in_group = 0;       // gate row, rows of it seen (cpg == 1)
+
+    // What all rows use: in LDS, each thread its own (registers would not leave 4 waves a
+    // SIMD): pre and post weight, alpha * gate, post bias.
+    float s_nw[8] = {}, s_bw[8] = {}, s_nb[8] = {}, s_bb[8] = {}, s_g[8] = {};
+    constexpr int NW = 2 + (GATE ? (FULL ? 2 : 1) : 0);
+    __shared__ float4 w_lds[NW][2][NT];
+    auto keep = [&](int i, const float (&v)[8]) {
+        w_lds[i][0][threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
+        w_lds[i][1][threadIdx.x] = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    auto kept = [&](int i, float (&v)[8]) {
+        const float4 f = w_lds[i][0][threadIdx.x], g = w_lds[i][1][threadIdx.x];
+        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        v[4] = g.x; v[5] = g.y; v[6] = g.z; v[7] = g.w;
+    };
+    {
+        float w[8];
+        load_cols<WHOLE>(a.pre_w, c, C, 1.f, w);
+        keep(0, w);
+        load_cols<WHOLE>(post ? a.post_w : nullptr, c, C, 1.f, w);
+        keep(1, w);
+        if constexpr (GATE && FULL) {
+            load_cols<WHOLE>(post ? a.post_b : nullptr, c, C, 0.f, w);
+            keep(NW - 1, w);
+        }
+    }
+    auto load_gates = [&] {
+        float w[8];
+        load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] *= a.alpha;
+        keep(2, w);
+    };
+    if constexpr (GATE) {
+        if (row0 < row1) load_gates();
+    }
+
+    Raw8<DT> dn{}, dro{};
+    Saved<DT, CODES, WHOLE> sn{}, sb{};
+    float mn = 0.f, rn = 0.f, mb = 0.f, rb = 1.f;
+    auto load_pre = [&](int64_t row) {
+        if (ALL || a.dr_out) dro = load(row_ptr<DT>(a.dr_out, row, a.lddro));
+        if (pre) {
+            dn = load(row_ptr<DT>(a.dn, row, a.lddn));
+            load_saved(sn, row_ptr<DT>(a.r_out, row, a.ldro), a.codes_n + row * Cp,
+                       a.exps_n + row * (Cp / kGroup));
+        }
+    };
+    auto load_post = [&](int64_t row) {
+        if (read_b)
+            load_saved(sb, row_ptr<DT>(a.b, row, a.ldb), a.codes_b + row * Cp,
+                       a.exps_b + row * (Cp / kGroup));
+    };
+    auto load_stats = [&](int64_t row) {
+        if (pre) {
+            if constexpr (!CODES) mn = a.pre_stats[2 * row];
+            rn = a.pre_stats[2 * row + 1];
+        }
+        if (has_b && post) {
+            if constexpr (!CODES) mb = a.post_stats[2 * row];
+            rb = a.post_stats[2 * row + 1];
+        }
+    };
+    if (row0 < row1) {
+        load_stats(row0);
+        load_pre(row0);
+        load_post(row0);
+    }
+    for (int64_t row = row0; row < row1; ++row) {
+        const int64_t next = row + 1 < row1 ? row + 1 : row;
+        // what follows from the column is formed anew in each row: held over the loop it
+        // takes registers that the row needs
+        if constexpr (WHOLE) asm volatile("" : "+v"(at));
+        // <q xn>, <q>, and the sums of the pre-norm's vectors
+        float x[8], q[8], D[8], m[M] = {};
+        widen8<DT>(dro, D);
+        const float rn_row = rn, mb_row = mb, rb_row = rb;
+        if (pre) {
+            float g[8], w_n[8];
+            kept(0, w_n);
+            widen8<DT>(dn, g);
+            sn.xhat(mn, rn, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s_nw[e] = fmaf(g[e], x[e], s_nw[e]);
+                q[e] = g[e] * w_n[e];
+                m[0] = fmaf(q[e], x[e], m[0]);
+                if constexpr (FULL) {
+                    s_nb[e] += g[e];
+                    m[1] += q[e];
+                }
+            }
+        }
+        load_pre(next);
+        load_stats(next);
+        if (pre) {
+            sum.add(m);
+            const float c1 = m[0] * inv_c;
+            const float c0 = FULL && a.pre == kNormLayer ? m[FULL ? 1 : 0] * inv_c : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if constexpr (FULL) q[e] -= c0;
+                D[e] = fmaf(rn_row, fmaf(-x[e], c1, q[e]), D[e]);
+            }
+        }
+        if (ALL || a.dr) put_row(row_ptr<DT>(a.dr, row, a.lddr), D);
+        if (!has_b) continue;
+
+        // h = alpha*g*D*w_post with its sums
+        if (read_b) {
+            sb.xhat(mb_row, post ? rb_row : 1.f, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        }
+        float w_b[8];
+        kept(1, w_b);
+        if constexpr (GATE) {
+            float o[8];
+            if constexpr (FULL) kept(NW - 1, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s_g[e] = fmaf(D[e], FULL ? fmaf(x[e], w_b[e], o[e]) : x[e] * w_b[e], s_g[e]);
+            kept(2, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) D[e] *= o[e];
+        }
+#pragma unroll
+        for (int k = 0; k < M; ++k) m[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (!GATE) D[e] *= a.alpha;
+            s_bw[e] = fmaf(D[e], x[e], s_bw[e]);
+            if constexpr (FULL) s_bb[e] += D[e];
+            D[e] *= w_b[e];
+            m[0] = fmaf(D[e], x[e], m[0]);
+            if constexpr (FULL) m[1] += D[e];
+        }
+        if constexpr (GATE) {
+            // a whole group's gate sum is done: write it and start the next
+            if (d.cpg == 1 && ++in_group == d.R) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s_g[e] *= a.alpha;
+                if (a.dgate && (!WHOLE || in)) {
+                    if (a.gate_f32)
+                        store8<kF32, WHOLE>(row_ptr<kF32>(a.dgate, grow, a.C), c, C, s_g);
+                    else store8<DT, WHOLE>(row_ptr<DT>(a.dgate, grow, a.C), c, C, s_g);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s_g[e] = 0.f;
+                in_group = 0;
+                ++grow;
+                if (row + 1 < row1) load_gates();
+            }
+        }
+        load_post(next);
+        if (post) {
+            sum.add(m);
+            const float e1 = m[0] * inv_c * rb_row;
+            const float e0 = FULL && a.post == kNormLayer ? m[FULL ? 1 : 0] * inv_c * rb_row : 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                D[e] = fmaf(D[e], rb_row, -x[e] * e1);
+                if constexpr (FULL) D[e] -= e0;
+            }
+        }
+        put_row(row_ptr<DT>(a.db, row, a.lddb), D);
+    }
+
+    // this workgroup's share of the sums: section, workgroup, column
+    auto put = [&](int section, const float (&v)[8]) {
+        if (section >= 0 && c < uint32_t(Cp))
+            store8<kF32, true>(row_ptr<kF32>(part, int64_t(section) * d.grid + blockIdx.x, Cp), c,
+                               int(Cp), v);
+    };
+    put(ss.at[kSumPreW], s_nw);
+    put(ss.at[kSumPostW], s_bw);
+    if constexpr (FULL) {
+        put(ss.at[kSumPreB], s_nb);
+        put(ss.at[kSumPostB], s_bb);
+    }
+    if constexpr (GATE) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_g[e] *= a.alpha;
+        put(ss.at[kSumGate], s_g);
     }
 }
 
@@ -748,51 +954,63 @@ void launch_resnorm_backward(const ResnormBwd& a, int dtype, int64_t cus, void* 
     const SumSlots ss = sum_slots(a, d.cpg);
     float* part = static_cast<float*>(ws);
     const bool codes = a.codes_n != nullptr || a.codes_b != nullptr;
-    const bool bias = a.dpre_b != nullptr || a.dpost_b != nullptr;
+    const bool full = a.pre == kNormLayer || a.post == kNormLayer || a.dpre_b || a.dpost_b ||
+                      a.post_b;
     const bool gate = a.gate != nullptr && a.db != nullptr;
+    const bool all = a.pre != kNormNone && a.post != kNormNone && a.dn && a.dr_out && a.dr && a.db;
     const BwdShape sh = bwd_shape(a.C);
     with_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         using std::integral_constant;
         using Y = std::true_type;
         using N = std::false_type;
-        auto run = [&](auto nt, auto nv, auto cd, auto bi, auto ga, auto whole) {
-            if (d.grid > 0)
-                hipLaunchKernelGGL(
-                    (k_resnorm_bwd<DT, decltype(nt)::value, decltype(nv)::value,
-                                   decltype(cd)::value, decltype(bi)::value,
-                                   decltype(ga)::value, decltype(whole)::value>),
-                    dim3(unsigned(d.grid)), dim3(decltype(nt)::value), 0, s, a, d, ss, part);
-        };
         auto on = [](bool v, auto&& f) {
             if (v) f(Y{});
             else f(N{});
         };
-        auto flags = [&](auto nt, auto nv) {
+        // f(codes, full, gate, whole); ragged rows take the kernel with every sum, whether
+        // wanted or not
+        auto flags = [&](auto&& f) {
             on(codes, [&](auto cd) {
-                // ragged rows take the kernel with every sum, whether wanted or not
                 if (a.C % kRowV != 0) {
-                    run(nt, nv, cd, Y{}, Y{}, N{});
+                    f(cd, Y{}, Y{}, N{});
                     return;
                 }
-                on(bias, [&](auto bi) {
-                    on(gate, [&](auto ga) { run(nt, nv, cd, bi, ga, Y{}); });
-                });
+                on(full, [&](auto fu) { on(gate, [&](auto ga) { f(cd, fu, ga, Y{}); }); });
             });
         };
-        using I64 = integral_constant<int, 64>;
-        using I128 = integral_constant<int, 128>;
-        using I256 = integral_constant<int, 256>;
-        using I512 = integral_constant<int, 512>;
-        using I1 = integral_constant<int, 1>;
-        using I2 = integral_constant<int, 2>;
-        using I4 = integral_constant<int, 4>;
-        if (sh.nt == 64) flags(I64{}, I1{});
-        else if (sh.nt == 128) flags(I128{}, I1{});
-        else if (sh.nt == 256) flags(I256{}, I1{});
-        else if (sh.nv == 1) flags(I512{}, I1{});
-        else if (sh.nv == 2) flags(I512{}, I2{});
-        else flags(I512{}, I4{});
+        const dim3 grid(unsigned(d.grid));
+        auto row_kernel = [&](auto nt) {
+            flags([&](auto cd, auto fu, auto ga, auto whole) {
+                constexpr int NT = decltype(nt)::value;
+                auto go = [&](auto all_) {
+                    hipLaunchKernelGGL(
+                        (k_resnorm_bwd_row<DT, NT, decltype(cd)::value, decltype(fu)::value,
+                                           decltype(ga)::value, decltype(whole)::value,
+                                           decltype(all_)::value>),
+                        grid, dim3(NT), 0, s, a, d, ss, part);
+                };
+                if constexpr (decltype(whole)::value) on(all, go);
+                else go(N{});
+            });
+        };
+        auto wide_kernel = [&](auto nv) {
+            flags([&](auto cd, auto fu, auto ga, auto whole) {
+                hipLaunchKernelGGL(
+                    (k_resnorm_bwd<DT, 512, decltype(nv)::value, decltype(cd)::value,
+                                   decltype(fu)::value, decltype(ga)::value,
+                                   decltype(whole)::value>),
+                    grid, dim3(512), 0, s, a, d, ss, part);
+            });
+        };
+        if (d.grid > 0) {
+            if (sh.nv == 4) wide_kernel(integral_constant<int, 4>{});
+            else if (sh.nv == 2) wide_kernel(integral_constant<int, 2>{});
+            else if (sh.nt == 64) row_kernel(integral_constant<int, 64>{});
+            else if (sh.nt == 128) row_kernel(integral_constant<int, 128>{});
+            else if (sh.nt == 256) row_kernel(integral_constant<int, 256>{});
+            else row_kernel(integral_constant<int, 512>{});
+        }
         const int vectors = ss.count - (ss.at[kSumGate] >= 0 ? 1 : 0);
         const int64_t gates = ss.at[kSumGate] >= 0 ? a.T / a.R : 0;
         if (vectors + gates > 0)
