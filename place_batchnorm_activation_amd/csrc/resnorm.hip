@@ -128,6 +128,78 @@ __device__ __forceinline__ void normalise(float (&x)[NV][8], const int (&col)[NV
         for (int e = 0; e < 8; ++e) x[k][e] *= rstd;
 }
 
+// A thread's eight columns of a row of C >= 8 columns: those at `at`, which for the last
+// vector of a ragged row begin `skip` columns early, so that every access of the row is
+// one wide one inside it.  The skipped columns belong to the thread before: they are kept
+// out of sums (their weights read as zero) and are not written.  Threads past the row
+// (in == false) read its last columns, with zero weights.
+struct Span {
+    uint32_t c, at, skip;
+    bool in;
+    __device__ __forceinline__ Span(uint32_t thread, int C)
+        : c(thread * kRowV), in(c < uint32_t(C))
+    {
+        const uint32_t last = uint32_t(C) - kRowV;
+        at = c < last ? c : last;
+        skip = in ? c - at : 0u;
+    }
+    __device__ __forceinline__ bool own(int e) const { return in && uint32_t(e) >= skip; }
+    template <int DT>
+    __device__ __forceinline__ Raw8<DT> load(const char* row) const
+    {
+        Raw8<DT> r;
+#pragma unroll
+        for (int h = 0; h < (DT == kF32 ? 2 : 1); ++h)
+            r.q[h] = load16_any(row + at * (DT == kF32 ? 4 : 2) + 16 * h);
+        return r;
+    }
+    template <int DT>
+    __device__ __forceinline__ void store(const char* row, const float (&v)[8]) const
+    {
+        if (!in) return;
+        if (skip == 0) {
+            store8<DT, true>(row, at, int(at) + kRowV, v);
+        } else {
+#pragma unroll
+            for (int e = 1; e < 8; ++e)
+                if (uint32_t(e) >= skip) {
+                    char* p = const_cast<char*>(row) + (at + e) * (DT == kF32 ? 4 : 2);
+                    if constexpr (DT == kF32) *reinterpret_cast<float*>(p) = v[e];
+                    else *reinterpret_cast<uint16_t*>(p) = pack1<DT>(v[e]);
+                }
+        }
+    }
+    // of a per-column vector (null: `none`), zero where not owned
+    __device__ __forceinline__ void cols(const float* p, float none, float (&v)[8]) const
+    {
+        if (p) {
+            widen8<kF32>(load<kF32>(reinterpret_cast<const char*>(p)), v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = none;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = own(e) ? v[e] : 0.f;
+    }
+    // of a gate row (1 without a gate)
+    template <int DT>
+    __device__ __forceinline__ void gate(const void* g, bool f32, int64_t grow, int64_t C,
+                                         float (&v)[8]) const
+    {
+        if (!g) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 1.f;
+        } else if (f32) widen8<kF32>(load<kF32>(row_ptr<kF32>(g, grow, C)), v);
+        else widen8<DT>(load<DT>(row_ptr<DT>(g, grow, C)), v);
+    }
+    // codes lie by whole vectors, at c
+    __device__ __forceinline__ uint2 load_codes(const int8_t* row) const
+    {
+        const uint64_t q = *reinterpret_cast<const uint64_t*>(row + (in ? c : 0u)) << (8 * skip);
+        return make_uint2(uint32_t(q), uint32_t(q >> 32));
+    }
+};
+
 // Eight gate values of gate row `grow` (1 without a gate).
 template <int DT, bool WHOLE>
 __device__ __forceinline__ void load_gate(const void* gate, bool f32, int64_t grow, int64_t C,
@@ -236,6 +308,117 @@ __global__ __launch_bounds__((TPR > kThreads ? TPR : kThreads)) void k_resnorm_f
             for (int e = 0; e < 8; ++e) x[k][e] = fmaf(x[k][e], w[e], o[e]);
             store8<DT, WHOLE>(row_ptr<DT>(a.n, row, a.ldn), col[k], C, x[k]);
         }
+    }
+}
+
+// The same for rows of 8 to 4096 columns, one vector a thread: the vectors that all rows
+// use stay in registers (a gate for some of the rows is read with them), and r and b of the
+// next row are in flight over this one's reductions.  Rows go to workgroups in turn, 16 waves a
+// CU (32 measure the same).  16384 x 4096 bf16: 104 us, 5.2 TB/s; with both codes 146 us; one
+// row of 4096: 3.8 us.
+template <int DT, int TPR>
+__global__ __launch_bounds__(TPR == kWave ? kThreads : TPR) void k_resnorm_fwd_row(ResnormFwd a,
+                                                                                  FastDiv dr)
+{
+    constexpr int NT = TPR == kWave ? kThreads : TPR, RPW = NT / TPR;
+    __shared__ float slots[kSlots][2][TPR / kWave];
+    RowSum<TPR> sum{slots};
+    const int C = int(a.C);
+    const float inv_c = 1.f / float(C);
+    const int64_t Cp = code_pitch(a.C);
+    const bool ragged = C % kRowV != 0, post = a.post != kNormNone, pre = a.pre != kNormNone;
+    Span span(threadIdx.x % TPR, C);
+    // uniform over a wave (and a barrier's workgroup)
+    const int sub = RPW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
+    const int64_t step = int64_t(gridDim.x) * RPW;
+    int64_t row = int64_t(blockIdx.x) * RPW + sub;
+    if (row >= a.T) return;                 // RPW == 1: whole workgroups; else single waves
+
+    float w_b[8], o_b[8], w_n[8], o_n[8];
+    if (post) {
+        span.cols(a.post_w, 1.f, w_b);
+        span.cols(a.post_b, 0.f, o_b);
+    }
+    if (pre) {
+        span.cols(a.pre_w, 1.f, w_n);
+        span.cols(a.pre_b, 0.f, o_n);
+    }
+    Raw8<DT> rr, rb{};
+    auto load = [&](int64_t i) {
+        rr = span.load<DT>(row_ptr<DT>(a.r, i, a.ldr));
+        if (a.b) rb = span.load<DT>(row_ptr<DT>(a.b, i, a.ldb));
+    };
+    // zero where this thread does not own the column
+    auto mask = [&](float (&v)[8]) {
+        if (ragged || !span.in) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = span.own(e) ? v[e] : 0.f;
+        }
+    };
+    auto normed = [&](float (&x)[8], bool layer, float* stats) {
+        float mean = 0.f;
+        mask(x);
+        if (layer) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mean += x[e];
+            sum(mean);
+            mean *= inv_c;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] -= mean;
+            mask(x);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], s);
+        sum(s);
+        const float rstd = 1.f / sqrtf(fmaf(s, inv_c, a.eps));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= rstd;
+        if (stats && threadIdx.x % TPR == 0) {
+            stats[2 * row] = mean;
+            stats[2 * row + 1] = rstd;
+        }
+    };
+    // codes of eight values that are zero where not owned; they lie by whole vectors
+    auto put_codes = [&](int8_t* codes, uint8_t* exps, const float (&x)[8]) {
+        uint32_t E;
+        const uint2 q = encode8(x, E);
+        const uint64_t v = ((uint64_t(q.y) << 32) | q.x) >> (8 * span.skip);
+        store_codes(codes + row * Cp, exps + row * (Cp / kGroup), uint32_t(Cp), span.c,
+                    make_uint2(uint32_t(v), uint32_t(v >> 32)), E);
+    };
+    load(row);
+    for (; row < a.T; row += step) {
+        float x[8], v[8];
+        widen8<DT>(rr, v);
+        if (a.b) widen8<DT>(rb, x);
+        load(row + step < a.T ? row + step : row);
+        if (a.b) {
+            if (post) normed(x, a.post == kNormLayer, a.post_stats);
+            if (a.codes_b) {
+                if (!post) mask(x);
+                put_codes(a.codes_b, a.exps_b, x);
+            }
+            if (post) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], w_b[e], o_b[e]);
+            }
+            if (a.gate) {
+                float g[8];
+                span.gate<DT>(a.gate, a.gate_f32, fast_div(uint32_t(row), dr), a.C, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= g[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(a.alpha, x[e], v[e]);
+        }
+        if (a.r_out) span.store<DT>(row_ptr<DT>(a.r_out, row, a.ldro), v);
+        if (!pre) continue;
+        normed(v, a.pre == kNormLayer, a.pre_stats);
+        if (a.codes_n) put_codes(a.codes_n, a.exps_n, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], w_n[e], o_n[e]);
+        span.store<DT>(row_ptr<DT>(a.n, row, a.ldn), v);
     }
 }
 
@@ -600,14 +783,15 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd(ResnormBwd a, RowDeal d, Sum
 // FULL: layer norms, or biases; without it (RMS norms) the means of q and h and the
 // biases' sums are left out.  ALL: both norms, both gradients in and both out (what a
 // training step asks for), so that nothing in a row depends on a pointer being there.
-// VALU issue bounds this kernel as much as HBM: 16384 x 4096
-// bf16 from codes with a gate vector went from 149 us at 530 vector instructions a row and
-// thread to what the table below its launcher says.
-template <int DT, int NT, bool CODES, bool FULL, bool GATE, bool WHOLE, bool ALL>
+// At 16384 x 4096 bf16 from codes with a gate vector: 142 us, 4.8 TB/s of the 675 MB it
+// cannot do without (a large copy runs at 4.9).  Vector instructions bounded earlier forms
+// of it as much as HBM (205 us at twice their number); 128 registers or fewer, two
+// workgroups of 512 a CU, are worth 40 us.
+template <int DT, int NT, bool CODES, bool FULL, bool GATE, bool ALL>
 __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d, SumSlots ss,
                                                         float* part)
 {
-    constexpr int ES = DT == kF32 ? 4 : 2, M = FULL ? 2 : 1;
+    constexpr int M = FULL ? 2 : 1;
     __shared__ float slots[kSlots][2][NT / kWave];
     RowSum<NT> sum{slots};
     const int C = int(a.C);
@@ -616,38 +800,14 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
     const bool has_b = ALL || a.db != nullptr, post = ALL || a.post != kNormNone;
     const bool pre = ALL || (a.pre != kNormNone && a.dn);
     const bool read_b = ALL || (has_b && (post || (GATE && a.dgate)));
-    const uint32_t c = threadIdx.x * kRowV;
-    // WHOLE: threads past the row read its last vector again; their weights are zero,
-    // which keeps them out of the row's sums, and they write nothing
-    const bool in = c < uint32_t(C);
-    uint32_t at = WHOLE ? (in ? c : uint32_t(C) - kRowV) : c;
-
-    auto load = [&](const char* row) {
-        if constexpr (WHOLE) {
-            Raw8<DT> r;
-#pragma unroll
-            for (int h = 0; h < (DT == kF32 ? 2 : 1); ++h) r.q[h] = load16_any(row + at * ES + 16 * h);
-            return r;
-        } else {
-            return load8<DT, false>(row, c, C);
-        }
-    };
-    auto put_row = [&](const char* row, const float (&v)[8]) {
-        if constexpr (WHOLE) {
-            if (in) store8<DT, true>(row, at, C, v);
-        } else {
-            store8<DT, false>(row, c, C, v);
-        }
-    };
-    auto load_saved = [&](Saved<DT, CODES, WHOLE>& s, const char* x, const int8_t* codes,
+    Span span(threadIdx.x, C);
+    auto load_saved = [&](Saved<DT, CODES, true>& s, const char* x, const int8_t* codes,
                           const uint8_t* exps) {
         if constexpr (CODES) {
-            // (c, not `at`, of a ragged row; idle threads: the row's first codes)
-            const uint32_t k = WHOLE ? at : (in ? c : 0u);
-            s.q = *reinterpret_cast<const uint2*>(codes + k);
-            s.E = exps[k / kGroup];
+            s.q = span.load_codes(codes);
+            s.E = exps[(span.in ? span.c : 0u) / kGroup];
         } else {
-            s.raw = load(x);
+            s.raw = span.load<DT>(x);
         }
     };
 
@@ -673,18 +833,18 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
     };
     {
         float w[8];
-        load_cols<WHOLE>(a.pre_w, c, C, 1.f, w);
+        span.cols(a.pre_w, 1.f, w);
         keep(0, w);
-        load_cols<WHOLE>(post ? a.post_w : nullptr, c, C, 1.f, w);
+        span.cols(post ? a.post_w : nullptr, 1.f, w);
         keep(1, w);
         if constexpr (GATE && FULL) {
-            load_cols<WHOLE>(post ? a.post_b : nullptr, c, C, 0.f, w);
+            span.cols(post ? a.post_b : nullptr, 0.f, w);
             keep(NW - 1, w);
         }
     }
     auto load_gates = [&] {
         float w[8];
-        load_gate<DT, WHOLE>(a.gate, a.gate_f32, grow, a.C, c, w);
+        span.gate<DT>(a.gate, a.gate_f32, grow, a.C, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] *= a.alpha;
         keep(2, w);
@@ -694,12 +854,12 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
     }
 
     Raw8<DT> dn{}, dro{};
-    Saved<DT, CODES, WHOLE> sn{}, sb{};
+    Saved<DT, CODES, true> sn{}, sb{};
     float mn = 0.f, rn = 0.f, mb = 0.f, rb = 1.f;
     auto load_pre = [&](int64_t row) {
-        if (ALL || a.dr_out) dro = load(row_ptr<DT>(a.dr_out, row, a.lddro));
+        if (ALL || a.dr_out) dro = span.load<DT>(row_ptr<DT>(a.dr_out, row, a.lddro));
         if (pre) {
-            dn = load(row_ptr<DT>(a.dn, row, a.lddn));
+            dn = span.load<DT>(row_ptr<DT>(a.dn, row, a.lddn));
             load_saved(sn, row_ptr<DT>(a.r_out, row, a.ldro), a.codes_n + row * Cp,
                        a.exps_n + row * (Cp / kGroup));
         }
@@ -728,7 +888,7 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
         const int64_t next = row + 1 < row1 ? row + 1 : row;
         // what follows from the column is formed anew in each row: held over the loop it
         // takes registers that the row needs
-        if constexpr (WHOLE) asm volatile("" : "+v"(at));
+        asm volatile("" : "+v"(span.at), "+v"(span.c));
         // <q xn>, <q>, and the sums of the pre-norm's vectors
         float x[8], q[8], D[8], m[M] = {};
         widen8<DT>(dro, D);
@@ -761,7 +921,7 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
                 D[e] = fmaf(rn_row, fmaf(-x[e], c1, q[e]), D[e]);
             }
         }
-        if (ALL || a.dr) put_row(row_ptr<DT>(a.dr, row, a.lddr), D);
+        if (ALL || a.dr) span.store<DT>(row_ptr<DT>(a.dr, row, a.lddr), D);
         if (!has_b) continue;
 
         // h = alpha*g*D*w_post with its sums
@@ -799,10 +959,9 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
             if (d.cpg == 1 && ++in_group == d.R) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s_g[e] *= a.alpha;
-                if (a.dgate && (!WHOLE || in)) {
-                    if (a.gate_f32)
-                        store8<kF32, WHOLE>(row_ptr<kF32>(a.dgate, grow, a.C), c, C, s_g);
-                    else store8<DT, WHOLE>(row_ptr<DT>(a.dgate, grow, a.C), c, C, s_g);
+                if (a.dgate) {
+                    if (a.gate_f32) span.store<kF32>(row_ptr<kF32>(a.dgate, grow, a.C), s_g);
+                    else span.store<DT>(row_ptr<DT>(a.dgate, grow, a.C), s_g);
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s_g[e] = 0.f;
@@ -822,14 +981,13 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
                 if constexpr (FULL) D[e] -= e0;
             }
         }
-        put_row(row_ptr<DT>(a.db, row, a.lddb), D);
+        span.store<DT>(row_ptr<DT>(a.db, row, a.lddb), D);
     }
 
     // this workgroup's share of the sums: section, workgroup, column
     auto put = [&](int section, const float (&v)[8]) {
-        if (section >= 0 && c < uint32_t(Cp))
-            store8<kF32, true>(row_ptr<kF32>(part, int64_t(section) * d.grid + blockIdx.x, Cp), c,
-                               int(Cp), v);
+        if (section >= 0)
+            span.store<kF32>(row_ptr<kF32>(part, int64_t(section) * d.grid + blockIdx.x, Cp), v);
     };
     put(ss.at[kSumPreW], s_nw);
     put(ss.at[kSumPostW], s_bw);
@@ -897,6 +1055,7 @@ struct BwdShape {
 BwdShape bwd_shape(int64_t C)
 {
     const int64_t v = code_pitch(C) / kRowV;
+    if (C < kRowV) return {512, 2};            // no vector fits: element by element
     if (v <= 64) return {64, 1};
     if (v <= 128) return {128, 1};
     if (v <= 256) return {256, 1};
@@ -925,24 +1084,30 @@ void launch_resnorm_forward(const ResnormFwd& a, int dtype, int64_t cus, hipStre
     const int64_t v = code_pitch(a.C) / kRowV;
     const FastDiv dr = make_fast_div(uint32_t(a.R));
     with_dtype(dtype, [&](auto dt) {
-        auto go = [&](auto tpr, auto nv) {
-            constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-            constexpr int NT = TPR > kThreads ? TPR : kThreads;
-            const int64_t wgs = ceil_div(a.T, NT / TPR);
-            const dim3 grid(unsigned(min64(wgs, cus * (2048 / NT))));
+        auto row = [&](auto tpr) {
+            constexpr int TPR = decltype(tpr)::value;
+            constexpr int NT = TPR == kWave ? kThreads : TPR;
+            const dim3 grid(unsigned(min64(ceil_div(a.T, NT / TPR), cus * (1024 / NT))));
+            hipLaunchKernelGGL((k_resnorm_fwd_row<decltype(dt)::value, TPR>), grid, dim3(NT), 0, s,
+                               a, dr);
+        };
+        auto wide = [&](auto tpr) {
+            constexpr int TPR = decltype(tpr)::value;
+            const dim3 grid(unsigned(min64(a.T, cus * (2048 / TPR))));
             with_whole(a.C, [&](auto whole) {
-                hipLaunchKernelGGL((k_resnorm_fwd<decltype(dt)::value, TPR, NV,
+                hipLaunchKernelGGL((k_resnorm_fwd<decltype(dt)::value, TPR, 2,
                                                   decltype(whole)::value>),
-                                   grid, dim3(NT), 0, s, a, dr);
+                                   grid, dim3(TPR), 0, s, a, dr);
             });
         };
         using std::integral_constant;
-        if (v <= 64) go(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-        else if (v <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-        else if (v <= 256) go(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-        else if (v <= 512) go(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-        else if (v <= 1024) go(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-        else go(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+        if (a.C < kRowV) wide(integral_constant<int, 512>{});      // element by element
+        else if (v <= 64) row(integral_constant<int, 64>{});
+        else if (v <= 128) row(integral_constant<int, 128>{});
+        else if (v <= 256) row(integral_constant<int, 256>{});
+        else if (v <= 512) row(integral_constant<int, 512>{});
+        else if (v <= 1024) wide(integral_constant<int, 512>{});
+        else wide(integral_constant<int, 1024>{});
     });
 }
 
@@ -968,39 +1133,34 @@ void launch_resnorm_backward(const ResnormBwd& a, int dtype, int64_t cus, void* 
             if (v) f(Y{});
             else f(N{});
         };
-        // f(codes, full, gate, whole); ragged rows take the kernel with every sum, whether
-        // wanted or not
-        auto flags = [&](auto&& f) {
-            on(codes, [&](auto cd) {
-                if (a.C % kRowV != 0) {
-                    f(cd, Y{}, Y{}, N{});
-                    return;
-                }
-                on(full, [&](auto fu) { on(gate, [&](auto ga) { f(cd, fu, ga, Y{}); }); });
-            });
-        };
         const dim3 grid(unsigned(d.grid));
         auto row_kernel = [&](auto nt) {
-            flags([&](auto cd, auto fu, auto ga, auto whole) {
-                constexpr int NT = decltype(nt)::value;
-                auto go = [&](auto all_) {
+            constexpr int NT = decltype(nt)::value;
+            on(codes, [&](auto cd) { on(full, [&](auto fu) { on(gate, [&](auto ga) {
+                on(all, [&](auto all_) {
                     hipLaunchKernelGGL(
                         (k_resnorm_bwd_row<DT, NT, decltype(cd)::value, decltype(fu)::value,
-                                           decltype(ga)::value, decltype(whole)::value,
-                                           decltype(all_)::value>),
+                                           decltype(ga)::value, decltype(all_)::value>),
                         grid, dim3(NT), 0, s, a, d, ss, part);
-                };
-                if constexpr (decltype(whole)::value) on(all, go);
-                else go(N{});
-            });
+                });
+            }); }); });
         };
+        // f(codes, full, gate, whole); ragged rows take the kernel with every sum, whether
+        // wanted or not
         auto wide_kernel = [&](auto nv) {
-            flags([&](auto cd, auto fu, auto ga, auto whole) {
+            auto go = [&](auto cd, auto fu, auto ga, auto whole) {
                 hipLaunchKernelGGL(
                     (k_resnorm_bwd<DT, 512, decltype(nv)::value, decltype(cd)::value,
                                    decltype(fu)::value, decltype(ga)::value,
                                    decltype(whole)::value>),
                     grid, dim3(512), 0, s, a, d, ss, part);
+            };
+            on(codes, [&](auto cd) {
+                if (a.C % kRowV != 0) {
+                    go(cd, Y{}, Y{}, N{});
+                    return;
+                }
+                on(full, [&](auto fu) { on(gate, [&](auto ga) { go(cd, fu, ga, Y{}); }); });
             });
         };
         if (d.grid > 0) {
