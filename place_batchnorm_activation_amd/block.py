@@ -12,7 +12,8 @@ import ctypes
 
 import torch
 
-from . import (_check, _dtype_arg, _dtype_code, _F, _I64, _INT, _P, _SZ, _stream, lib)
+from . import (_check, _dtype_arg, _dtype_code, _F, _I64, _INT, _P, _SZ, lib)
+from . import _stream as _any_stream
 
 GROUP = 32
 GLU_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
@@ -42,20 +43,23 @@ for _fn in ("iabn_codes_pack", "iabn_codes_unpack", "iabn_glu_forward", "iabn_gl
 
 def _rows(t, name):
     """(address, ld, rows, cols) of a tensor [..., cols]."""
-    if t.dim() == 2:
-        T, C = t.shape
-        if C > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) == 2:
+        T, C = shape
+        ld, cs = t.stride()
+        if cs != 1 and C > 1:
             raise ValueError("%s: the last dimension must be contiguous" % name)
-        ld = t.stride(0) if T > 1 else C
-        if ld < C:
+        if T <= 1:
+            ld = C
+        elif ld < C:
             raise ValueError("%s: rows overlap (stride %d, %d columns)" % (name, ld, C))
         return t.data_ptr(), ld, T, C
-    if t.dim() == 1:
+    if len(shape) == 1:
         return _rows(t[None], name)
-    if t.dim() == 0:
+    if len(shape) == 0:
         raise ValueError("%s: a tensor [..., cols] is needed" % name)
     try:
-        return _rows(t.view(-1, t.shape[-1]), name)
+        return _rows(t.view(-1, shape[-1]), name)
     except RuntimeError:
         raise ValueError("%s: its leading dimensions do not collapse to rows at one distance"
                          % name) from None
@@ -68,19 +72,20 @@ def _like(t, name, T, C, ref):
     p, ld, t_rows, t_cols = _rows(t, name)
     if t_rows != T or t_cols != C:
         raise ValueError("%s is %d x %d, expected %d x %d" % (name, t_rows, t_cols, T, C))
-    if t.dtype != ref.dtype or t.device != ref.device:
+    if t.dtype != ref.dtype or t.get_device() != ref.get_device():
         raise TypeError("%s is %s on %s, expected %s on %s" % (name, t.dtype, t.device, ref.dtype,
                                                               ref.device))
     return p, ld
 
 
 def _flat(t, name, numel, dtype, device):
-    """Address of an optional contiguous tensor of numel elements."""
+    """Address of an optional contiguous tensor of numel elements on GPU `device` (-1:
+    the host)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device:
-        raise TypeError("%s is %s on %s, expected %s on %s" % (name, t.dtype, t.device, dtype,
-                                                              device))
+    if t.dtype != dtype or t.get_device() != device:
+        raise TypeError("%s is %s on %s, expected %s on GPU %d" % (name, t.dtype, t.device, dtype,
+                                                                  device))
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError("%s: %d contiguous elements are needed, got %s" % (name, numel,
                                                                           tuple(t.shape)))
@@ -121,10 +126,30 @@ def _name(v, table, what):
     return int(v)
 
 
-def _on_gpu(t):
-    """The library reads addresses on the GPU: a host tensor's would fault there."""
-    if t.device.type != "cuda":
+# the current stream as an integer, without torch's wrapper object (3 us a call) where this
+# torch has the accessor that its own compiler uses
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, t):
+    """The stream to launch on: the given one, or the current one of t's GPU.  The library
+    reads addresses on the GPU, where a host tensor's would fault."""
+    device = t.get_device()
+    if device < 0:
         raise TypeError("the library's tensors live on the GPU, got %s" % t.device)
+    if stream is None:
+        return _raw_stream(device) if _raw_stream else \
+            torch.cuda.current_stream(device).cuda_stream
+    return _any_stream(stream)
+
+
+def _space(workspace, ref):
+    """(address, bytes) of an optional workspace on ref's GPU."""
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != ref.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on %s is needed" % ref.device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # ---------------------------------------------------------------------------
@@ -132,20 +157,20 @@ def _on_gpu(t):
 
 def iabn_codes_pack(x, codes, exps, stream=None):
     p, ld, T, C = _rows(x, "x")
-    cp, ep = _codes(codes, exps, "x", T, C, x.device)
-    _on_gpu(x)
+    cp, ep = _codes(codes, exps, "x", T, C, x.get_device())
+    s = _stream(stream, x)
     _check("iabn_codes_pack", lib.iabn_codes_pack(p, ld, T, C, _dtype_code(x), cp, ep,
-                                                  _stream(stream)))
+                                                  s))
 
 
 def iabn_codes_unpack(codes, exps, y, scale=None, shift=None, stream=None):
     """y = scale * value + shift (fp32 vectors of y's columns, or None)."""
     p, ld, T, C = _rows(y, "y")
-    cp, ep = _codes(codes, exps, "y", T, C, y.device)
-    _on_gpu(y)
+    cp, ep = _codes(codes, exps, "y", T, C, y.get_device())
+    s = _stream(stream, y)
     _check("iabn_codes_unpack", lib.iabn_codes_unpack(
-        cp, ep, T, C, _cols(scale, "scale", C, y.device), _cols(shift, "shift", C, y.device), p,
-        ld, _dtype_code(y), _stream(stream)))
+        cp, ep, T, C, _cols(scale, "scale", C, y.get_device()), _cols(shift, "shift", C, y.get_device()), p,
+        ld, _dtype_code(y), s))
 
 
 # ---------------------------------------------------------------------------
@@ -157,12 +182,12 @@ def iabn_glu_forward(gate, up, out, act, codes_gate=None, exps_gate=None, codes_
     gp, ldg, T, F = _rows(gate, "gate")
     up_p, ldu = _like(up, "up", T, F, gate)
     op, ldo = _like(out, "out", T, F, gate)
-    cg, eg = _codes(codes_gate, exps_gate, "gate", T, F, gate.device)
-    cu, eu = _codes(codes_up, exps_up, "up", T, F, gate.device)
-    _on_gpu(gate)
+    cg, eg = _codes(codes_gate, exps_gate, "gate", T, F, gate.get_device())
+    cu, eu = _codes(codes_up, exps_up, "up", T, F, gate.get_device())
+    s = _stream(stream, gate)
     _check("iabn_glu_forward", lib.iabn_glu_forward(
         gp, ldg, up_p, ldu, op, ldo, T, F, _dtype_code(gate), _name(act, GLU_ACTS, "act"), cg,
-        eg, cu, eu, _stream(stream)))
+        eg, cu, eu, s))
 
 
 def iabn_glu_backward(codes_gate, exps_gate, codes_up, exps_up, dout, dgate, dup, act, out=None,
@@ -173,12 +198,12 @@ def iabn_glu_backward(codes_gate, exps_gate, codes_up, exps_up, dout, dgate, dup
     gp, ldg = _like(dgate, "dgate", T, F, dout)
     up_p, ldu = _like(dup, "dup", T, F, dout)
     op, ldo = _like(out, "out", T, F, dout)
-    cg, eg = _codes(codes_gate, exps_gate, "gate", T, F, dout.device)
-    cu, eu = _codes(codes_up, exps_up, "up", T, F, dout.device)
-    _on_gpu(dout)
+    cg, eg = _codes(codes_gate, exps_gate, "gate", T, F, dout.get_device())
+    cu, eu = _codes(codes_up, exps_up, "up", T, F, dout.get_device())
+    s = _stream(stream, dout)
     _check("iabn_glu_backward", lib.iabn_glu_backward(
         cg, eg, cu, eu, dp, ldd, gp, ldg, up_p, ldu, op, ldo, T, F, _dtype_code(dout),
-        _name(act, GLU_ACTS, "act"), _stream(stream)))
+        _name(act, GLU_ACTS, "act"), s))
 
 
 # ---------------------------------------------------------------------------
@@ -201,16 +226,15 @@ def iabn_linear_wgrad(dy, codes, exps, dw, workspace=None, scale=None, shift=Non
     dp, ldd, T, N = _rows(dy, "dy")
     wp, ldw, n, K = _rows(dw, "dw")
     if n != N or dw.device != dy.device:
-        raise ValueError("dw has %d rows on %s, expected %d on %s" % (n, dw.device, N, dy.device))
-    cp, ep = _codes(codes, exps, "x", T, K, dy.device)
-    ws, wb = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                  workspace.numel() * workspace.element_size())
-    _on_gpu(dy)
+        raise ValueError("dw has %d rows on %s, expected %d on %s" % (n, dw.device, N, dy.get_device()))
+    cp, ep = _codes(codes, exps, "x", T, K, dy.get_device())
+    ws, wb = _space(workspace, dy)
+    s = _stream(stream, dy)
     _check("iabn_linear_wgrad", lib.iabn_linear_wgrad(
-        dp, ldd, _dtype_code(dy), cp, ep, _cols(scale, "scale", K, dy.device),
-        _cols(shift, "shift", K, dy.device), wp, ldw, _dtype_code(dw),
-        _cols(dbias, "dbias", N, dy.device), int(bool(accumulate)), T, N, K, ws, wb,
-        _stream(stream)))
+        dp, ldd, _dtype_code(dy), cp, ep, _cols(scale, "scale", K, dy.get_device()),
+        _cols(shift, "shift", K, dy.get_device()), wp, ldw, _dtype_code(dw),
+        _cols(dbias, "dbias", N, dy.get_device()), int(bool(accumulate)), T, N, K, ws, wb,
+        s))
 
 
 # ---------------------------------------------------------------------------
@@ -242,7 +266,7 @@ class ResNormSpec:
     def _c(self, T, C, ref, gate):
         if C != self.cols:
             raise ValueError("the layer has %d columns, the tensors %d" % (self.cols, C))
-        dev = ref.device
+        dev = ref.get_device()
         gp, gd, per = None, 0, 1
         if gate is not None:
             groups = gate.shape[0] if gate.dim() == 2 else 1
@@ -271,15 +295,15 @@ def iabn_resnorm_forward(layer, r, b, r_out, n, gate=None, post_stats=None, pre_
     bp, ldb = _like(b, "b", T, C, r)
     op, ldo = _like(r_out, "r_out", T, C, r)
     np_, ldn = _like(n, "n", T, C, r)
-    dev = r.device
+    dev = r.get_device()
     cb, eb = _codes(codes_b, exps_b, "b", T, C, dev)
     cn, en = _codes(codes_n, exps_n, "n", T, C, dev)
     c = layer._c(T, C, r, gate)
-    _on_gpu(r)
+    s = _stream(stream, r)
     _check("iabn_resnorm_forward", lib.iabn_resnorm_forward(
         ctypes.byref(c), rp, ldr, bp, ldb, op, ldo, np_, ldn,
         _stats(post_stats, "post_stats", T, dev), _stats(pre_stats, "pre_stats", T, dev), cb, eb,
-        cn, en, _stream(stream)))
+        cn, en, s))
 
 
 def iabn_resnorm_workspace_size(rows, cols, rows_per_gate=1) -> int:
@@ -303,7 +327,7 @@ def iabn_resnorm_backward(layer, dr_out, dn, workspace, r_out=None, b=None, code
     if ref is None:
         raise ValueError("dr_out or dn is needed")
     _, _, T, C = _rows(ref, "dn" if dn is not None else "dr_out")
-    dev = ref.device
+    dev = ref.get_device()
     dop, lddo = _like(dr_out, "dr_out", T, C, ref)
     dnp, lddn = _like(dn, "dn", T, C, ref)
     rp, ldr = _like(r_out, "r_out", T, C, ref)
@@ -318,12 +342,11 @@ def iabn_resnorm_backward(layer, dr_out, dn, workspace, r_out=None, b=None, code
         if gate is None:
             raise ValueError("dgate needs the gate")
         dgp = _flat(dgate, "dgate", gate.numel(), gate.dtype, dev)
-    ws, wb = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                  workspace.numel() * workspace.element_size())
-    _on_gpu(ref)
+    ws, wb = _space(workspace, ref)
+    s = _stream(stream, ref)
     _check("iabn_resnorm_backward", lib.iabn_resnorm_backward(
         ctypes.byref(c), dop, lddo, dnp, lddn, rp, ldr, bp, ldb, cn, en, cb, eb,
         _stats(post_stats, "post_stats", T, dev), _stats(pre_stats, "pre_stats", T, dev), drp,
         lddr, dbp, lddb, _cols(dpost_weight, "dpost_weight", C, dev),
         _cols(dpost_bias, "dpost_bias", C, dev), _cols(dpre_weight, "dpre_weight", C, dev),
-        _cols(dpre_bias, "dpre_bias", C, dev), dgp, ws, wb, _stream(stream)))
+        _cols(dpre_bias, "dpre_bias", C, dev), dgp, ws, wb, s))
