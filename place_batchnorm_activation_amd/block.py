@@ -129,6 +129,7 @@ def _name(v, table, what):
 # the current stream as an integer, without torch's wrapper object (3 us a call) where this
 # torch has the accessor that its own compiler uses
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream, t):
@@ -137,6 +138,9 @@ def _stream(stream, t):
     device = t.get_device()
     if device < 0:
         raise TypeError("the library's tensors live on the GPU, got %s" % t.device)
+    if device != _current_device():
+        raise ValueError("the tensors are on GPU %d, the current one is %d (torch.cuda.device)"
+                         % (device, _current_device()))
     if stream is None:
         return _raw_stream(device) if _raw_stream else \
             torch.cuda.current_stream(device).cuda_stream

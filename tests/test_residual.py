@@ -1,0 +1,164 @@
+"""The residual modules (place_batchnorm_activation_amd.residual) on the GPU against
+torch's autograd of the same functions in float64 on the CPU.
+
+With stored tensors (keep="full") in float32 the gradients are torch's up to fp32
+rounding.  With codes they differ by the codes' own rounding: a value is off by at most
+half a step, and a step is at most 1/63.5 of its group's largest magnitude; for rows of
+normal values (largest of 32: 2 to 3 sigma) that is an rms error of 3/63.5/sqrt(12) = 1.4%
+of sigma at the most, in each operand of a gradient that codes enter.  A gradient here
+has at most three such factors: 5% in the 2-norm."""
+import pytest
+import torch
+
+pytest.importorskip("place_batchnorm_activation_amd")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from place_batchnorm_activation_amd import residual
+    from place_batchnorm_activation_amd.residual import (GLULinear, KeptLinear, ResidualMLP,
+                                                         ResNorm)
+
+
+def norm64(x, kind, w, b, eps):
+    if kind == "none":
+        return x
+    if kind == "layer":
+        x = x - x.mean(-1, keepdim=True)
+    x = x / torch.sqrt(x.square().mean(-1, keepdim=True) + eps)
+    x = x * w
+    return x if b is None else x + b
+
+
+def off(got, want):
+    want = want.double().cpu()
+    got, want = got.detach().double().cpu(), want.detach()
+    return float((got - want).norm() / (want.norm() + 1e-300))
+
+
+def leaf(t):
+    return t.detach().double().cpu().requires_grad_()
+
+
+@pytest.mark.parametrize("keep,tol", [("full", 2e-5), ("codes", 0.05)])
+@pytest.mark.parametrize("post,pre,gate", [("rms", "rms", "vector"), ("layer", "layer", "rows"),
+                                           ("none", "rms", "none"), ("none", "layer", "vector"),
+                                           ("rms", "none", "rows")])
+def test_resnorm_module(post, pre, gate, keep, tol):
+    torch.manual_seed(3)
+    B, S, C = 3, 40, 96
+    m = ResNorm(C, post, pre, alpha=0.5, gate=gate == "vector", keep=keep, device="cuda")
+    with torch.no_grad():
+        for p in m.parameters():
+            p.add_(0.2 * torch.randn_like(p))
+    r, b = (torch.randn(B, S, C, device="cuda", requires_grad=True) for _ in range(2))
+    g = torch.randn(B, C, device="cuda", requires_grad=True) if gate == "rows" else None
+    r_out, n, kept = m(r, b, g)
+    assert (kept is None) == (keep == "full" or pre == "none")
+    vr, vn = torch.randn_like(r), torch.randn_like(r)
+    loss = (r_out * vr).sum() + ((n * vn).sum() if n is not None else 0.0)
+    loss.backward()
+    p = {k: leaf(v) for k, v in m.named_parameters()}
+    r64, b64 = leaf(r), leaf(b)
+    g64 = leaf(g) if g is not None else p.get("gate")
+    br = norm64(b64, post, p.get("post_weight"), p.get("post_bias"), m.eps)
+    if g64 is not None:
+        br = br * (g64[:, None] if gate == "rows" else g64)
+    ro = r64 + 0.5 * br
+    loss64 = (ro * vr.double().cpu()).sum()
+    assert off(r_out, ro) < 1e-6
+    if pre != "none":
+        n64 = norm64(ro, pre, p["pre_weight"], p.get("pre_bias"), m.eps)
+        assert off(n, n64) < 1e-6
+        loss64 = loss64 + (n64 * vn.double().cpu()).sum()
+    loss64.backward()
+    assert off(r.grad, r64.grad) < tol and off(b.grad, b64.grad) < tol
+    if g is not None:
+        assert off(g.grad, g64.grad) < tol
+    for k, v in m.named_parameters():
+        assert off(v.grad, p[k].grad) < tol, k
+
+
+@pytest.mark.parametrize("dtype,rounding", [(torch.float32, 1e-6), (torch.bfloat16, 0.01)])
+def test_linear_and_glu_modules(dtype, rounding):
+    torch.manual_seed(5)
+    T, C, F = 300, 160, 104
+    norm = ResNorm(C, pre="layer", device="cuda")
+    up = KeptLinear(C, 2 * F, device="cuda", dtype=dtype)
+    alone = KeptLinear(C, 2 * F, device="cuda", dtype=dtype)
+    alone.load_state_dict(up.state_dict())
+    down = GLULinear(F, C, device="cuda", dtype=dtype, act="gelu")
+    x = torch.randn(T, C, device="cuda").to(dtype).requires_grad_()
+    _, n, kept = norm(x)
+    dy = torch.randn(T, C, device="cuda").to(dtype)
+    y = down(up(n, kept))
+    y.backward(dy)
+    p = {k: leaf(v) for k, v in [("uw", up.weight), ("ub", up.bias), ("dw", down.weight),
+                                 ("db", down.bias), ("nw", norm.pre_weight),
+                                 ("nb", norm.pre_bias)]}
+    x64 = leaf(x)
+    n64 = norm64(x64, "layer", p["nw"], p["nb"], norm.eps)
+    g, u = (n64 @ p["uw"].t() + p["ub"]).chunk(2, -1)
+    y64 = (torch.nn.functional.gelu(g) * u) @ p["dw"].t() + p["db"]
+    assert off(y, y64) < max(rounding, 1e-5)
+    y64.backward(dy.double().cpu())
+    tol = 0.05 + 3 * rounding
+    for got, want in ((x, x64), (up.weight, p["uw"]), (up.bias, p["ub"]), (down.weight, p["dw"]),
+                      (down.bias, p["db"]), (norm.pre_weight, p["nw"]), (norm.pre_bias, p["nb"])):
+        assert off(got.grad, want.grad) < tol
+    # the layer's own codes of n serve as well as the norm's of xhat
+    z = alone(n.detach())
+    z.backward(torch.randn_like(z))
+    dz = torch.randn_like(z)
+    alone.weight.grad = None
+    alone(n.detach()).backward(dz)
+    assert off(alone.weight.grad, dz.double().t() @ n.detach().double()) < tol
+
+
+def test_inference_keeps_nothing():
+    m = ResidualMLP(64, 32, device="cuda", dtype=torch.bfloat16)
+    x = torch.randn(5, 64, device="cuda", dtype=torch.bfloat16)
+    r, b = m(x)
+    with torch.no_grad():
+        r2, b2 = m(x)
+        assert m.norm(x)[2] is None
+    assert torch.equal(r, r2) and torch.equal(b, b2)
+    one, _ = m(x[:1])
+    assert torch.equal(one, r[:1])
+
+
+def test_unused_outputs_and_strided_gradients():
+    """dn or dr_out missing, gradients that are expanded or transposed views."""
+    m = ResNorm(48, post="rms", pre="rms", device="cuda")
+    r, b = (torch.randn(6, 48, device="cuda", requires_grad=True) for _ in range(2))
+    r_out, n, _ = m(r, b)
+    n.sum().backward()                                  # an expanded gradient, dr_out None
+    want = [t.grad.clone() for t in (r, b)]
+    r.grad = b.grad = None
+    r_out, n, _ = m(r, b)
+    (n.t().contiguous().t() * torch.ones(48, 6, device="cuda").t()).sum().backward()
+    assert torch.equal(r.grad, want[0]) and torch.equal(b.grad, want[1])
+    r.grad = b.grad = None
+    m(r, b)[0].sum().backward()                         # dn None
+    assert torch.equal(r.grad, torch.ones_like(r)) and bool(torch.isfinite(b.grad).all())
+    with pytest.raises(ValueError):
+        m(r, b[:3])
+    with pytest.raises(ValueError):
+        ResNorm(48, keep="some")
+    with pytest.raises(ValueError):
+        GLULinear(10, 48, device="cuda")(r)
+
+
+def test_example_trains_like_plain_torch_with_less_memory(capsys):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "residual_mlp.py")
+    spec = importlib.util.spec_from_file_location("residual_mlp_example", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    kept, plain = mod.main(["--rows", "4096", "--cols", "512", "--hidden", "1024", "--layers", "4",
+                            "--steps", "6"])
+    assert plain[0][-1] < plain[0][0] and kept[0][-1] < kept[0][0]
+    for a, b in zip(kept[0], plain[0]):
+        assert abs(a - b) < 0.01 * abs(b)
+    assert kept[2] < 0.6 * plain[2]
