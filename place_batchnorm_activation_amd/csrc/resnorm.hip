@@ -131,8 +131,8 @@ __device__ __forceinline__ void normalise(float (&x)[NV][8], const int (&col)[NV
 // A thread's eight columns of a row of C >= 8 columns: those at `at`, which for the last
 // vector of a ragged row begin `skip` columns early, so that every access of the row is
 // one wide one inside it.  The skipped columns belong to the thread before: they are kept
-// out of sums (their weights read as zero) and are not written.  Threads past the row
-// (in == false) read its last columns, with zero weights.
+// out of sums (mask) and are not written.  Threads past the row (in == false) read its
+// last columns and own none.
 struct Span {
     uint32_t c, at, skip;
     bool in;
@@ -144,6 +144,14 @@ struct Span {
         skip = in ? c - at : 0u;
     }
     __device__ __forceinline__ bool own(int e) const { return in && uint32_t(e) >= skip; }
+    // zero where not owned, by selection: the columns read twice may hold an infinity
+    __device__ __forceinline__ void mask(bool ragged, float (&v)[8]) const
+    {
+        if (ragged || !in) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = own(e) ? v[e] : 0.f;
+        }
+    }
     template <int DT>
     __device__ __forceinline__ Raw8<DT> load(const char* row) const
     {
@@ -348,16 +356,9 @@ __global__ __launch_bounds__(TPR == kWave ? kThreads : TPR) void k_resnorm_fwd_r
         rr = span.load<DT>(row_ptr<DT>(a.r, i, a.ldr));
         if (a.b) rb = span.load<DT>(row_ptr<DT>(a.b, i, a.ldb));
     };
-    // zero where this thread does not own the column
-    auto mask = [&](float (&v)[8]) {
-        if (ragged || !span.in) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = span.own(e) ? v[e] : 0.f;
-        }
-    };
     auto normed = [&](float (&x)[8], bool layer, float* stats) {
         float mean = 0.f;
-        mask(x);
+        span.mask(ragged, x);
         if (layer) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) mean += x[e];
@@ -365,7 +366,7 @@ __global__ __launch_bounds__(TPR == kWave ? kThreads : TPR) void k_resnorm_fwd_r
             mean *= inv_c;
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] -= mean;
-            mask(x);
+            span.mask(ragged, x);
         }
         float s = 0.f;
 #pragma unroll
@@ -396,7 +397,7 @@ __global__ __launch_bounds__(TPR == kWave ? kThreads : TPR) void k_resnorm_fwd_r
         if (a.b) {
             if (post) normed(x, a.post == kNormLayer, a.post_stats);
             if (a.codes_b) {
-                if (!post) mask(x);
+                if (!post) span.mask(ragged, x);
                 put_codes(a.codes_b, a.exps_b, x);
             }
             if (post) {
@@ -800,6 +801,7 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
     const bool has_b = ALL || a.db != nullptr, post = ALL || a.post != kNormNone;
     const bool pre = ALL || (a.pre != kNormNone && a.dn);
     const bool read_b = ALL || (has_b && (post || (GATE && a.dgate)));
+    const bool ragged = C % kRowV != 0;
     Span span(threadIdx.x, C);
     auto load_saved = [&](Saved<DT, CODES, true>& s, const char* x, const int8_t* codes,
                           const uint8_t* exps) {
@@ -898,6 +900,8 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
             kept(0, w_n);
             widen8<DT>(dn, g);
             sn.xhat(mn, rn, x);
+            span.mask(ragged, g);
+            span.mask(ragged, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 s_nw[e] = fmaf(g[e], x[e], s_nw[e]);
@@ -927,6 +931,8 @@ __global__ __launch_bounds__(NT) void k_resnorm_bwd_row(ResnormBwd a, RowDeal d,
         // h = alpha*g*D*w_post with its sums
         if (read_b) {
             sb.xhat(mb_row, post ? rb_row : 1.f, x);
+            span.mask(ragged, x);
+            span.mask(ragged, D);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = 0.f;

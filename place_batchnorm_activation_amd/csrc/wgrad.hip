@@ -479,19 +479,33 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * kWave) void k_wgrad(WgradAr
     }
 }
 
-// Adds the shares of the t axis in their order: one output row a blockIdx.y.
+// The sum of `count` shares, `stride` apart, in their order; eight loads at a time in
+// flight (past the last share, the last one again).
+__device__ __forceinline__ float sum_shares(const float* p, int64_t stride, int64_t count)
+{
+    float s = 0.f;
+    for (int64_t i = 0; i < count; i += 8) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = p[(i + u < count ? i + u : count - 1) * stride];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i + u < count) s += v[u];
+    }
+    return s;
+}
+
+// Adds the shares of the t axis: one output row a blockIdx.y.
 __global__ __launch_bounds__(kThreads) void k_wgrad_join(WgradArgs a, WgradTiles tl)
 {
     const int64_t n = blockIdx.y, k = int64_t(blockIdx.x) * kThreads + threadIdx.x;
     float s = 0.f;
     if (tl.want_sum) {
-        for (int64_t i = 0; i < tl.splits; ++i) s += tl.part_sum[i * a.N + n];
+        s = sum_shares(tl.part_sum + n, a.N, tl.splits);
         if (a.dbias && k == 0) a.dbias[n] = a.accumulate ? a.dbias[n] + s : s;
     }
     if (k >= a.K) return;
-    float v = 0.f;
-#pragma unroll 8
-    for (int64_t i = 0; i < tl.splits; ++i) v += tl.part[(i * a.N + n) * a.K + k];
+    float v = sum_shares(tl.part + n * a.K + k, a.N * a.K, tl.splits);
     if (a.scale) v *= a.scale[k];
     if (a.shift) v = fmaf(a.shift[k], s, v);
     with_out(a, [&](auto put) { put(n * a.lddw + k, v); });

@@ -618,6 +618,35 @@ def test_resnorm_rows_keep_to_themselves():
         assert int(cn[1][4].min()) == 255
 
 
+@pytest.mark.parametrize("C", [1001, 1100, 1537, 4095])
+def test_resnorm_gradients_that_overflowed(C):
+    """An infinity in the last columns of dn or dr_out: the row's gradients are
+    non-finite where the formula's are, other rows untouched."""
+    T = 3
+    g = gen(C)
+    r, b, dro, dn = (torch.randn(T, C, generator=g) for _ in range(4))
+    dn[1, C - 2] = float("inf")
+    dro[2, C - 1] = float("-inf")
+    p = dict(post="rms", pre="rms", alpha=1.0, eps=1e-5, post_weight=None, post_bias=None,
+             pre_weight=None, pre_bias=None, gate=None)
+    layer, _ = spec(p, C)
+    ro, n = torch.empty(T, C, device="cuda"), torch.empty(T, C, device="cuda")
+    st = dict(post_stats=torch.empty(T, 2, device="cuda"),
+              pre_stats=torch.empty(T, 2, device="cuda"))
+    iabn.iabn_resnorm_forward(layer, r.cuda(), b.cuda(), ro, n, **st)
+    dr, db = torch.empty_like(ro), torch.empty_like(ro)
+    iabn.iabn_resnorm_backward(layer, dro.cuda(), dn.cuda(), iabn.resnorm_workspace(T, C), r_out=ro,
+                               b=b.cuda(), dr=dr, db=db, **st)
+    pst, nst = ref.f64(st["post_stats"]), ref.f64(st["pre_stats"])
+    with np.errstate(invalid="ignore"):
+        want, mag = ref.resnorm_grad(ref.f64(dro), ref.f64(dn), ref.f64(ro) * nst[:, 1:], nst[:, 1:],
+                                     ref.f64(b) * pst[:, 1:], pst[:, 1:], p, 1)
+    for k, got in (("dr", dr), ("db", db)):
+        assert np.array_equal(np.isnan(ref.f64(got)), np.isnan(want[k])), k
+        assert np.array_equal(np.isinf(ref.f64(got)), np.isinf(want[k])), k
+    assert np.isfinite(ref.f64(dr)[0]).all() and np.isinf(ref.f64(dr)[1]).any()
+
+
 def test_resnorm_of_no_rows():
     C = 40
     w = torch.ones(C, device="cuda")
