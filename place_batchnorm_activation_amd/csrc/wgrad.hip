@@ -500,10 +500,8 @@ __global__ __launch_bounds__(kThreads) void k_wgrad_join(WgradArgs a, WgradTiles
 {
     const int64_t n = blockIdx.y, k = int64_t(blockIdx.x) * kThreads + threadIdx.x;
     float s = 0.f;
-    if (tl.want_sum) {
-        s = sum_shares(tl.part_sum + n, a.N, tl.splits);
-        if (a.dbias && k == 0) a.dbias[n] = a.accumulate ? a.dbias[n] + s : s;
-    }
+    if (a.shift || (a.dbias && k == 0)) s = sum_shares(tl.part_sum + n, a.N, tl.splits);
+    if (a.dbias && k == 0) a.dbias[n] = a.accumulate ? a.dbias[n] + s : s;
     if (k >= a.K) return;
     float v = sum_shares(tl.part + n * a.K + k, a.N * a.K, tl.splits);
     if (a.scale) v *= a.scale[k];
@@ -518,8 +516,10 @@ __global__ __launch_bounds__(kThreads) void k_wgrad_join(WgradArgs a, WgradTiles
 // 128 x 128, whose shares of t are larger and fewer (us, 256 against 128 tiles, bf16:
 // 8192 x 2048 x 4096 166 against 191, 8192 x 2048^2 95 against 108; 8192 x 1024^2 44 against
 // 40, 1024^3 29 against 21).  f16 and f32: 128 x 256, which shares the conversion of dY
-// among twice the products (8192 x 4096^2 503 against 675 us f16, 740 against 953 f32;
-// 2049 x 1001 x 777 f32 30.3 against 28.7), and 128 x 128 where K is under 256.
+// among twice the products, where its tiles and their splits make a workgroup for every CU
+// (8192 x 4096^2 503 against 675 us f16, 740 against 953 f32; 2048^2 x 1024 f32 43 against
+// 47; but 1024 x 512^2 20 against 16 f32 and 300 x 1000 x 777 22 against 15 f16), else, and
+// where K is under 256, 128 x 128.
 WgradTiles make_tiles(int64_t T, int64_t N, int64_t K, int dtype, int64_t cus)
 {
     WgradTiles tl{};
@@ -529,7 +529,8 @@ WgradTiles make_tiles(int64_t T, int64_t N, int64_t K, int dtype, int64_t cus)
         tl.bm = tl.bn = big ? 256 : 128;
     } else {
         tl.bm = 128;
-        tl.bn = Kp >= 256 && N >= 128 ? 256 : 128;
+        const int64_t wide = ceil_div(N, 128) * ceil_div(K, 256) * max64(1, ceil_div(T, kBT) / 4);
+        tl.bn = Kp >= 256 && N >= 128 && wide >= cus ? 256 : 128;
     }
     tl.nt = uint32_t(ceil_div(N, tl.bm));
     tl.kt = uint32_t(ceil_div(K, tl.bn));

@@ -324,6 +324,12 @@ def test_linear_wgrad_large_tiles(T, N, K, affine):
     test_linear_wgrad(T, N, K, torch.bfloat16, affine)
 
 
+@pytest.mark.parametrize("T,N,K", [(70, 4096, 2090), (130, 2053, 4100), (4200, 1030, 600)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32], ids=str)
+def test_linear_wgrad_large_tiles_of_several_parts(T, N, K, dtype):
+    test_linear_wgrad(T, N, K, dtype, "shift")
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 def test_linear_wgrad_of_no_rows(dtype):
     dy = torch.empty(0, 6, device="cuda", dtype=dtype)
