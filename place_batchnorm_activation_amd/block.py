@@ -47,7 +47,7 @@ def _rows(t, name):
     if len(shape) == 2:
         T, C = shape
         ld, cs = t.stride()
-        if cs != 1 and C > 1:
+        if cs != 1 and C > 1 and T > 0:          # of no rows, any strides will do
             raise ValueError("%s: the last dimension must be contiguous" % name)
         if T <= 1:
             ld = C

@@ -209,3 +209,14 @@ def test_binding_checks():
         iabn.iabn_resnorm_backward(layer, None, None, None)
     with pytest.raises(TypeError):                      # host tensors, all else being right
         iabn.iabn_resnorm_forward(layer, t(4, 40), None, None, t(4, 40), stream=0)
+
+
+def test_tensors_of_no_rows_are_taken_with_any_strides():
+    """An expanded gradient of an empty batch keeps strides of zero through contiguous()."""
+    for shape in ((0, 40), (3, 0, 40), (0, 1)):
+        t = torch.ones(()).expand(*shape)
+        assert set(t.contiguous().stride()) <= {0, 1} and 0 in t.stride()
+        ld, rows, cols = block._rows(t, "t")[1:]
+        assert rows == 0 and cols == shape[-1] and ld >= cols
+    with pytest.raises(ValueError):
+        block._rows(torch.ones(()).expand(1, 40), "t")

@@ -162,3 +162,17 @@ def test_example_trains_like_plain_torch_with_less_memory(capsys):
     for a, b in zip(kept[0], plain[0]):
         assert abs(a - b) < 0.01 * abs(b)
     assert kept[2] < 0.6 * plain[2]
+
+
+def test_an_empty_batch_has_gradients():
+    """Expanded gradients of no rows, through every module of a block."""
+    m = ResidualMLP(64, 32, device="cuda")
+    r = torch.empty(0, 64, device="cuda", requires_grad=True)
+    b = torch.empty(0, 64, device="cuda", requires_grad=True)
+    r_out, n, _ = m.norm(r, b)
+    (r_out.sum() + n.sum()).backward()
+    r_out, out = m(r, b)
+    out.sum().backward()
+    assert r.grad.shape == b.grad.shape == (0, 64)
+    for k, p in m.named_parameters():
+        assert float(p.grad.abs().max()) == 0.0, k
