@@ -468,6 +468,8 @@ size_t iabn_resnorm_workspace_size(int64_t rows, int64_t cols, int64_t rows_per_
  * NULL).  dpost_*, dpre_* fp32 [cols], dgate of gate_dtype shaped as gate; each may be
  * NULL.  b (codes_b) is needed with db for a post-norm or dgate only.  dr and db may be
  * exactly dr_out or dn, but not one another, and must not overlap what was saved.
+ * rows == 0: dpost_* and dpre_* are written as zeros; dgate has no rows and is not
+ * written (a caller whose gate is one vector for every row clears it itself).
  * workspace: device, 16-byte aligned; it carries no status word.  Sums over rows are
  * fp32 within a block of rows and finished in fp64, in a fixed order. */
 iabn_status iabn_resnorm_backward(const iabn_resnorm *layer, const void *dr_out,

@@ -354,3 +354,7 @@ def iabn_resnorm_backward(layer, dr_out, dn, workspace, r_out=None, b=None, code
         lddr, dbp, lddb, _cols(dpost_weight, "dpost_weight", C, dev),
         _cols(dpost_bias, "dpost_bias", C, dev), _cols(dpre_weight, "dpre_weight", C, dev),
         _cols(dpre_bias, "dpre_bias", C, dev), dgp, ws, wb, s))
+    if T == 0 and dgate is not None:
+        # the library knows a gate's rows from those of the tensors, which are none here
+        with torch.cuda.stream(torch.cuda.ExternalStream(s, device=dgate.device)):
+            dgate.zero_()

@@ -667,6 +667,24 @@ def test_resnorm_of_no_rows():
     assert float(dw[0].abs().max()) == 0.0 and float(dw[1].abs().max()) == 0.0
 
 
+@pytest.mark.parametrize("groups", [1, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+def test_resnorm_gate_gradient_of_no_rows(dtype, groups):
+    """Zeros, also on another stream than the current one."""
+    C = 40
+    layer = iabn.ResNormSpec(C, post="rms", pre="rms")
+    e, st = torch.empty(0, C, device="cuda", dtype=dtype), torch.empty(0, 2, device="cuda")
+    gate = torch.ones(groups, C, device="cuda", dtype=dtype)
+    for stream in (None, torch.cuda.Stream()):
+        dgate = torch.full_like(gate, 3.0)
+        torch.cuda.synchronize()
+        iabn.iabn_resnorm_backward(layer, e, e, None, r_out=e, b=e, post_stats=st, pre_stats=st,
+                                   gate=gate, dr=torch.empty_like(e), db=torch.empty_like(e),
+                                   dgate=dgate, stream=stream)
+        torch.cuda.synchronize()
+        assert float(dgate.float().abs().max()) == 0.0
+
+
 @pytest.mark.parametrize("post,pre,gate", [("rms", "rms", "vector"), ("layer", "layer", "full"),
                                            ("none", "layer", "none")])
 def test_resnorm_gradient_against_differences(post, pre, gate):

@@ -176,3 +176,16 @@ def test_an_empty_batch_has_gradients():
     assert r.grad.shape == b.grad.shape == (0, 64)
     for k, p in m.named_parameters():
         assert float(p.grad.abs().max()) == 0.0, k
+
+
+def test_an_empty_batch_leaves_a_gate_no_gradient():
+    m = ResNorm(64, post="rms", pre="rms", gate=True, device="cuda")
+    r, b = (torch.empty(0, 64, device="cuda", requires_grad=True) for _ in range(2))
+    own = torch.ones(5, 64, device="cuda", requires_grad=True)
+    for gate, leaf_ in ((None, m.gate), (own, own)):
+        dirt = [torch.full((5, 64), 9.0, device="cuda") for _ in range(16)]
+        dirt += [torch.full((64,), 9.0, device="cuda") for _ in range(16)]
+        r_out, n, _ = m(r, b, gate)
+        del dirt                       # what the next allocations find in memory
+        torch.autograd.backward([r_out, n], [torch.empty_like(r_out), torch.empty_like(n)])
+        assert float(leaf_.grad.abs().max()) == 0.0
