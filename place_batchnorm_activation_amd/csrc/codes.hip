@@ -29,7 +29,7 @@ __global__ __launch_bounds__(kThreads) void k_codes_pack(const void* __restrict_
     const int64_t row = row0 + r;
     const uint32_t c = (i - r * vpr) * kRowV, Cp = vpr * kRowV;
     float v[8];
-    widen8<DT>(load8<DT, WHOLE>(row_ptr<DT>(x, row, ldx), c, C), v);
+    widen8<DT>(load8<DT, WHOLE, uint64_t>(row_ptr<DT>(x, row, ldx), c, C), v);
     uint32_t E;
     const uint2 q = encode8(v, E);
     store_codes(codes + row * Cp, exps + row * (Cp / kGroup), Cp, c, q, E);
@@ -52,12 +52,12 @@ __global__ __launch_bounds__(kThreads) void k_codes_unpack(
             exps[row * (Cp / kGroup) + c / kGroup], v);
     if (scale || shift) {                   // uniform over the launch
         float a[8], b[8];
-        load_cols<WHOLE>(scale, c, C, 1.f, a);
-        load_cols<WHOLE>(shift, c, C, 0.f, b);
+        load_cols<WHOLE, uint64_t>(scale, c, C, 1.f, a);
+        load_cols<WHOLE, uint64_t>(shift, c, C, 0.f, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], a[e], b[e]);
     }
-    store8<DT, WHOLE>(row_ptr<DT>(y, row, ldy), c, C, v);
+    store8<DT, WHOLE, uint64_t>(row_ptr<DT>(y, row, ldy), c, C, v);
 }
 
 }  // namespace

@@ -73,9 +73,9 @@ __global__ __launch_bounds__(kThreads) void k_glu_fwd(GluFwd a, int64_t row0, ui
     const int64_t row = row0 + r;
     const uint32_t c = (i - r * vpr) * kRowV, Fp = vpr * kRowV;
     float g[8], u[8];
-    const Raw8<DT> rg = load8<DT, WHOLE>(row_ptr<DT>(a.gate, row, a.ldg), c, F);
+    const Raw8<DT> rg = load8<DT, WHOLE, uint64_t>(row_ptr<DT>(a.gate, row, a.ldg), c, F);
     if (a.up) {
-        const Raw8<DT> ru = load8<DT, WHOLE>(row_ptr<DT>(a.up, row, a.ldu), c, F);
+        const Raw8<DT> ru = load8<DT, WHOLE, uint64_t>(row_ptr<DT>(a.up, row, a.ldu), c, F);
         widen8<DT>(ru, u);
     }
     widen8<DT>(rg, g);
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kThreads) void k_glu_fwd(GluFwd a, int64_t row0, ui
         glu_act<ACT>(g[e], f, d);
         g[e] = a.up ? f * u[e] : f;
     }
-    store8<DT, WHOLE>(row_ptr<DT>(a.out, row, a.ldo), c, F, g);
+    store8<DT, WHOLE, uint64_t>(row_ptr<DT>(a.out, row, a.ldo), c, F, g);
 }
 
 template <int DT, int ACT, bool WHOLE>
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(kThreads) void k_glu_bwd(GluBwd a, int64_t row0, ui
     const int64_t row = row0 + r;
     const uint32_t c = (i - r * vpr) * kRowV, Fp = vpr * kRowV;
     if (c >= uint32_t(F)) return;
-    const Raw8<DT> ro = load8<DT, WHOLE>(row_ptr<DT>(a.dout, row, a.lddo), c, F);
+    const Raw8<DT> ro = load8<DT, WHOLE, uint64_t>(row_ptr<DT>(a.dout, row, a.lddo), c, F);
     float g[8], u[8], o[8];
     decode8(*reinterpret_cast<const uint2*>(a.codes_g + row * Fp + c),
             a.exps_g[row * (Fp / kGroup) + c / kGroup], g);
@@ -124,9 +124,9 @@ __global__ __launch_bounds__(kThreads) void k_glu_bwd(GluBwd a, int64_t row0, ui
         dg[e] = a.codes_u ? o[e] * u[e] * d : o[e] * d;
         o[e] = a.codes_u ? f * u[e] : f;
     }
-    store8<DT, WHOLE>(row_ptr<DT>(a.dgate, row, a.lddg), c, F, dg);
-    if (a.codes_u) store8<DT, WHOLE>(row_ptr<DT>(a.dup, row, a.lddu), c, F, du);
-    if (a.out) store8<DT, WHOLE>(row_ptr<DT>(a.out, row, a.ldo), c, F, o);
+    store8<DT, WHOLE, uint64_t>(row_ptr<DT>(a.dgate, row, a.lddg), c, F, dg);
+    if (a.codes_u) store8<DT, WHOLE, uint64_t>(row_ptr<DT>(a.dup, row, a.lddu), c, F, du);
+    if (a.out) store8<DT, WHOLE, uint64_t>(row_ptr<DT>(a.out, row, a.ldo), c, F, o);
 }
 
 template <class F>

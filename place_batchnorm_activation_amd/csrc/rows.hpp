@@ -7,6 +7,10 @@
 // accesses below promise the alignment of one element only, which the hardware's
 // unaligned access mode serves, so odd widths and slices keep wide loads.
 //
+// OFF is the type of a byte offset within a row: uint64_t where a row may have 2^30 columns
+// and more (codes, gated unit: its address is a lane's own there, and 64 bits cost nothing),
+// uint32_t in the norms, whose rows are narrow and whose row addresses are scalar.
+//
 // Codes: value = q * 2^(E - 127), q in [-127, 127], E one byte for each group.
 // E is the smallest exponent under which the group's largest magnitude rounds to
 // at most 127: with that magnitude m * 2^k, 1 <= m < 2, m * 64 rounds to at most
@@ -86,7 +90,7 @@ __device__ __forceinline__ void shift_down(uint32_t (&w)[DT == kF32 ? 8 : 4], ui
 // every load is one wide access; rows of fewer than eight columns are read one by one.
 // (The ragged form takes dozens of vector instructions a load, which bounds kernels of
 // several loads a row: 16640 x 1152 in resnorm's backward took 167 us with it.)
-template <int DT, bool WHOLE>
+template <int DT, bool WHOLE, class OFF = uint32_t>
 __device__ __forceinline__ Raw8<DT> load8(const char* row, uint32_t c, int C)
 {
     constexpr int N = DT == kF32 ? 8 : 4, es = DT == kF32 ? 4 : 2;
@@ -96,7 +100,7 @@ __device__ __forceinline__ Raw8<DT> load8(const char* row, uint32_t c, int C)
     if constexpr (WHOLE) {
         if (c < uint32_t(C)) {
 #pragma unroll
-            for (int h = 0; h < N / 4; ++h) r.q[h] = load16_any(row + c * es + 16 * h);
+            for (int h = 0; h < N / 4; ++h) r.q[h] = load16_any(row + OFF(c) * es + 16 * h);
         }
         return r;
     }
@@ -105,7 +109,7 @@ __device__ __forceinline__ Raw8<DT> load8(const char* row, uint32_t c, int C)
         const uint32_t last = uint32_t(C) - kRowV, at = c < last ? c : last;
         if (c < uint32_t(C)) {
 #pragma unroll
-            for (int h = 0; h < N / 4; ++h) r.q[h] = load16_any(row + at * es + 16 * h);
+            for (int h = 0; h < N / 4; ++h) r.q[h] = load16_any(row + OFF(at) * es + 16 * h);
         }
         if (c > last && c < uint32_t(C)) {
 #pragma unroll
@@ -153,11 +157,11 @@ __device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8])
 
 // Eight values at column c of a row of C columns, rounded once to the storage dtype;
 // those past its end are not written (WHOLE as above; else four, two and one of the rest).
-template <int DT, bool WHOLE>
+template <int DT, bool WHOLE, class OFF = uint32_t>
 __device__ __forceinline__ void store8(const char* row, uint32_t c, int C, const float (&v)[8])
 {
     constexpr int es = DT == kF32 ? 4 : 2;
-    char* p = const_cast<char*>(row) + c * es;
+    char* p = const_cast<char*>(row) + OFF(c) * es;
     const int nv = valid8(int(c), C);
     if (nv >= kRowV) {
         if constexpr (DT == kF32) {
@@ -205,12 +209,12 @@ __device__ __forceinline__ void store8(const char* row, uint32_t c, int C, const
 }
 
 // Eight of a per-column vector of C fp32 values (null: `none`); zero past its end.
-template <bool WHOLE>
+template <bool WHOLE, class OFF = uint32_t>
 __device__ __forceinline__ void load_cols(const float* p, uint32_t c, int C, float none,
                                           float (&v)[8])
 {
     if (p) {
-        widen8<kF32>(load8<kF32, WHOLE>(reinterpret_cast<const char*>(p), c, C), v);
+        widen8<kF32>(load8<kF32, WHOLE, OFF>(reinterpret_cast<const char*>(p), c, C), v);
     } else {
         const int nv = valid8(int(c), C);
 #pragma unroll

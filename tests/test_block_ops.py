@@ -152,6 +152,51 @@ def test_codes_past_32_bit_offsets():
     assert torch.equal(x[-5000:], y) and float(x[:1000].abs().max()) == 0.0
 
 
+#: fp32 columns whose bytes pass 32 bits: whole vectors, and a ragged end
+LONG = [(1 << 30) + 72, (1 << 30) + 75]
+
+
+@pytest.mark.parametrize("cols", LONG)
+def test_codes_of_a_row_past_32_bit_offsets(cols):
+    """One fp32 row of more than 2^30 columns, as a flat tensor makes: its first and last
+    groups come out as they do on their own."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB")
+    n = 4096 + cols % 32                                    # whole groups and the ragged end
+    head, tail = (values(gen(s), 1, n, torch.float32)[0].cuda() for s in (1, 2))
+    x = torch.zeros(cols, device="cuda")
+    x[:n], x[-n:] = head, tail
+    codes, exps = iabn.codes_empty(1, cols)
+    iabn.iabn_codes_pack(x, codes, exps)
+    p = iabn.code_cols(n)
+    ends = {}
+    for name, v in (("head", head), ("tail", tail)):
+        ends[name] = iabn.codes_empty(1, n)
+        iabn.iabn_codes_pack(v, *ends[name])
+    assert torch.equal(codes[0, -p:], ends["tail"][0][0])
+    assert torch.equal(exps[0, -p // 32:], ends["tail"][1][0])
+    assert torch.equal(codes[0, :n - n % 32], ends["head"][0][0, :n - n % 32])
+    assert int(exps[0, 1 << 20:-(1 << 20)].max()) == 0
+    # back, alone and with a scale and a shift, to fp32 and (the vectors' rows only are
+    # long there) bf16
+    vec = torch.ones(cols, device="cuda")
+    vec[-n:] = torch.linspace(1, 2, n, device="cuda")
+    for scale in (None, vec):
+        for dtype in (torch.float32, torch.bfloat16):
+            y = torch.full((cols,), 5.0, device="cuda", dtype=dtype)
+            iabn.iabn_codes_unpack(codes, exps, y, scale, scale)
+            for at, v in ((slice(0, 4096), "head"), (slice(cols - n, cols), "tail")):
+                k = at.stop - at.start
+                want = torch.empty(n, device="cuda", dtype=dtype)
+                s = None if scale is None else scale[at][:k].contiguous()
+                if s is not None and k < n:
+                    s = torch.cat((s, s.new_ones(n - k)))
+                iabn.iabn_codes_unpack(*ends[v], want, s, s)
+                assert torch.equal(y[at], want[:k])
+            mid = y[1 << 20:-(1 << 20)]
+            assert float(mid.min()) == float(mid.max()) == (0.0 if scale is None else 1.0)
+
+
 # ---------------------------------------------------------------------------
 # gated activation
 
@@ -209,6 +254,31 @@ def test_glu(T, F, dtype, act, gated):
     assert torch.equal(h2[:, :F], o2)
     iabn.iabn_glu_backward(*kept[0], *kept[1], d2, d2, torch.empty_like(d2) if gated else None, act)
     assert torch.equal(d2, dg)
+
+
+@pytest.mark.parametrize("cols", LONG)
+def test_glu_of_a_row_past_32_bit_offsets(cols):
+    """Gate and up of one fp32 row each of more than 2^30 columns: the last columns are those
+    of a short row."""
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GiB")
+    n = 4096 + cols % 32
+    ends = [values(gen(s), 1, n, torch.float32)[0].cuda() for s in (3, 4, 5)]
+    gate, up, dout = (torch.zeros(cols, device="cuda") for _ in range(3))
+    for t, e in zip((gate, up, dout), ends):
+        t[-n:] = e
+
+    def passes(g, u, d):
+        m = g.numel()
+        kept = [*iabn.codes_empty(1, m), *iabn.codes_empty(1, m)]
+        out, dg, du, again = (torch.full_like(g, 7.0) for _ in range(4))
+        iabn.iabn_glu_forward(g, u, out, "silu", *kept)
+        iabn.iabn_glu_backward(*kept, d, dg, du, "silu", out=again)
+        return out, dg, du, again
+
+    for got, want in zip(passes(gate, up, dout), passes(*ends)):
+        assert torch.equal(got[-n:], want)
+        assert float(got[:-n].abs().max()) == 0.0
 
 
 @pytest.mark.parametrize("act", ACTS)
