@@ -409,6 +409,7 @@ size_t iabn_linear_wgrad_workspace_size(int64_t rows, int64_t n, int64_t k, iabn
  *   dw = (dw +) dy^T (scale * x + shift), dbias = (dbias +) sum over rows of dy,
  * the bracketed terms with accumulate != 0.  dy [rows, n] of `dtype`; dw [n, k], rows
  * lddw apart, of dw_dtype; scale, shift fp32 [k] or NULL; dbias fp32 [n] or NULL.
+ * k == 0 leaves dbias alone to compute.
  * lddy and k stay below 2^26.  Sums are fp32; the products are exact (codes are exact in bf16, and f16 and f32
  * values of dy enter as two and three bf16 parts).  workspace: device, 16-byte
  * aligned, iabn_linear_wgrad_workspace_size bytes; it carries no status word. */

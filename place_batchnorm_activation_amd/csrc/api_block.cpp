@@ -284,7 +284,7 @@ size_t iabn_linear_wgrad_workspace_size(int64_t rows, int64_t n, int64_t k, iabn
 {
     if (check_extents(rows, n, dtype) != IABN_OK || check_extents(rows, k, dtype) != IABN_OK)
         return 0;
-    if (n == 0 || k == 0) return 0;
+    if (n == 0) return 0;
     return wgrad_workspace_bytes(rows, n, k, dtype, device_cus());
 }
 
@@ -296,19 +296,19 @@ iabn_status iabn_linear_wgrad(const void* dy, int64_t lddy, iabn_dtype dtype, co
 {
     IABN_TRY(check_extents(rows, n, dtype));
     IABN_TRY(check_extents(rows, k, dw_dtype));
-    if (n == 0 || k == 0) return IABN_OK;
+    if (n == 0 || (k == 0 && !dbias)) return IABN_OK;
     // tiles of 128 x 128 in 31 bits of workgroups
     if (double(ceil_div(n, 128)) * double(ceil_div(k, 128)) > 2.0e9) return IABN_ERR_UNSUPPORTED;
     if (lddy >= kWgradMaxLd || k >= kWgradMaxLd) return IABN_ERR_UNSUPPORTED;
     const Rows out{dw, lddw, n, k, esize(dw_dtype)};
     const Rows in{dy, lddy, rows, n, esize(dtype)};
-    IABN_TRY(check_rows(out));
+    if (k > 0) IABN_TRY(check_rows(out));
     IABN_TRY(check_vec(scale));
     IABN_TRY(check_vec(shift));
     IABN_TRY(check_vec(dbias));
     if (rows > 0) {
         IABN_TRY(check_rows(in));
-        IABN_TRY(check_codes(codes, exps));
+        if (k > 0) IABN_TRY(check_codes(codes, exps));
         IABN_TRY(check_apart(out, in));
         IABN_TRY(check_codes_apart(codes, exps, rows, k, out));
     }

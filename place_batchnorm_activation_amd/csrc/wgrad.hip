@@ -533,7 +533,7 @@ WgradTiles make_tiles(int64_t T, int64_t N, int64_t K, int dtype, int64_t cus)
         tl.bn = Kp >= 256 && N >= 128 && wide >= cus ? 256 : 128;
     }
     tl.nt = uint32_t(ceil_div(N, tl.bm));
-    tl.kt = uint32_t(ceil_div(K, tl.bn));
+    tl.kt = uint32_t(max64(1, ceil_div(K, tl.bn)));      // K == 0: dY's sums alone
     const int64_t tiles = int64_t(tl.nt) * tl.kt, steps = ceil_div(T, kBT);
     const int64_t places = dtype == kBF16 && tl.bm == 128 ? 2 * cus : cus;
     int64_t splits = max64(1, min64(places / tiles, steps / 4));
@@ -589,7 +589,8 @@ void launch_linear_wgrad(const WgradArgs& a, int dtype, int64_t cus, void* ws, h
         else go(std::false_type{});
     });
     if (tl.splits > 1)
-        hipLaunchKernelGGL(k_wgrad_join, dim3(unsigned(ceil_div(a.K, kThreads)), unsigned(a.N)),
+        hipLaunchKernelGGL(k_wgrad_join,
+                           dim3(unsigned(max64(1, ceil_div(a.K, kThreads))), unsigned(a.N)),
                            dim3(kThreads), 0, s, a, tl);
 }
 

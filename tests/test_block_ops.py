@@ -412,6 +412,23 @@ def test_linear_wgrad_of_no_rows(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("T,N", [(4, 6), (300, 200), (5000, 96), (0, 6)])
+def test_linear_wgrad_of_no_columns(T, N, dtype):
+    """The bias's gradient of a layer without inputs, in one part and in several."""
+    dy = torch.randn(T, N, generator=gen(T)).to(dtype).cuda()
+    codes, exps = iabn.codes_empty(T, 0)
+    ws = iabn.linear_wgrad_workspace(T, N, 0, dtype)
+    assert (ws is not None) == (T == 5000)
+    dw, db = torch.empty(N, 0, device="cuda"), torch.full((N,), 3.0, device="cuda")
+    iabn.iabn_linear_wgrad(dy, codes, exps, dw, ws, dbias=db)
+    d = ref.f64(dy)
+    ref.within(db, d.sum(0), (T / 16 + 8) * 2 * U * np.abs(d).sum(0) + 1e-30)
+    twice = db.clone()
+    iabn.iabn_linear_wgrad(dy, codes, exps, dw, ws, dbias=twice, accumulate=True)
+    assert torch.equal(twice, db + db)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
 def test_linear_wgrad_keeps_non_finite_values_in_place(dtype):
     """An infinity in dy reaches its row of dW only, a group of NaN codes its
     columns; the padding of the last group reaches nothing."""
