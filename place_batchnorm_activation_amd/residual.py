@@ -31,11 +31,21 @@ from . import (ResNormSpec, codes_empty, iabn_codes_pack, iabn_glu_backward, iab
 
 
 class Kept(NamedTuple):
-    """Codes of a layer's input, which is scale * value + shift (None: 1 and 0)."""
+    """Codes of a layer's input, which is scale * value + shift (None: 1 and 0).  `of`
+    says which tensor that is (its address and version): a layer given another one would
+    return that input's weight gradient, so it refuses.  None: not checked."""
     codes: torch.Tensor
     exps: torch.Tensor
     scale: Optional[torch.Tensor]
     shift: Optional[torch.Tensor]
+    of: Optional[tuple] = None
+
+    def fits(self, x):
+        """Whether these are codes of x, or of x's rows in another shape."""
+        if self.codes.shape[0] * x.shape[-1] != x.numel():
+            return False
+        return self.of is None or (x.is_contiguous() and x.data_ptr() == self.of[0] and
+                                   x._version == self.of[1])
 
 
 def _flat(t):
@@ -153,7 +163,8 @@ class ResNorm(torch.nn.Module):
         kept = None
         if codes is not None:
             kept = Kept(codes, exps, self.pre_weight.detach(),
-                        None if self.pre_bias is None else self.pre_bias.detach())
+                        None if self.pre_bias is None else self.pre_bias.detach(),
+                        (n.data_ptr(), n._version))
         return r_out, n, kept
 
     def extra_repr(self):
@@ -195,17 +206,22 @@ class KeptLinearFunction(torch.autograd.Function):
 
 class KeptLinear(torch.nn.Linear):
     """A linear layer that keeps its input in 8 bits: its own codes, or those of `kept`
-    (ResNorm's third output for this input).  Weight and input are of one type."""
+    (ResNorm's third output for this input, which must come as the norm returned it, in any
+    shape of the same rows).  Weight and input are of one type; with `kept`, an input of
+    another is cast to the weight's here."""
 
     def forward(self, x, kept: Optional[Kept] = None):
         if not torch.is_grad_enabled():
             return super().forward(x)
         if kept is None:
-            kept = Kept(None, None, None, None)
-        elif kept.codes.shape[0] * x.shape[-1] != x.numel():
-            raise ValueError("kept has %d rows, the input is %s" % (kept.codes.shape[0],
-                                                                   tuple(x.shape)))
-        return KeptLinearFunction.apply(x, self.weight, self.bias, *kept)
+            return KeptLinearFunction.apply(x, self.weight, self.bias, None, None, None, None)
+        if not kept.fits(x):
+            raise ValueError("kept (of %d rows) was made for another tensor than this input %s; "
+                             "without it the layer keeps its own codes"
+                             % (kept.codes.shape[0], tuple(x.shape)))
+        if x.dtype != self.weight.dtype and not torch.is_autocast_enabled("cuda"):
+            x = x.to(self.weight.dtype)
+        return KeptLinearFunction.apply(x, self.weight, self.bias, *kept[:4])
 
 
 class GLULinearFunction(torch.autograd.Function):

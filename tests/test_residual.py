@@ -189,3 +189,31 @@ def test_an_empty_batch_leaves_a_gate_no_gradient():
         del dirt                       # what the next allocations find in memory
         torch.autograd.backward([r_out, n], [torch.empty_like(r_out), torch.empty_like(n)])
         assert float(leaf_.grad.abs().max()) == 0.0
+
+
+def test_kept_codes_serve_their_own_tensor_only():
+    torch.manual_seed(11)
+    norm, other = (ResNorm(64, device="cuda") for _ in range(2))
+    lin = KeptLinear(64, 32, device="cuda")
+    x = torch.randn(4, 6, 64, device="cuda")
+    _, n, kept = norm(x)
+    for bad in (2.0 * n, n.clone(), n.transpose(0, 1), other(x)[1], n[:, :3], n.reshape(48, 32)):
+        with pytest.raises(ValueError):
+            lin(bad, kept)
+    # its rows in any shape, cut from the graph, and cast to the weight's type
+    dy = torch.randn(24, 32, device="cuda")
+    want = dy.double().t() @ n.detach().double().view(24, 64)
+    for good in (n, n.view(24, 64), n.flatten(0, 1)[None], n.detach()):
+        lin.weight.grad = None
+        lin(good, kept).backward(dy.view(*good.shape[:-1], 32), retain_graph=True)
+        assert off(lin.weight.grad, want) < 0.05
+    low = KeptLinear(64, 32, device="cuda", dtype=torch.bfloat16)
+    y = low(n, kept)
+    assert y.dtype == torch.bfloat16
+    y.backward(dy.view(4, 6, 32).bfloat16())
+    assert off(low.weight.grad, want) < 0.08
+    with torch.no_grad():
+        n.mul_(2.0)                                   # written since
+    with pytest.raises(ValueError):
+        lin(n, kept)
+    assert residual.Kept(*kept[:4]).fits(n)               # without a mark only the shape counts
