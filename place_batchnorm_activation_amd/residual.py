@@ -20,6 +20,7 @@ half a step of 1/127 to 1/64 of the largest of 32 neighbours).
 """
 from __future__ import annotations
 
+import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -58,6 +59,26 @@ def _flat(t):
     return t.reshape(-1, t.shape[-1])
 
 
+def _gate_rows(gate, shape):
+    """A gate [..., cols] as [groups, cols], each group a run of consecutive rows of a tensor
+    of `shape`.  Leading dimensions past the first must be those of the tensor (ones after
+    them): anything else would put its rows in another order than broadcasting does."""
+    if gate.dim() < 1 or gate.shape[-1] != shape[-1]:
+        raise ValueError("gate is %s, expected [..., %d]" % (tuple(gate.shape), shape[-1]))
+    lead, rows = list(gate.shape[:-1]), math.prod(shape[:-1])
+    while lead and lead[-1] == 1:
+        lead.pop()
+    if gate.dim() > 2:
+        if len(shape) > 2:
+            fits = lead == list(shape[:len(lead)])
+        else:
+            fits = len(lead) < 2 or math.prod(lead) == rows
+        if not fits:
+            raise ValueError("gate is %s, which is not a gate for runs of rows of %s"
+                             % (tuple(gate.shape), tuple(shape)))
+    return gate.reshape(math.prod(lead), shape[-1]).contiguous()
+
+
 class ResNormFunction(torch.autograd.Function):
     """(r_out, n, codes_n, exps_n); n and the codes are None without a pre-norm, the
     codes with keep="full" and keep=None (no backward will follow) too."""
@@ -82,7 +103,7 @@ class ResNormFunction(torch.autograd.Function):
                 cb, eb = codes_empty(T, C, r.device)
             if has_n:
                 cn, en = codes_empty(T, C, r.device)
-        gate2 = None if gate is None else gate.reshape(-1, C).contiguous()
+        gate2 = None if gate is None else _gate_rows(gate, shape)
         iabn_resnorm_forward(layer, r2, b2, r_out, n, gate2, post_stats, pre_stats, cb, eb, cn, en)
         full = train and keep == "full"
         ctx.save_for_backward(gate2, post_weight, post_bias, pre_weight, pre_bias, post_stats,
@@ -134,7 +155,8 @@ class ResNorm(torch.nn.Module):
     n = pre(r') (post and pre: "none", "rms" or "layer").  Norm weights and biases are
     float32, biases with layer norms only.  gate=True learns a vector [cols]; forward's
     own gate, [cols] or [groups, cols] for rows / groups consecutive rows each, of
-    float32 or the rows' type, takes its place.
+    float32 or the rows' type, takes its place; for rows [b, s, cols] also [b, 1, cols] or
+    [b, s, cols].
 
     forward(r, b=None) -> (r', n, kept): kept is what KeptLinear takes for n, None with
     keep="full" (the backward then reads r' and b themselves), in inference and without a

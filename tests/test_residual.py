@@ -217,3 +217,27 @@ def test_kept_codes_serve_their_own_tensor_only():
     with pytest.raises(ValueError):
         lin(n, kept)
     assert residual.Kept(*kept[:4]).fits(n)               # without a mark only the shape counts
+
+
+def test_gates_are_broadcast_or_refused():
+    """Whatever shape of gate is taken means what broadcasting makes of it."""
+    torch.manual_seed(13)
+    B, S, C = 4, 64, 64
+    m = ResNorm(C, pre="none", keep="full", device="cuda")
+    r, b = torch.zeros(B, S, C, device="cuda"), torch.randn(B, S, C, device="cuda")
+    for shape in ((C,), (1, C), (1, 1, C), (B, 1, C), (B, S, C)):
+        g = torch.randn(*shape, device="cuda", requires_grad=True)
+        out = m(r, b, g)[0]
+        assert torch.equal(out, g.detach() * b)
+        out.sum().backward()
+        assert off(g.grad, b.double().sum_to_size(shape)) < 1e-6
+    # rows without a batch: runs of them, or one each
+    g = torch.randn(B, 1, C, device="cuda")
+    assert torch.equal(m(r.view(-1, C), b.view(-1, C), g)[0], (g * b).view(-1, C))
+    g = torch.randn(B, S, C, device="cuda")
+    assert torch.equal(m(r.view(-1, C), b.view(-1, C), g)[0], (g * b).view(-1, C))
+    # one value a row, a vector of another length, a gate for each position, batch and
+    # position in the other order
+    for shape in ((B, S, 1), (B * S, 1), (2 * C,), (C // 2,), (1, S, C), (S, B, C), (S, 1, C), ()):
+        with pytest.raises(ValueError):
+            m(r, b, torch.ones(shape, device="cuda"))
