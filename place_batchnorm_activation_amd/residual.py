@@ -24,6 +24,7 @@ import math
 from typing import NamedTuple, Optional
 
 import torch
+from torch.amp import custom_bwd, custom_fwd
 from torch.autograd.function import once_differentiable
 
 from . import (ResNormSpec, codes_empty, iabn_codes_pack, iabn_glu_backward, iabn_glu_forward,
@@ -195,7 +196,11 @@ class ResNorm(torch.nn.Module):
 
 
 class KeptLinearFunction(torch.autograd.Function):
+    """Under autocast the products run in its type, forward and backward; dw is written in
+    the weight's own."""
+
     @staticmethod
+    @custom_fwd(device_type="cuda")
     def forward(ctx, x, weight, bias, codes, exps, scale, shift):
         if ctx.needs_input_grad[1] and codes is None:
             x2 = _flat(x)
@@ -207,6 +212,7 @@ class KeptLinearFunction(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @custom_bwd(device_type="cuda")
     def backward(ctx, dy):
         weight, codes, exps, scale, shift = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -223,7 +229,7 @@ class KeptLinearFunction(torch.autograd.Function):
                               shift=shift, dbias=db)
         elif need[2]:
             db = dy2.sum(0, dtype=torch.float32)
-        return dx, dw, None if db is None else db.to(dy.dtype), None, None, None, None
+        return dx, dw, None if db is None else db.to(weight.dtype), None, None, None, None
 
 
 class KeptLinear(torch.nn.Linear):
@@ -248,6 +254,7 @@ class KeptLinear(torch.nn.Linear):
 
 class GLULinearFunction(torch.autograd.Function):
     @staticmethod
+    @custom_fwd(device_type="cuda")
     def forward(ctx, h, weight, bias, act, train):
         h2 = _flat(h)
         T, F = h2.shape[0], weight.shape[1]
@@ -265,6 +272,7 @@ class GLULinearFunction(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @custom_bwd(device_type="cuda")
     def backward(ctx, dy):
         weight, cg, eg, cu, eu = ctx.saved_tensors
         need = ctx.needs_input_grad
@@ -276,7 +284,7 @@ class GLULinearFunction(torch.autograd.Function):
         a = da if need[1] else None
         iabn_glu_backward(cg, eg, cu, eu, da, dh[:, :F], dh[:, F:], ctx.act, out=a)
         dw = dy2.t() @ a if need[1] else None
-        db = dy2.sum(0, dtype=torch.float32).to(dy.dtype) if need[2] else None
+        db = dy2.sum(0, dtype=torch.float32).to(weight.dtype) if need[2] else None
         return dh.view(ctx.shape) if need[0] else None, dw, db, None, None
 
 

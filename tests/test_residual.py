@@ -241,3 +241,35 @@ def test_gates_are_broadcast_or_refused():
     for shape in ((B, S, 1), (B * S, 1), (2 * C,), (C // 2,), (1, S, C), (S, B, C), (S, 1, C), ()):
         with pytest.raises(ValueError):
             m(r, b, torch.ones(shape, device="cuda"))
+
+
+@pytest.mark.parametrize("low", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("with_kept", [False, True], ids=["own", "kept"])
+def test_linear_and_glu_modules_under_autocast(low, with_kept):
+    """Parameters in float32, products in 16 bits, gradients in float32 (the bounds of
+    test_linear_and_glu_modules in bf16)."""
+    torch.manual_seed(17)
+    T, C, F = 300, 160, 104
+    norm = ResNorm(C, pre="layer", device="cuda")
+    up, down = KeptLinear(C, 2 * F, device="cuda"), GLULinear(F, C, device="cuda")
+    x = torch.randn(T, C, device="cuda", requires_grad=True)
+    with torch.autocast("cuda", dtype=low):
+        _, n, kept = norm(x)
+        h = up(n, kept if with_kept else None)
+        y = down(h)
+    assert n.dtype == torch.float32 and h.dtype == y.dtype == low
+    dy = torch.randn(T, C, device="cuda").to(low)
+    y.backward(dy)
+    p = {k: leaf(v) for k, v in [("uw", up.weight), ("ub", up.bias), ("dw", down.weight),
+                                 ("db", down.bias), ("nw", norm.pre_weight),
+                                 ("nb", norm.pre_bias)]}
+    x64 = leaf(x)
+    n64 = norm64(x64, "layer", p["nw"], p["nb"], norm.eps)
+    g, u = (n64 @ p["uw"].t() + p["ub"]).chunk(2, -1)
+    y64 = (torch.nn.functional.silu(g) * u) @ p["dw"].t() + p["db"]
+    assert off(y, y64) < 0.01
+    y64.backward(dy.double().cpu())
+    for got, want in ((x, x64), (up.weight, p["uw"]), (up.bias, p["ub"]), (down.weight, p["dw"]),
+                      (down.bias, p["db"]), (norm.pre_weight, p["nw"]), (norm.pre_bias, p["nb"])):
+        assert got.grad.dtype == torch.float32
+        assert off(got.grad, want.grad) < 0.08
