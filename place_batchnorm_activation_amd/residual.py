@@ -153,10 +153,11 @@ class ResNormFunction(torch.autograd.Function):
 
 class ResNorm(torch.nn.Module):
     """The boundary between two residual blocks: r' = r + alpha * gate * post(b) and
-    n = pre(r') (post and pre: "none", "rms" or "layer").  Norm weights and biases are
-    float32, biases with layer norms only.  gate=True learns a vector [cols]; forward's
-    own gate, [cols] or [groups, cols] for rows / groups consecutive rows each, of
-    float32 or the rows' type, takes its place; for rows [b, s, cols] also [b, 1, cols] or
+    n = pre(r') (post and pre: "none", "rms" or "layer"), in r's and b's type or what the two
+    promote to.  Norm weights and biases are float32 and read so (a parameter of another type
+    is cast in each call), biases with layer norms only.  gate=True learns a vector [cols]; forward's
+    own gate, [cols] or [groups, cols] for rows / groups consecutive rows each, takes its
+    place (of the rows' type, or cast to float32); for rows [b, s, cols] also [b, 1, cols] or
     [b, s, cols].
 
     forward(r, b=None) -> (r', n, kept): kept is what KeptLinear takes for n, None with
@@ -179,14 +180,23 @@ class ResNorm(torch.nn.Module):
         self.gate = p(torch.ones, gate)
 
     def forward(self, r, b=None, gate=None):
+        # r + b promotes as in torch; the vectors are read in float32 whatever a module-wide
+        # .to(dtype) made of them
+        if b is not None and b.dtype != r.dtype:
+            dtype = torch.promote_types(r.dtype, b.dtype)
+            r, b = r.to(dtype), b.to(dtype)
+        gate = self.gate if gate is None else gate
+        if gate is not None and gate.dtype != r.dtype:
+            gate = gate.float()
+        vec = [None if v is None else v.float() for v in (self.post_weight, self.post_bias,
+                                                          self.pre_weight, self.pre_bias)]
         r_out, n, codes, exps = ResNormFunction.apply(
-            r, b, self.gate if gate is None else gate, self.post_weight, self.post_bias,
-            self.pre_weight, self.pre_bias, self.post, self.pre, self.alpha, self.eps,
+            r, b, gate, *vec, self.post, self.pre, self.alpha, self.eps,
             self.keep if torch.is_grad_enabled() else None)
         kept = None
         if codes is not None:
-            kept = Kept(codes, exps, self.pre_weight.detach(),
-                        None if self.pre_bias is None else self.pre_bias.detach(),
+            kept = Kept(codes, exps, vec[2].detach(),
+                        None if vec[3] is None else vec[3].detach(),
                         (n.data_ptr(), n._version))
         return r_out, n, kept
 
@@ -235,21 +245,22 @@ class KeptLinearFunction(torch.autograd.Function):
 class KeptLinear(torch.nn.Linear):
     """A linear layer that keeps its input in 8 bits: its own codes, or those of `kept`
     (ResNorm's third output for this input, which must come as the norm returned it, in any
-    shape of the same rows).  Weight and input are of one type; with `kept`, an input of
-    another is cast to the weight's here."""
+    shape of the same rows).  An input of another type than the weight is cast to it (as the
+    norms of a float32 stream give to 16-bit layers)."""
 
     def forward(self, x, kept: Optional[Kept] = None):
-        if not torch.is_grad_enabled():
-            return super().forward(x)
-        if kept is None:
-            return KeptLinearFunction.apply(x, self.weight, self.bias, None, None, None, None)
-        if not kept.fits(x):
-            raise ValueError("kept (of %d rows) was made for another tensor than this input %s; "
-                             "without it the layer keeps its own codes"
-                             % (kept.codes.shape[0], tuple(x.shape)))
+        codes = (None,) * 4
+        if kept is not None and torch.is_grad_enabled():
+            if not kept.fits(x):
+                raise ValueError("kept (of %d rows) was made for another tensor than this input "
+                                 "%s; without it the layer keeps its own codes"
+                                 % (kept.codes.shape[0], tuple(x.shape)))
+            codes = kept[:4]
         if x.dtype != self.weight.dtype and not torch.is_autocast_enabled("cuda"):
             x = x.to(self.weight.dtype)
-        return KeptLinearFunction.apply(x, self.weight, self.bias, *kept[:4])
+        if not torch.is_grad_enabled():
+            return super().forward(x)
+        return KeptLinearFunction.apply(x, self.weight, self.bias, *codes)
 
 
 class GLULinearFunction(torch.autograd.Function):

@@ -273,3 +273,60 @@ def test_linear_and_glu_modules_under_autocast(low, with_kept):
                       (down.bias, p["db"]), (norm.pre_weight, p["nw"]), (norm.pre_bias, p["nb"])):
         assert got.grad.dtype == torch.float32
         assert off(got.grad, want.grad) < 0.08
+
+
+def block64(m, r, b):
+    """ResidualMLP in float64 on leaves of its parameters: (r', b', leaves)."""
+    p = {k: leaf(v) for k, v in m.named_parameters()}
+    if b is not None:
+        br = norm64(b, "rms", p["norm.post_weight"], None, m.norm.eps)
+        r = r + m.norm.alpha * (br if m.norm.gate is None else br * p["norm.gate"])
+    n = norm64(r, "rms", p["norm.pre_weight"], None, m.norm.eps)
+    g, u = (n @ p["up.weight"].t()).chunk(2, -1)
+    return r, (torch.nn.functional.silu(g) * u) @ p["down.weight"].t(), p
+
+
+@pytest.mark.parametrize("how", ["autocast", "stream", "cast"])
+def test_blocks_of_mixed_types(how):
+    """A float32 stream with 16-bit branches (under autocast, and with 16-bit layers), and a
+    block whose parameters .to() made 16-bit.  Bounds: those of 8 bits and of bf16, 5 of its
+    roundings deep."""
+    torch.manual_seed(19)
+    T, C, F, low = 200, 96, 64, torch.bfloat16
+    first, second = (ResidualMLP(C, F, gate=True, device="cuda",
+                                 dtype=low if how == "stream" else None) for _ in range(2))
+    if how == "cast":
+        first, second = first.to(low), second.to(low)
+    x = torch.randn(T, C, device="cuda", dtype=low if how == "cast" else torch.float32)
+    x.requires_grad_()
+    b0 = torch.randn(T, C, device="cuda").to(low).requires_grad_()
+    with torch.autocast("cuda", dtype=low, enabled=how == "autocast"):
+        r, b = first(x, b0)
+        r, b = second(r, b)
+    assert r.dtype == x.dtype and b.dtype == low
+    vr, vb = torch.randn(T, C, device="cuda"), torch.randn(T, C, device="cuda").to(low)
+    torch.autograd.backward([r, b], [vr.to(r.dtype), vb])
+    x64, b64 = leaf(x), leaf(b0)
+    r1, out, p1 = block64(first, x64, b64)
+    r2, out, p2 = block64(second, r1, out)
+    assert off(r, r2) < 0.02 and off(b, out) < 0.04
+    with torch.no_grad(), torch.autocast("cuda", dtype=low, enabled=how == "autocast"):
+        assert torch.equal(second(*first(x, b0))[1], b)
+    torch.autograd.backward([r2, out], [vr.to(r.dtype).double().cpu(), vb.double().cpu()])
+    for got, want in [(x, x64), (b0, b64)] + [(v, p[k]) for m, p in ((first, p1), (second, p2))
+                                              for k, v in m.named_parameters()]:
+        assert got.grad.dtype == got.dtype and off(got.grad, want.grad) < 0.1
+
+
+def test_norms_promote_and_cast():
+    """A 16-bit stream with a float32 branch, 16-bit gates with float32 rows."""
+    m = ResNorm(64, post="rms", pre="layer", keep="full", device="cuda")
+    r, b = torch.randn(8, 64, device="cuda"), torch.randn(8, 64, device="cuda")
+    r_out, n, _ = m(r.half(), b)
+    want = m(r.half().float(), b)
+    assert r_out.dtype == n.dtype == torch.float32
+    assert torch.equal(r_out, want[0]) and torch.equal(n, want[1])
+    g = torch.rand(8, 64, device="cuda").bfloat16()
+    assert torch.equal(m(r, b, g)[1], m(r, b, g.float())[1])
+    want = m(r.half(), b.half(), g.float())[1]
+    assert want.dtype == torch.float16 and torch.equal(m(r.half(), b.half(), g)[1], want)
