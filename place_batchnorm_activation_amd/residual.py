@@ -232,7 +232,7 @@ class KeptLinearFunction(torch.autograd.Function):
         if need[0]:
             dx = (dy2 @ weight).view(ctx.x_shape)
         if need[1]:
-            dw = torch.empty_like(weight)
+            dw = torch.empty(N, K, dtype=weight.dtype, device=dy.device)
             db = torch.empty(N, device=dy.device) if need[2] else None
             iabn_linear_wgrad(dy2, codes, exps, dw,
                               linear_wgrad_workspace(T, N, K, dy.dtype, dy.device), scale=scale,

@@ -330,3 +330,14 @@ def test_norms_promote_and_cast():
     assert torch.equal(m(r, b, g)[1], m(r, b, g.float())[1])
     want = m(r.half(), b.half(), g.float())[1]
     assert want.dtype == torch.float16 and torch.equal(m(r.half(), b.half(), g)[1], want)
+
+
+def test_a_weight_may_be_a_transposed_view():
+    torch.manual_seed(23)
+    lin = KeptLinear(64, 48, bias=False, device="cuda")
+    lin.weight = torch.nn.Parameter(torch.randn(64, 48, device="cuda").t())
+    x = torch.randn(30, 64, device="cuda", requires_grad=True)
+    dy = torch.randn(30, 48, device="cuda")
+    lin(x).backward(dy)
+    assert off(lin.weight.grad, dy.double().t() @ x.detach().double()) < 0.05
+    assert off(x.grad, dy.double() @ lin.weight.detach().double()) < 1e-5
