@@ -51,13 +51,14 @@ class Kept(NamedTuple):
 
 
 def _flat(t):
-    """t as rows x columns with contiguous columns (a copy only where its strides do not
-    allow it); None stays None."""
+    """t as rows x columns with contiguous columns and rows that do not overlap (a copy only
+    where its strides do not allow it); None stays None."""
     if t is None:
         return None
     if t.stride(-1) != 1 and t.shape[-1] > 1 or 0 in t.stride():
         t = t.contiguous()
-    return t.reshape(-1, t.shape[-1])
+    t = t.reshape(-1, t.shape[-1])
+    return t.contiguous() if t.stride(0) < t.shape[1] else t
 
 
 def _gate_rows(gate, shape):

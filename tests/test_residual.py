@@ -341,3 +341,20 @@ def test_a_weight_may_be_a_transposed_view():
     lin(x).backward(dy)
     assert off(lin.weight.grad, dy.double().t() @ x.detach().double()) < 0.05
     assert off(x.grad, dy.double() @ lin.weight.detach().double()) < 1e-5
+
+
+def test_overlapping_windows_are_taken():
+    """Windows of one sequence, as unfold makes them, into every module."""
+    torch.manual_seed(29)
+    x = torch.randn(100, device="cuda").unfold(0, 64, 1)
+    own = x.contiguous()
+    for m in (KeptLinear(64, 32, device="cuda"), GLULinear(32, 16, device="cuda")):
+        dy = torch.randn(len(x), m.out_features, device="cuda")
+        grads = []
+        for v in (x, own):
+            m.weight.grad = None
+            m(v).backward(dy)
+            grads.append(m.weight.grad)
+        assert torch.equal(*grads)
+    m = ResNorm(64, post="rms", pre="rms", device="cuda")
+    assert torch.equal(m(x, x)[1], m(own, own)[1])
