@@ -354,7 +354,9 @@ iabn_status iabn_forward_train_noalloc(void *x_inout,
  * cost one element-wise access a row.  rows and cols stay below 2^31; offsets are
  * 64-bit.  An output may be exactly an input of the same call (same pointer and
  * ld) unless said otherwise, and must not overlap one in any other way; two slices of
- * one buffer (equal ld, disjoint columns) do not overlap.  rows == 0 or cols == 0 is
+ * one buffer (equal ld, disjoint columns) do not overlap.  No two outputs of a call
+ * overlap, and vectors of cols, statistics, codes and workspaces overlap nothing else of
+ * it (but a vector's gradient may be exactly a vector that the call reads).  rows == 0 or cols == 0 is
  * a no-op that succeeds (gradients summed over no rows are written as zeros).
  *
  * Codes: a tensor [rows, cols] is kept as
@@ -409,7 +411,7 @@ size_t iabn_linear_wgrad_workspace_size(int64_t rows, int64_t n, int64_t k, iabn
  *   dw = (dw +) dy^T (scale * x + shift), dbias = (dbias +) sum over rows of dy,
  * the bracketed terms with accumulate != 0.  dy [rows, n] of `dtype`; dw [n, k], rows
  * lddw apart, of dw_dtype; scale, shift fp32 [k] or NULL; dbias fp32 [n] or NULL.
- * k == 0 leaves dbias alone to compute.
+ * k == 0 leaves dbias alone to compute.  dw must not overlap dy.
  * lddy and k stay below 2^26.  Sums are fp32; the products are exact (codes are exact in bf16, and f16 and f32
  * values of dy enter as two and three bf16 parts).  workspace: device, 16-byte
  * aligned, iabn_linear_wgrad_workspace_size bytes; it carries no status word. */
@@ -448,7 +450,7 @@ typedef struct iabn_resnorm {
  * post_stats, pre_stats: fp32 [rows, 2], mean and rstd, or NULL.  codes_b / exps_b:
  * codes of post's xhat (of b itself when post is none), codes_n / exps_n: codes of
  * pre's xhat; NULL when the backward will read the tensors themselves.  r_out and n
- * may each be exactly r or b, but not one another. */
+ * may each be exactly r or b, but not one another (or the gate, if it has a row for each). */
 iabn_status iabn_resnorm_forward(const iabn_resnorm *layer, const void *r, int64_t ldr,
                                  const void *b, int64_t ldb, void *r_out, int64_t ldr_out,
                                  void *n, int64_t ldn, float *post_stats, float *pre_stats,
@@ -468,7 +470,8 @@ size_t iabn_resnorm_workspace_size(int64_t rows, int64_t cols, int64_t rows_per_
  * dr may be NULL; db NULL: the branch gets no gradients (and dpost_*, dgate must be
  * NULL).  dpost_*, dpre_* fp32 [cols], dgate of gate_dtype shaped as gate; each may be
  * NULL.  b (codes_b) is needed with db for a post-norm or dgate only.  dr and db may be
- * exactly dr_out or dn, but not one another, and must not overlap what was saved.
+ * exactly dr_out or dn, but not one another, nor the gate; dgate may be exactly the gate.
+ * No output overlaps what was saved.
  * rows == 0: dpost_* and dpre_* are written as zeros; dgate has no rows and is not
  * written (a caller whose gate is one vector for every row clears it itself).
  * workspace: device, 16-byte aligned; it carries no status word.  Sums over rows are

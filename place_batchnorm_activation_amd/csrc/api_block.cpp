@@ -95,7 +95,8 @@ bool overlap(const Rows& a, const Rows& b)
 
 bool same(const Rows& a, const Rows& b)
 {
-    return a.p == b.p && (a.ld == b.ld || a.rows <= 1) && a.es == b.es && a.cols == b.cols;
+    return a.p == b.p && (a.ld == b.ld || a.rows <= 1) && a.es == b.es && a.cols == b.cols &&
+           a.rows == b.rows;
 }
 
 // An output against an input that it may replace exactly.
@@ -117,6 +118,35 @@ Rows code_rows(const void* codes, int64_t rows, int64_t cols)
 Rows exp_rows(const void* exps, int64_t rows, int64_t cols)
 {
     return Rows{exps, code_pitch(cols) / kGroup, rows, code_pitch(cols) / kGroup, 1};
+}
+
+Rows vector_row(const void* p, int64_t n, int64_t es = 4) { return Rows{p, n, 1, n, es}; }
+
+// Outputs of one call against each other.
+template <size_t N>
+iabn_status check_distinct(const Rows (&outs)[N])
+{
+    for (size_t i = 1; i < N; ++i)
+        for (size_t j = 0; j < i; ++j) IABN_TRY(check_apart(outs[i], outs[j]));
+    return IABN_OK;
+}
+
+// Outputs against inputs that they may (check_outs) or may not replace exactly.
+template <size_t N, size_t M>
+iabn_status check_outs(const Rows (&outs)[N], const Rows (&ins)[M])
+{
+    for (const Rows& o : outs)
+        if (o.p)
+            for (const Rows& i : ins) IABN_TRY(check_out(o, i));
+    return IABN_OK;
+}
+template <size_t N, size_t M>
+iabn_status check_all_apart(const Rows (&outs)[N], const Rows (&ins)[M])
+{
+    for (const Rows& o : outs)
+        if (o.p)
+            for (const Rows& i : ins) IABN_TRY(check_apart(o, i));
+    return IABN_OK;
 }
 
 iabn_status check_codes(const int8_t* codes, const uint8_t* exps)
@@ -177,6 +207,13 @@ iabn_status check_layer(const iabn_resnorm* l)
     return l->cols <= kResnormMaxC ? IABN_OK : IABN_ERR_UNSUPPORTED;
 }
 
+Rows gate_tensor(const iabn_resnorm* l, const void* p)
+{
+    const int64_t groups = l->gate && l->rows > 0 ? l->rows / l->rows_per_gate : 0;
+    return Rows{p, l->cols, groups, l->cols, esize(l->gate_dtype)};
+}
+Rows gate_tensor(const iabn_resnorm* l) { return gate_tensor(l, l->gate); }
+
 int64_t gate_rows(const iabn_resnorm* l)
 {
     return l->gate ? l->rows_per_gate : max64(1, l->rows);
@@ -195,6 +232,7 @@ iabn_status iabn_codes_pack(const void* x, int64_t ldx, int64_t rows, int64_t co
     IABN_TRY(check_rows(in));
     IABN_TRY(check_codes(codes, exps));
     IABN_TRY(check_codes_apart(codes, exps, rows, cols, in));
+    IABN_TRY(check_apart(code_rows(codes, rows, cols), exp_rows(exps, rows, cols)));
     launch_codes_pack(x, ldx, rows, cols, dtype, codes, exps, stream);
     return launched();
 }
@@ -211,6 +249,8 @@ iabn_status iabn_codes_unpack(const int8_t* codes, const uint8_t* exps, int64_t 
     IABN_TRY(check_vec(scale));
     IABN_TRY(check_vec(shift));
     IABN_TRY(check_codes_apart(codes, exps, rows, cols, out));
+    IABN_TRY(check_apart(out, vector_row(scale, cols)));
+    IABN_TRY(check_apart(out, vector_row(shift, cols)));
     launch_codes_unpack(codes, exps, rows, cols, scale, shift, y, ldy, dtype, stream);
     return launched();
 }
@@ -240,6 +280,9 @@ iabn_status iabn_glu_forward(const void* gate, int64_t ldgate, const void* up, i
         IABN_TRY(check_codes_apart(codes_gate, exps_gate, rows, cols, t));
         IABN_TRY(check_codes_apart(codes_up, exps_up, rows, cols, t));
     }
+    const Rows kept[] = {code_rows(codes_gate, rows, cols), exp_rows(exps_gate, rows, cols),
+                         code_rows(codes_up, rows, cols), exp_rows(exps_up, rows, cols)};
+    IABN_TRY(check_distinct(kept));
     const GluFwd a{gate, up, out, ldgate, ldup, ldout, codes_gate, codes_up, exps_gate, exps_up};
     launch_glu_forward(a, rows, cols, dtype, act, stream);
     return launched();
@@ -309,11 +352,16 @@ iabn_status iabn_linear_wgrad(const void* dy, int64_t lddy, iabn_dtype dtype, co
     if (rows > 0) {
         IABN_TRY(check_rows(in));
         if (k > 0) IABN_TRY(check_codes(codes, exps));
-        IABN_TRY(check_apart(out, in));
-        IABN_TRY(check_codes_apart(codes, exps, rows, k, out));
     }
     const int64_t cus = device_cus();
-    IABN_TRY(check_ws(workspace, workspace_bytes, wgrad_workspace_bytes(rows, n, k, dtype, cus)));
+    const size_t need = wgrad_workspace_bytes(rows, n, k, dtype, cus);
+    IABN_TRY(check_ws(workspace, workspace_bytes, need));
+    const Rows outs[] = {out, vector_row(dbias, n),
+                         vector_row(need ? workspace : nullptr, int64_t(need), 1)};
+    const Rows ins[] = {in, code_rows(codes, rows, k), exp_rows(exps, rows, k),
+                        vector_row(scale, k), vector_row(shift, k)};
+    IABN_TRY(check_distinct(outs));
+    IABN_TRY(check_all_apart(outs, ins));
     const WgradArgs a{dy,    lddy,       codes, exps, scale, shift, dw, lddw, dw_dtype,
                       accumulate != 0, dbias, rows, n,     k};
     launch_linear_wgrad(a, dtype, cus, workspace, stream);
@@ -342,15 +390,20 @@ iabn_status iabn_resnorm_forward(const iabn_resnorm* l, const void* r, int64_t l
     IABN_TRY(check_codes_opt(codes_b, exps_b));
     IABN_TRY(check_codes_opt(codes_n, exps_n));
     if ((codes_b && !b) || (codes_n && !n)) return IABN_ERR_INVALID_ARG;
-    for (const Rows& in : {tr, tb}) {
-        IABN_TRY(check_out(to, in));
-        IABN_TRY(check_out(tn, in));
-    }
+    const Rows tensors[] = {to, tn};
+    const Rows kept[] = {vector_row(post_stats, 2 * T), vector_row(pre_stats, 2 * T),
+                         code_rows(codes_b, T, C), exp_rows(exps_b, T, C),
+                         code_rows(codes_n, T, C), exp_rows(exps_n, T, C)};
+    const Rows ins[] = {tr, tb, gate_tensor(l)};
+    const Rows vectors[] = {vector_row(l->post_weight, C), vector_row(l->post_bias, C),
+                            vector_row(l->pre_weight, C), vector_row(l->pre_bias, C)};
     IABN_TRY(check_apart(to, tn));
-    for (const Rows& t : {tr, tb, to, tn}) {
-        IABN_TRY(check_codes_apart(codes_b, exps_b, T, C, t));
-        IABN_TRY(check_codes_apart(codes_n, exps_n, T, C, t));
-    }
+    IABN_TRY(check_distinct(kept));
+    IABN_TRY(check_outs(tensors, ins));
+    IABN_TRY(check_all_apart(tensors, vectors));
+    IABN_TRY(check_all_apart(kept, tensors));
+    IABN_TRY(check_all_apart(kept, ins));
+    IABN_TRY(check_all_apart(kept, vectors));
     ResnormFwd a{};
     a.r = r; a.b = b; a.r_out = r_out; a.n = n;
     a.ldr = ldr; a.ldb = ldb; a.ldro = ldr_out; a.ldn = ldn;
@@ -424,19 +477,34 @@ iabn_status iabn_resnorm_backward(const iabn_resnorm* l, const void* dr_out, int
         if (need_b && !codes_b && !b) return IABN_ERR_INVALID_ARG;
         if (r_out) IABN_TRY(check_rows(tro));
         if (b) IABN_TRY(check_rows(tb));
-        for (const Rows& out : {tdr, tdb}) {
-            IABN_TRY(check_out(out, tdo));
-            IABN_TRY(check_out(out, tdn));
-            IABN_TRY(check_apart(out, tro));
-            IABN_TRY(check_apart(out, tb));
-            IABN_TRY(check_codes_apart(codes_n, exps_n, T, C, out));
-            IABN_TRY(check_codes_apart(codes_b, exps_b, T, C, out));
-        }
-        IABN_TRY(check_apart(tdr, tdb));
     }
     const int64_t cus = device_cus(), R = gate_rows(l);
-    IABN_TRY(check_ws(workspace, workspace_bytes,
-                      T > 0 ? resnorm_workspace_bytes(T, C, R, cus) : 0));
+    const size_t need = T > 0 ? resnorm_workspace_bytes(T, C, R, cus) : 0;
+    IABN_TRY(check_ws(workspace, workspace_bytes, need));
+    const Rows saved[] = {tro, tb, code_rows(codes_n, T, C), exp_rows(exps_n, T, C),
+                          code_rows(codes_b, T, C), exp_rows(exps_b, T, C),
+                          vector_row(post_stats, 2 * T), vector_row(pre_stats, 2 * T)};
+    const Rows gate = gate_tensor(l), space = vector_row(need ? workspace : nullptr, int64_t(need), 1);
+    const Rows vectors[] = {vector_row(l->post_weight, C), vector_row(l->post_bias, C),
+                            vector_row(l->pre_weight, C)};
+    const Rows grads[] = {tdr, tdb}, dgates[] = {gate_tensor(l, dgate)};
+    const Rows dvectors[] = {vector_row(dpost_weight, C), vector_row(dpost_bias, C),
+                             vector_row(dpre_weight, C), vector_row(dpre_bias, C)};
+    const Rows outs[] = {tdr, tdb, dgates[0], dvectors[0], dvectors[1], dvectors[2], dvectors[3],
+                         space};
+    const Rows in[] = {tdo, tdn}, in_gate[] = {tdo, tdn, gate};
+    const Rows gate_vectors[] = {gate, vectors[0], vectors[1], vectors[2]};
+    IABN_TRY(check_distinct(outs));
+    IABN_TRY(check_all_apart(outs, saved));
+    IABN_TRY(check_outs(grads, in));
+    IABN_TRY(check_all_apart(grads, gate_vectors));
+    IABN_TRY(check_outs(dgates, in_gate));
+    IABN_TRY(check_all_apart(dgates, vectors));
+    IABN_TRY(check_outs(dvectors, vectors));       // finished by a later kernel
+    IABN_TRY(check_all_apart(dvectors, in_gate));
+    const Rows spaces[] = {space};
+    IABN_TRY(check_all_apart(spaces, in_gate));
+    IABN_TRY(check_all_apart(spaces, vectors));
     ResnormBwd a{};
     a.dr_out = dr_out; a.dn = dn; a.lddro = lddr_out; a.lddn = lddn;
     a.r_out = r_out; a.b = b; a.ldro = ldr_out; a.ldb = ldb;

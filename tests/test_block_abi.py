@@ -220,3 +220,63 @@ def test_tensors_of_no_rows_are_taken_with_any_strides():
         assert rows == 0 and cols == shape[-1] and ld >= cols
     with pytest.raises(ValueError):
         block._rows(torch.ones(()).expand(1, 40), "t")
+
+
+def vectors(**kw):
+    """A layer whose vectors lie at 20M .. 23M."""
+    l = layer(**kw)
+    l.post_weight, l.post_bias, l.pre_weight, l.pre_bias = (i * M for i in range(20, 24))
+    return l
+
+
+def test_outputs_keep_apart():
+    """Outputs over one another, over vectors, statistics, codes and the workspace.  T = 4
+    rows of 40: 320 bytes a tensor, 256 of codes, 8 of exponents, 160 a vector."""
+    assert pack(exps=2 * M + 255) == INVALID and pack(codes=3 * M, exps=3 * M) == INVALID
+    assert unpack(scale=M) == INVALID and unpack(shift=M + 316) == INVALID
+    assert unpack(T=1, dt=F32, scale=M) == INVALID
+    assert glu_f(cu=5 * M) == INVALID and glu_f(cu=5 * M + 240) == INVALID
+    assert glu_f(eu=6 * M) == INVALID and glu_f(eg=5 * M + 255) == INVALID
+    assert glu_f(eu=5 * M) == INVALID and glu_f(cu=6 * M) == INVALID
+
+    for at in (M, 2 * M, 3 * M, 4 * M):                    # dy, codes, exps, dw
+        assert wgrad(db=at) == INVALID
+    assert wgrad(db=5 * M, s=5 * M) == INVALID and wgrad(db=5 * M, t=5 * M + 40) == INVALID
+    assert wgrad(s=4 * M) == INVALID and wgrad(t=4 * M + 64) == INVALID       # dw over them
+    big = dict(T=100000, dy=1 << 40, c=1 << 41, e=1 << 42, db=1 << 44)
+    need = lib.iabn_linear_wgrad_workspace_size(100000, 64, 48, BF16)
+    for at in (1 << 40, (1 << 41) + 16, 1 << 42, 4 * M, 1 << 44, (1 << 44) - need + 16):
+        assert wgrad(ws=at, wsb=need, **big) == INVALID
+
+    kept = dict(ps=5 * M, ns=6 * M, cb=7 * M, eb=8 * M, cn=9 * M, en=10 * M)
+    for a in kept:
+        for at in [M, 2 * M, 3 * M, 4 * M, 20 * M, 21 * M, 22 * M, 23 * M] + \
+                [v for k, v in kept.items() if k != a]:
+            assert rn_f(l=vectors(), **dict(kept, **{a: at})) == INVALID, (a, at)
+    for at in (20 * M, 21 * M, 22 * M, 23 * M):
+        assert rn_f(l=vectors(), ro=at) == INVALID and rn_f(l=vectors(), n=at) == INVALID
+    gated = dict(gate=30 * M, gd=BF16)
+    assert rn_f(l=vectors(R=2, **gated), n=30 * M) == INVALID
+    assert rn_f(l=vectors(R=1, **gated), ro=30 * M + 2) == INVALID
+    assert rn_f(l=vectors(R=1, **gated), ps=30 * M) == INVALID
+
+    outs = dict(dr=7 * M, db=8 * M, dqw=12 * M, dqb=13 * M, dpw=14 * M, dpb=15 * M, dg=16 * M,
+                ws=9 * M)
+    def over(name, at, R=1, **kw):                         # noqa: E306
+        return rn_b(l=vectors(R=R, **gated), **dict(outs, **{name: at}, **kw))
+    for name in outs:
+        ours = [v for k, v in outs.items() if k != name]
+        for at in ours + [3 * M, 4 * M, 5 * M, 6 * M]:     # one another, and what was saved
+            assert over(name, at) == INVALID, (name, at)
+        if name[:2] not in ("dq", "dp"):
+            for at in (20 * M, 21 * M, 22 * M):
+                assert over(name, at) == INVALID, (name, at)
+        if name not in ("dr", "db", "dg"):
+            assert over(name, M) == INVALID and over(name, 2 * M) == INVALID
+        if name != "dg":
+            assert over(name, 30 * M) == INVALID, name
+        coded = dict(ro=None, b=None, cn=40 * M, en=41 * M, cb=42 * M, eb=43 * M)
+        for at in (40 * M, 41 * M, 42 * M, 43 * M):
+            assert over(name, at, **coded) == INVALID, (name, at)
+    assert over("dg", 30 * M, R=4, dr=30 * M) == INVALID
+    assert over("dg", 30 * M + 2) == INVALID and over("dg", M + 2) == INVALID

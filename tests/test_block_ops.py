@@ -689,6 +689,23 @@ def test_resnorm_in_place(codes):
     assert torch.equal(rs.view, want_ro) and torch.equal(bs.view, want_n)
 
 
+@pytest.mark.parametrize("codes", [False, True], ids=["full", "codes"])
+@pytest.mark.parametrize("T,C,R", [(9, 1000, 9), (8, 1001, 1), (8, 8200, 2), (4, 8200, 1),
+                                   (600, 136, 2)])
+def test_resnorm_gradients_over_what_they_are_of(T, C, R, codes):
+    """dgate over the gate and the vectors' gradients over the vectors: the same bits."""
+    gate = "vector" if R == T else "full" if R == 1 else "rows"
+    layer, gt, st, saved, outs, bufs = check_resnorm(T, C, torch.bfloat16, "layer", "layer", gate,
+                                                     R, codes)
+    dros, dns, ws = bufs[4:]
+    want = {k: v.clone() for k, v in outs.items()}
+    outs = dict(outs, dgate=gt, **{"d" + k: getattr(layer, k) for k in
+                                   ("post_weight", "post_bias", "pre_weight", "pre_bias")})
+    iabn.iabn_resnorm_backward(layer, dros.view, dns.view, ws, gate=gt, **st, **saved, **outs)
+    for k, v in outs.items():
+        assert torch.equal(v, want[k]), k
+
+
 def test_resnorm_rows_keep_to_themselves():
     """A row of zeros normalises to zeros, rows with an infinity or a NaN spoil
     themselves alone."""
