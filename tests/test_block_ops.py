@@ -400,6 +400,36 @@ def test_linear_wgrad_large_tiles_of_several_parts(T, N, K, dtype):
     test_linear_wgrad(T, N, K, dtype, "shift")
 
 
+@pytest.mark.parametrize("T,N,K,affine", [(1100, 2040, 2090, "shift"), (1152, 2053, 2048, "scale")])
+def test_linear_wgrad_large_tiles_in_parts(T, N, K, affine):
+    """256 x 256 tiles whose sum over t is cut, with ragged last tiles and columns."""
+    assert iabn.iabn_linear_wgrad_workspace_size(T, N, K, torch.bfloat16) >= 2 * N * (K + 1) * 4
+    test_linear_wgrad(T, N, K, torch.bfloat16, affine)
+
+
+@pytest.mark.parametrize("low", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("T,N,K", [(200, 129, 257), (5000, 96, 40), (70, 2048, 2048),
+                                   (1100, 2040, 2090)])
+def test_linear_wgrad_added_to_16_bits(T, N, K, dtype, low):
+    """The sum in fp32 of what was there and the product, rounded once; in one part and in
+    several."""
+    g = gen(T + K)
+    dy = torch.randn(T, N, generator=g).to(dtype).cuda()
+    codes, exps = iabn.codes_empty(T, K)
+    iabn.iabn_codes_pack(torch.randn(T, K, generator=g).cuda(), codes, exps)
+    s, t = (torch.randn(K, generator=g).cuda() for _ in range(2))
+    ws = iabn.linear_wgrad_workspace(T, N, K, dtype)
+    full = torch.empty(N, K, device="cuda")
+    iabn.iabn_linear_wgrad(dy, codes, exps, full, ws, scale=s, shift=t)
+    base = (T ** 0.5 * torch.randn(N, K, generator=g)).to(low).cuda()
+    dw = Slice(N, K, low)
+    dw.view.copy_(base)
+    iabn.iabn_linear_wgrad(dy, codes, exps, dw.view, ws, scale=s, shift=t, accumulate=True)
+    dw.check()
+    assert torch.equal(dw.view, (base.float() + full).to(low))
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 def test_linear_wgrad_of_no_rows(dtype):
     dy = torch.empty(0, 6, device="cuda", dtype=dtype)
