@@ -350,8 +350,8 @@ iabn_status iabn_forward_train_noalloc(void *x_inout,
  *
  * Tensors here are rows x cols of the storage dtype, the columns contiguous and the
  * rows `ld` elements apart (ld >= cols), so a slice of a wider buffer is taken as it
- * is.  Any alignment of one element is accepted; widths that are no multiple of 8
- * cost one element-wise access a row.  rows and cols stay below 2^31; offsets are
+ * is.  Any alignment of one element is accepted; where a width is no multiple of 8, the
+ * row's end is read by one wide access inside the row and written in smaller pieces.  rows and cols stay below 2^31; offsets are
  * 64-bit.  An output may be exactly an input of the same call (same pointer and
  * ld) unless said otherwise, and must not overlap one in any other way; two slices of
  * one buffer (equal ld, disjoint columns) do not overlap.  No two outputs of a call
@@ -412,8 +412,8 @@ size_t iabn_linear_wgrad_workspace_size(int64_t rows, int64_t n, int64_t k, iabn
  * the bracketed terms with accumulate != 0.  dy [rows, n] of `dtype`; dw [n, k], rows
  * lddw apart, of dw_dtype; scale, shift fp32 [k] or NULL; dbias fp32 [n] or NULL.
  * k == 0 leaves dbias alone to compute.  dw must not overlap dy.
- * lddy and k stay below 2^26.  Sums are fp32; the products are exact (codes are exact in bf16, and f16 and f32
- * values of dy enter as two and three bf16 parts).  workspace: device, 16-byte
+ * lddy and k stay below 2^26.  Sums are fp32; the products are exact (codes are exact in
+ * bf16, and f16 and f32 values of dy enter as two and three bf16 parts).  workspace: device, 16-byte
  * aligned, iabn_linear_wgrad_workspace_size bytes; it carries no status word. */
 iabn_status iabn_linear_wgrad(const void *dy, int64_t lddy, iabn_dtype dtype, const int8_t *codes,
                               const uint8_t *exps, const float *scale, const float *shift,

@@ -26,8 +26,10 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// 1/(1 + e^-x) and 1/(1 + e^x), its complement, to a few ulps each: both from
-// t = e^-|x| <= 1, which cannot overflow.
+// 1/(1 + e^-x) and 1/(1 + e^x), its complement: both from t = e^-|x| <= 1, which cannot
+// overflow.  Relative errors are a few ulps and, in the one that t multiplies, |x| * 2^-24
+// from the rounding of the exponent's argument; a t below 2^-126 (|x| from 87.4 on) is taken
+// as zero, so that SiLU is zero there (its value is below 1e-36).
 __device__ __forceinline__ void sigmoids(float x, float& s, float& sc)
 {
     const float t = __builtin_amdgcn_exp2f(-fabsf(x) * kLog2e);

@@ -89,7 +89,8 @@ __device__ __forceinline__ void shift_down(uint32_t (&w)[DT == kF32 ? 8 : 4], ui
 // the vector that holds the end is the row's last eight elements moved down, so
 // every load is one wide access; rows of fewer than eight columns are read one by one.
 // (The ragged form takes dozens of vector instructions a load, which bounds kernels of
-// several loads a row: 16640 x 1152 in resnorm's backward took 167 us with it.)
+// several loads a row: 16640 x 1151 in resnorm's backward took 158 us with it, and takes 78
+// where the last vector begins early instead, which is what rows of up to 4096 columns do.)
 template <int DT, bool WHOLE, class OFF = uint32_t>
 __device__ __forceinline__ Raw8<DT> load8(const char* row, uint32_t c, int C)
 {
