@@ -274,12 +274,12 @@ class ResNormSpec:
         gp, gd, per = None, 0, 1
         if gate is not None:
             groups = gate.shape[0] if gate.dim() == 2 else 1
-            if groups < 1 or T % groups:
+            if groups > 0 and T % groups or groups < 1 and T > 0:
                 raise ValueError("gate: %d rows do not divide %d" % (groups, T))
             if gate.dtype != torch.float32 and gate.dtype != ref.dtype:
                 raise TypeError("gate is %s, expected float32 or %s" % (gate.dtype, ref.dtype))
             gp = _flat(gate, "gate", groups * C, gate.dtype, dev)
-            gd, per = _dtype_code(gate), max(1, T // groups)
+            gd, per = _dtype_code(gate), max(1, T // max(1, groups))
         return _Layer(T, C, _dtype_code(ref), self.post, self.pre,
                       _cols(self.post_weight, "post_weight", C, dev),
                       _cols(self.post_bias, "post_bias", C, dev),

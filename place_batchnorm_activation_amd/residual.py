@@ -140,7 +140,7 @@ class ResNormFunction(torch.autograd.Function):
         dgate = torch.empty_like(gate) if need[2] and branch and gate is not None else None
         saved = dict(r_out=r_out, b=b) if cn is None and cb is None else \
             dict(codes_n=cn, exps_n=en, codes_b=cb, exps_b=eb)
-        groups = 1 if gate is None else gate.shape[0]
+        groups = 1 if gate is None else max(1, gate.shape[0])
         ws = resnorm_workspace(T, C, max(1, T // groups), ref.device)
         iabn_resnorm_backward(layer, dr_out, dn, ws, post_stats=post_stats, pre_stats=pre_stats,
                               gate=gate, dr=dr, db=db, dpost_weight=dpw, dpost_bias=dpb,
@@ -156,10 +156,10 @@ class ResNorm(torch.nn.Module):
     """The boundary between two residual blocks: r' = r + alpha * gate * post(b) and
     n = pre(r') (post and pre: "none", "rms" or "layer"), in r's and b's type or what the two
     promote to.  Norm weights and biases are float32 and read so (a parameter of another type
-    is cast in each call), biases with layer norms only.  gate=True learns a vector [cols]; forward's
-    own gate, [cols] or [groups, cols] for rows / groups consecutive rows each, takes its
-    place (of the rows' type, or cast to float32); for rows [b, s, cols] also [b, 1, cols] or
-    [b, s, cols].
+    is cast in each call), biases with layer norms only.  gate=True learns a vector [cols];
+    forward's own gate, [cols] or [groups, cols] for rows / groups consecutive rows each, takes
+    its place (of the rows' type, or cast to float32); for rows [b, s, cols] also [b, 1, cols]
+    or [b, s, cols].
 
     forward(r, b=None) -> (r', n, kept): kept is what KeptLinear takes for n, None with
     keep="full" (the backward then reads r' and b themselves), in inference and without a

@@ -358,3 +358,18 @@ def test_overlapping_windows_are_taken():
         assert torch.equal(*grads)
     m = ResNorm(64, post="rms", pre="rms", device="cuda")
     assert torch.equal(m(x, x)[1], m(own, own)[1])
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (0, 1, 64), (0, 5, 64)])
+def test_gates_of_an_empty_batch(shape):
+    """A gate for each of no samples, or of their rows."""
+    m = ResNorm(64, post="rms", pre="layer", device="cuda")
+    r, b = (torch.empty(0, 5, 64, device="cuda", requires_grad=True) for _ in range(2))
+    g = torch.empty(shape, device="cuda", requires_grad=True)
+    r_out, n, _ = m(r, b, g)
+    (r_out.sum() + n.sum()).backward()
+    assert r_out.shape == n.shape == r.grad.shape == (0, 5, 64) and g.grad.shape == shape
+    for p in m.parameters():
+        assert float(p.grad.abs().max()) == 0.0
+    with pytest.raises(ValueError):
+        m(torch.ones(2, 64, device="cuda"), torch.ones(2, 64, device="cuda"), g)
