@@ -487,6 +487,142 @@ iabn_status iabn_resnorm_backward(const iabn_resnorm *layer, const void *dr_out,
                                   void *dgate, void *workspace, size_t workspace_bytes,
                                   hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention, rotary positions and group norm: what a block of an image, video or
+ * language model needs next to the norms and gated units above.
+ *
+ * A tensor of heads [batch, rows, heads, head_dim]: element (b, r, h, d) lies at
+ * data + b*batch + r*row + h*head + d (strides in elements, not negative; any alignment
+ * of one element).  Slices of a wider projection and layouts with heads before rows
+ * are taken as they lie. */
+typedef struct iabn_heads {
+    void *data;
+    int64_t batch, row, head;
+} iabn_heads;
+
+/* One attention problem: batch sequences of q_len queries and k_len keys, heads query heads
+ * (a multiple of kv_heads: query head h goes with key head h / (heads / kv_heads)) of
+ * head_dim elements, a multiple of 8 up to 128.
+ *
+ * Query i of a sequence of Lq queries and Lk keys sees the keys j < Lk with
+ *   i + (Lk - Lq) - left <= j <= i + (Lk - Lq) + right,
+ * left or right < 0: unbounded on that side.  right = 0 is causal with the last query at
+ * the last key (new tokens behind a cache).  A query that sees no key gets out = 0,
+ * lse = -inf, and has no part in any gradient.  Hidden keys take no part, but a NaN or an infinity in k or v of a key
+ * that a neighbouring query sees may reach queries that do not see it (0 * NaN); keys that lie
+ * behind a sequence's length are not read.
+ *
+ * Lengths: q_lens, k_lens int32 [batch] on the device, or NULL (the whole length).  Rows of
+ * out and of gradients behind a length are written as zeros (lse: -inf).
+ * Packed: q_starts, k_starts int32 [batch + 1] on the device: sequence b is rows
+ * starts[b] .. starts[b+1] - 1 of a tensor of q_rows (k_rows) rows, the batch stride is not
+ * used, and q_len (k_len) is the most rows that a sequence has; rows in no sequence are
+ * left as they were.  Either side may be packed, padded or full by itself.  Values outside
+ * the tensors are cut to them.
+ *
+ * q_len and k_len times heads / kv_heads stay at or below 2^29. scale > 0. */
+typedef struct iabn_attention {
+    int64_t batch, heads, kv_heads, head_dim, q_len, k_len;
+    iabn_dtype dtype;
+    float scale;
+    int64_t left, right;
+    const int32_t *q_starts, *k_starts;
+    int64_t q_rows, k_rows;
+    const int32_t *q_lens, *k_lens;
+} iabn_attention;
+
+/* Bytes of workspace of iabn_attention_forward (backward == 0) or _backward; 0 when it needs
+ * none (and for invalid arguments).  Depends on the arguments and the device's CU count,
+ * not on lengths or starts. */
+size_t iabn_attention_workspace_size(const iabn_attention *problem, int backward);
+
+/* out = softmax(scale * q k^T) v over the visible keys; lse: fp32 [batch, heads, q_len]
+ * (packed queries: [heads, q_rows]), log of the sum of exp(scale * q k^T), or NULL.  out
+ * overlaps none of q, k, v.  Softmax statistics and sums are fp32; for 16-bit types the
+ * probabilities are rounded to them before they meet v.  workspace: device, 16-byte aligned,
+ * iabn_attention_workspace_size(problem, 0) bytes; it carries no status word. */
+iabn_status iabn_attention_forward(const iabn_attention *problem, const iabn_heads *q,
+                                   const iabn_heads *k, const iabn_heads *v,
+                                   const iabn_heads *out, float *lse, void *workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of the forward from its out and lse, the probabilities recomputed:
+ *   P = exp(scale * q k^T - lse), delta = sum_d dout * out, dS = P * (dout v^T - delta),
+ *   dv = P^T dout, dq = scale * dS k, dk = scale * dS^T q,
+ * dk and dv summed over the query heads of a key head.  dq, dk and dv overlap nothing else
+ * of the call (slices of one buffer do not overlap).  For 16-bit types P and dS are rounded to them before their products
+ * (float16: raised by powers of two first, so that small gradients keep their digits). */
+iabn_status iabn_attention_backward(const iabn_attention *problem, const iabn_heads *q,
+                                    const iabn_heads *k, const iabn_heads *v,
+                                    const iabn_heads *out, const float *lse,
+                                    const iabn_heads *dout, const iabn_heads *dq,
+                                    const iabn_heads *dk, const iabn_heads *dv, void *workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+
+typedef enum iabn_pos { IABN_POS_I32 = 0, IABN_POS_I64 = 1, IABN_POS_F32 = 2 } iabn_pos;
+
+/* Rotary positions with `axes` coordinates a token: pair p (of `pairs`) of every head turns by
+ * angle = position[axis[p]] * inv_freq[p], (a, b) -> (a cos - b sin, b cos + a sin), a and b
+ * the head's elements p and pairs + p, or with `interleaved` 2p and 2p + 1; elements from
+ * 2*pairs on are copied.  inv_freq float64 [pairs] (radians a step) and axis int32 [pairs] (NULL: all
+ * 0; values are cut to [0, axes)) on the device.  positions: coordinate c of token (b, r)
+ * at b*pos_batch + r*pos_row + c, of pos_type; pos_batch 0 shares them among the batch.
+ * Angles are formed in float64. */
+typedef struct iabn_rotary_spec {
+    int64_t batch, rows, head_dim, pairs, axes;
+    iabn_dtype dtype;
+    int interleaved;
+    const double *inv_freq;
+    const int32_t *axis;
+    const void *positions;
+    iabn_pos pos_type;
+    int64_t pos_batch, pos_row;
+} iabn_rotary_spec;
+
+/* q_out = turned q, and k_out = turned k where k_heads > 0 (k, k_out may else be NULL).  With
+ * `inverse` by the negative angles: the gradient.  q_out may be exactly q, k_out exactly k. */
+iabn_status iabn_rotary(const iabn_rotary_spec *spec, const iabn_heads *q, int64_t q_heads,
+                        const iabn_heads *q_out, const iabn_heads *k, int64_t k_heads,
+                        const iabn_heads *k_out, int inverse, hipStream_t stream);
+
+/* Activations of the group norm: those of the gated unit, identity, and leaky ReLU with slope
+ * act_param for z < 0 (0: ReLU). */
+typedef enum iabn_gn_act {
+    IABN_GN_SILU = 0, IABN_GN_GELU = 1, IABN_GN_GELU_TANH = 2, IABN_GN_IDENTITY = 3,
+    IABN_GN_LEAKY_RELU = 4
+} iabn_gn_act;
+
+/* Group norm with an activation, channels last: n samples of hw rows of c channels, rows ld
+ * elements apart (ld >= c); groups of c / groups neighbouring channels, groups a divisor of c. */
+typedef struct iabn_group_norm {
+    int64_t n, hw, c, groups;
+    iabn_dtype dtype;
+    const float *weight, *bias;          /* fp32 [c], NULL: 1 and 0 */
+    iabn_gn_act act;
+    float act_param, eps;
+} iabn_group_norm;
+
+/* Bytes of workspace of both passes (0 for an empty problem and invalid arguments). */
+size_t iabn_group_norm_workspace_size(const iabn_group_norm *layer);
+
+/* y = act(xhat * weight + bias), xhat = (x - mean) * rstd over a sample's group,
+ * rstd = 1 / sqrt(biased variance + eps).  stats: fp32 [n, groups, 2], mean and rstd, or NULL.
+ * y may be exactly x.  Rows n*hw below 2^31, c below 2^26.  workspace: device, 16-byte aligned; it carries no
+ * status word. */
+iabn_status iabn_group_norm_forward(const iabn_group_norm *layer, const void *x, int64_t ldx,
+                                    void *y, int64_t ldy, float *stats, void *workspace,
+                                    size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients from x and the forward's stats: dz = act'(z) * dy, dbias_c = sum dz,
+ * dweight_c = sum dz * xhat, dx = rstd * (weight dz - <weight dz> - xhat <weight dz xhat>),
+ * <.> the mean over the group.  dx, dweight and dbias may each be NULL; dx may be exactly
+ * dy or x, dweight exactly weight and dbias exactly bias.  n == 0 or hw == 0: dweight and dbias
+ * are written as zeros. */
+iabn_status iabn_group_norm_backward(const iabn_group_norm *layer, const void *x, int64_t ldx,
+                                     const void *dy, int64_t lddy, void *dx, int64_t lddx,
+                                     const float *stats, float *dweight, float *dbias,
+                                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Describes, as a short text, the kernels that iabn_forward_train and
  * iabn_backward launch for this problem when every tensor pointer is 16-byte
  * aligned (aligned16 != 0) or not, e.g.

@@ -333,3 +333,9 @@ from .block import (ResNormSpec, code_cols, codes_empty, iabn_codes_pack,  # noq
                     iabn_linear_wgrad_workspace_size, iabn_resnorm_backward,
                     iabn_resnorm_forward, iabn_resnorm_workspace_size, linear_wgrad_workspace,
                     resnorm_workspace)
+
+# attention, rotary positions and group norm (heads.py, likewise)
+from .heads import (AttentionSpec, RotarySpec, attention_lse, attention_workspace,  # noqa: E402,F401
+                    group_norm_workspace, iabn_attention_backward, iabn_attention_forward,
+                    iabn_attention_workspace_size, iabn_group_norm_backward,
+                    iabn_group_norm_forward, iabn_group_norm_workspace_size, iabn_rotary)

@@ -16,7 +16,8 @@ LIB = os.path.join(HERE, "libiabn.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["fwd.hip", "bwd.hip", "fused_nchw.hip", "fused_nhwc.hip", "ckpt.hip", "noalloc.hip", "api.cpp",
-           "codes.hip", "glu.hip", "wgrad.hip", "resnorm.hip", "api_block.cpp"]
+           "codes.hip", "glu.hip", "wgrad.hip", "resnorm.hip", "api_block.cpp",
+           "attn_fwd.hip", "attn_bwd.hip", "rotary.hip", "api_attn.cpp", "groupnorm.hip", "api_gnorm.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

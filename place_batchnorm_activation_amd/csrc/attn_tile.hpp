@@ -1,0 +1,340 @@
+// Device helpers of the attention kernels: sequences, tiles of rows in LDS and the
+// fragments that the matrix instructions take from them.
+//
+// Products are 32 x 32 x 16 on the matrix units: a lane holds 8 consecutive elements of
+// the summed index of one row (operand A, row lane % 32) or column (operand B), those of
+// half lane / 32, and of the result the elements of column lane % 32 in rows
+// 8 * (r / 4) + 4 * (lane / 32) + r % 4, r = 0 .. 15.  Scores are formed transposed
+// (keys x queries, or queries x keys where a wave owns keys), so that a lane's results
+// belong to one query (key): its statistics are scalars of the lane, and the results,
+// converted, are as they lie the operand B of the next product, whose summed index is
+// what the rows were.  That product's operand A, the transpose of a tile that lies in LDS row by
+// row, comes through the transposing LDS reads.
+//
+// float32 takes the same fragments of 8 elements through eight 32 x 32 x 2 instructions.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "attn.hpp"
+#include "rows.hpp"
+
+namespace iabn {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2_any4_t __attribute__((ext_vector_type(2), aligned(2)));
+
+constexpr float kLog2eA = 1.44269504088896341f;
+constexpr float kLn2A = 0.693147180559945309f;
+
+// A problem's sequence: rows of q and k, and where they begin.  Starts and lengths are
+// the caller's device data: whatever they hold, no row outside the tensors results.
+struct Sequence {
+    int64_t q0, k0;
+    int lq, lk;
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi)
+{
+    return v < lo ? lo : v > hi ? hi : v;
+}
+
+__device__ __forceinline__ void sequence_side(const int32_t* starts, const int32_t* lens, int b,
+                                              int64_t rows, int most, int64_t& first, int& len)
+{
+    first = 0;
+    len = most;
+    if (starts) {
+        first = clamp64(starts[b], 0, rows);
+        const int64_t n = clamp64(int64_t(starts[b + 1]) - first, 0, most);
+        len = int(dmin(n, rows - first));
+    } else if (lens) {
+        len = int(clamp64(lens[b], 0, most));
+    }
+}
+
+__device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int b)
+{
+    Sequence s;
+    sequence_side(a.q_starts, a.q_lens, b, a.q_rows, a.Sq, s.q0, s.lq);
+    sequence_side(a.k_starts, a.k_lens, b, a.k_rows, a.Sk, s.k0, s.lk);
+    return s;
+}
+
+// Keys [lo, hi) that query token t sees.
+__device__ __forceinline__ void visible(const AttnArgs& a, const Sequence& s, int t, int& lo,
+                                        int& hi)
+{
+    const int at = t + s.lk - s.lq;
+    lo = max(0, at - a.left);
+    hi = min(s.lk, at + a.right + 1);
+}
+
+// First address of head h of sequence b.
+__device__ __forceinline__ char* head_of(const Heads& t, bool packed, int b, int64_t first, int h,
+                                         int es)
+{
+    return t.p + ((packed ? 0 : b * t.batch) + first * t.row + h * t.head) * es;
+}
+
+// ---------------------------------------------------------------------------
+// fragments and products
+
+template <int DT>
+struct Frag {
+    uint32_t w[DT == kF32 ? 8 : 4];
+};
+
+template <int DT>
+__device__ __forceinline__ f32x16_t mma(const Frag<DT>& a, const Frag<DT>& b, f32x16_t c)
+{
+    if constexpr (DT == kBF16) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    } else if constexpr (DT == kF16) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
+                                                      __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.w[i]),
+                                                     __uint_as_float(b.w[i]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void zero(Frag<DT>& f)
+{
+#pragma unroll
+    for (uint32_t& w : f.w) w = 0u;
+}
+
+__device__ __forceinline__ void zero(f32x16_t& v)
+{
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v[r] = 0.f;
+}
+
+// Results 8i .. 8i + 7 of a product, as the next one's operand B (rounded to DT).
+template <int DT>
+__device__ __forceinline__ Frag<DT> results(const f32x16_t& v, int i)
+{
+    Frag<DT> f;
+#pragma unroll
+    for (int j = 0; j < (DT == kF32 ? 8 : 4); ++j) {
+        if constexpr (DT == kF32) f.w[j] = __float_as_uint(v[8 * i + j]);
+        else f.w[j] = pack2<DT>(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+    }
+    return f;
+}
+
+// Eight elements of a row from global memory (any alignment of one element).
+template <int DT>
+__device__ __forceinline__ Frag<DT> frag_of(const char* p)
+{
+    Frag<DT> f;
+#pragma unroll
+    for (int i = 0; i < (DT == kF32 ? 2 : 1); ++i) {
+        const uint4 q = load16_any(p + 16 * i);
+        f.w[4 * i] = q.x; f.w[4 * i + 1] = q.y; f.w[4 * i + 2] = q.z; f.w[4 * i + 3] = q.w;
+    }
+    return f;
+}
+
+template <int DT>
+__device__ __forceinline__ float frag_value(const Frag<DT>& f, int i)
+{
+    if constexpr (DT == kF32) return __uint_as_float(f.w[i]);
+    else return unpack1<DT>(uint16_t(f.w[i / 2] >> (16 * (i & 1))));
+}
+
+// The largest, and the sum, of both halves' values of a column, in both.
+__device__ __forceinline__ float both_max(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float both_sum(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---------------------------------------------------------------------------
+// tiles of rows in LDS
+
+// DP: the head's elements as the kernel counts them, a multiple of 32 (those past D are
+// zeros).  Rows are NC 16-byte chunks apart, a power of two; chunk c of row r lies at
+// place c XOR a mix of r, so that
+//   - 16 lanes that read one chunk of 16 neighbouring rows meet 16 different bank quads,
+//   - 32 lanes that read 64 bytes of each of 4 neighbouring rows (a transposing read)
+//     cover all 64 banks.
+template <int DT, int DP>
+struct TileShape {
+    static constexpr int ES = DT == kF32 ? 4 : 2;
+    static constexpr int E = 16 / ES;                            // elements of a chunk
+    static constexpr int USED = DP / E;                          // chunks of a row
+    static constexpr int NC = (DP <= 64 ? 64 : 128) / E;
+    static_assert(DP % 32 == 0 && DP <= 128, "head sizes");
+
+    static __device__ __forceinline__ int slot(int r, int c)
+    {
+        if constexpr (NC == 8) return r * 8 + (c ^ (((r & 2) << 1) | ((r >> 2) & 3)));
+        else if constexpr (DT == kF32) return r * NC + (c ^ (((r & 7) << 1) | ((r >> 3) & 1)));
+        else return r * NC + (c ^ (((r & 3) << 2) | ((r >> 2) & 3)));
+    }
+};
+
+// ROWS rows on their way from global memory to LDS through NT threads' registers.
+template <int DT, int DP, int ROWS, int NT>
+struct TileLoad {
+    using S = TileShape<DT, DP>;
+    static constexpr int PER = NT / S::NC;                       // rows a pass
+    static constexpr int N = ROWS / PER;
+    static_assert(NT % S::NC == 0 && ROWS % PER == 0, "threads for a tile");
+    uint4 q[N];
+
+    // rows first .. first + ROWS - 1, row r at at(r); those from `end` on, and elements from
+    // D on, are zeros
+    template <class At>
+    __device__ __forceinline__ void load_at(At&& at, int first, int end, int D)
+    {
+        const int c = threadIdx.x % S::NC, r = first + int(threadIdx.x) / S::NC;
+        const bool in = c * S::E < D;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            q[i] = make_uint4(0, 0, 0, 0);
+            if (in && r + i * PER < end) q[i] = load16_any(at(r + i * PER) + c * 16);
+        }
+    }
+    // rows `pitch` bytes apart
+    __device__ __forceinline__ void load(const char* head, int64_t pitch, int first, int end,
+                                         int D)
+    {
+        load_at([&](int r) { return head + int64_t(r) * pitch; }, first, end, D);
+    }
+    __device__ __forceinline__ void store(uint4* tile) const
+    {
+        const int c = threadIdx.x % S::NC, r = int(threadIdx.x) / S::NC;
+        if (S::USED < S::NC && c >= S::USED) return;
+#pragma unroll
+        for (int i = 0; i < N; ++i) tile[S::slot(r + i * PER, c)] = q[i];
+    }
+};
+
+// Operand A of rows row0 .. row0 + 31 at elements 16 * ks .. 16 * ks + 15.
+template <int DT, int DP>
+__device__ __forceinline__ Frag<DT> row_frag(const uint4* tile, int row0, int ks)
+{
+    using S = TileShape<DT, DP>;
+    const int lane = threadIdx.x % 64, r = row0 + lane % 32, h = lane / 32;
+    Frag<DT> f;
+#pragma unroll
+    for (int i = 0; i < (DT == kF32 ? 2 : 1); ++i) {
+        const uint4 q = tile[S::slot(r, DT == kF32 ? 4 * ks + 2 * h + i : 2 * ks + h)];
+        f.w[4 * i] = q.x; f.w[4 * i + 1] = q.y; f.w[4 * i + 2] = q.z; f.w[4 * i + 3] = q.w;
+    }
+    return f;
+}
+
+// Operand A of the transposed tile: elements 32 * db .. 32 * db + 31, summed over the 16
+// rows from row0 in the order in which a lane holds a product's results: element i of half
+// h is row row0 + 8 * (i / 4) + 4 * h + i % 4.
+template <int DT, int DP>
+__device__ __forceinline__ Frag<DT> col_frag(const uint4* tile, int row0, int db)
+{
+    using S = TileShape<DT, DP>;
+    const int lane = threadIdx.x % 64, h = lane / 32;
+    Frag<DT> f;
+    if constexpr (DT == kF32) {
+        const int d = 32 * db + lane % 32;
+        const float* t = reinterpret_cast<const float*>(tile);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = row0 + 8 * (i / 4) + 4 * h + i % 4;
+            f.w[i] = __float_as_uint(t[S::slot(r, d / 4) * 4 + d % 4]);
+        }
+    } else {
+        // 16 lanes read 16 columns of 4 rows, 4 columns each, and get one column's 4 rows
+        const int l = lane % 16, col = 32 * db + (lane & 16) + 4 * (l % 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = row0 + 8 * j + 4 * h + l / 4;
+            const char* p = reinterpret_cast<const char*>(tile + S::slot(r, col / 8)) +
+                            (col & 4) * 2;
+            const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4_t*)p);
+            const uint2 u = __builtin_bit_cast(uint2, v);
+            f.w[2 * j] = u.x;
+            f.w[2 * j + 1] = u.y;
+        }
+    }
+    return f;
+}
+
+// Four consecutive elements d .. d + 3 of a row, rounded.
+template <int DT>
+__device__ __forceinline__ void store4(char* row, int d, float a, float b, float c, float e)
+{
+    if constexpr (DT == kF32) {
+        const u32x4_any_t w = {__float_as_uint(a), __float_as_uint(b), __float_as_uint(c),
+                               __float_as_uint(e)};
+        *reinterpret_cast<u32x4_any_t*>(row + 4 * d) = w;
+    } else {
+        const u32x2_any_t w = {pack2<DT>(a, b), pack2<DT>(c, e)};
+        *reinterpret_cast<u32x2_any_t*>(row + 2 * d) = w;
+    }
+}
+
+// Rows of a key head's group (attn.hpp) in global memory.
+struct GroupRows {
+    const char* p;                    // the first query head of the group
+    int64_t row, head;                // bytes
+    FastDiv group;
+    int G;
+
+    __device__ __forceinline__ const char* operator()(int r) const
+    {
+        const int t = int(fast_div(uint32_t(r), group));
+        return p + int64_t(t) * row + int64_t(r - t * G) * head;
+    }
+};
+
+__device__ __forceinline__ GroupRows group_rows(const AttnArgs& a, const Heads& t, int b,
+                                                const Sequence& s, int hk, int es)
+{
+    return GroupRows{head_of(t, a.q_starts != nullptr, b, s.q0, hk * a.G, es), t.row * es,
+                     t.head * es, a.group, a.G};
+}
+
+// The place of a row's log-sum-exp.
+__device__ __forceinline__ int64_t lse_index(const AttnArgs& a, const Sequence& s, int b, int hq,
+                                             int tok)
+{
+    return a.q_starts ? int64_t(hq) * a.q_rows + s.q0 + tok
+                      : (int64_t(b) * a.KV * a.G + hq) * a.Sq + tok;
+}
+
+// Which workgroup of a key head, and which key head, blockIdx.x stands for: consecutive
+// workgroups go to the 8 XCDs in turn, so where the heads divide by 8 all workgroups of
+// one run on one XCD, whose L2 then holds its keys once.
+__device__ __forceinline__ void head_and_tile(uint32_t heads, uint32_t tiles, uint32_t& head,
+                                              uint32_t& tile)
+{
+    const uint32_t b = blockIdx.x;
+    if (heads % 8 == 0) {
+        head = b % 8 + 8 * (b / 8 / tiles);
+        tile = b / 8 % tiles;
+    } else {
+        head = b / tiles;
+        tile = b % tiles;
+    }
+}
+
+}  // namespace iabn

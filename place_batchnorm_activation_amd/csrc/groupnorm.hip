@@ -1,0 +1,533 @@
+// Group norm with an activation, channels last: a sample's rows (pixels) of C channels,
+// groups of C / G neighbouring ones.
+//
+//   xhat = (x - mean) * rstd over the pixels and channels of a group of a sample,
+//   z = w_c xhat + b_c,  y = act(z);
+//   dz = act'(z) dy,  dw_c = sum dz xhat,  db_c = sum dz,
+//   dx = rstd (w dz - <w dz> - xhat <w dz xhat>),  <.> the mean over the group.
+//
+// Bound by memory.  A thread keeps 8 channels and walks rows, so that what belongs to a
+// channel (weight, statistics, sums) stays in its registers and every access is a row's
+// run of 16 bytes a lane, whatever the groups' width.
+//
+// Large maps: sums over runs of rows, a workgroup each, for each channel; a small kernel
+// finishes them for the groups; an elementwise pass.  Two reads of x (three passes over
+// x and dy in the backward), the second of which the 256 MB cache serves where the map
+// fits it.  Small maps: one workgroup a group and sample reads it twice, the second time
+// from its L2, in one launch.
+//
+// Statistics: a thread's rows about its own first value in fp32, joined as mean and sum of
+// squares about it, the mean from the chunk's first value on (a mean far from zero takes no digits from the variance), the chunks in
+// fp64.  Gradients' sums: fp32 within a workgroup, fp64 over them.  All in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include "acts.hpp"
+#include "gnorm.hpp"
+#include "rows.hpp"
+
+namespace iabn {
+
+namespace {
+
+constexpr int kGnThreads = 256;
+constexpr int kBlockC = kGnThreads * kRowV;        // channels of a workgroup
+
+template <int ACT>
+__device__ __forceinline__ void gn_act(float z, float param, float& f, float& d)
+{
+    if constexpr (ACT == kGnIdentity) {
+        f = z;
+        d = 1.f;
+    } else if constexpr (ACT == kGnLeaky) {
+        f = z >= 0.f ? z : z * param;
+        if (z != z) f = z;
+        d = z >= 0.f ? 1.f : param;
+    } else {
+        glu_act<ACT>(z, f, d);
+    }
+}
+
+// How a workgroup of rows lies over the tensor.
+struct GnGrid {
+    int64_t chunk;                    // rows of a workgroup
+    int chunks, blocks;               // workgroups of a sample: along its rows, its channels
+    FastDiv width;                    // by C / G
+    int64_t n0;                       // first sample of the launch
+};
+
+// A thread's place: 8 channels from c on, rows first, first + step, ... of its chunk.
+struct Place {
+    int c, nv;                        // nv: valid channels, 0 none
+    int lane, lanes;                  // row lanes of the workgroup
+    int64_t row0, row1;
+};
+
+__device__ __forceinline__ Place place_of(const GnArgs& a, const GnGrid& gr)
+{
+    Place p;
+    const int c0 = int(blockIdx.z) * kBlockC;
+    const int vecs = (min(int(a.C) - c0, kBlockC) + kRowV - 1) / kRowV;
+    p.lanes = kGnThreads / vecs;
+    p.lane = int(threadIdx.x) / vecs;
+    p.c = c0 + (int(threadIdx.x) - p.lane * vecs) * kRowV;
+    p.nv = p.lane < p.lanes ? valid8(p.c, int(a.C)) : 0;
+    p.row0 = int64_t(blockIdx.x) * gr.chunk;
+    p.row1 = dmin(p.row0 + gr.chunk, a.HW);
+    return p;
+}
+
+template <int DT>
+__device__ __forceinline__ const char* sample_row(const void* t, int64_t ld, const GnArgs& a,
+                                                  int64_t n, int64_t row)
+{
+    return row_ptr<DT>(t, n * a.HW + row, ld);
+}
+
+// What a channel's elementwise pass needs.
+struct Channel {
+    float mean[8], rstd[8], w[8], b[8];
+    int group[8];
+};
+
+template <bool WHOLE>
+__device__ __forceinline__ void load_channels(const GnArgs& a, FastDiv width, int64_t n, int c,
+                                              int nv, Channel& ch)
+{
+    load_cols<WHOLE>(a.weight, uint32_t(c), int(a.C), 1.f, ch.w);
+    load_cols<WHOLE>(a.bias, uint32_t(c), int(a.C), 0.f, ch.b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        ch.group[e] = e < nv ? int(fast_div(uint32_t(c + e), width)) : int(a.G) - 1;
+        const float2 st = reinterpret_cast<const float2*>(a.stats)[n * a.G + ch.group[e]];
+        ch.mean[e] = st.x;
+        ch.rstd[e] = st.y;
+    }
+}
+
+// The row lanes' pairs of each channel, joined in their order: out[c] of the block.
+template <class Join>
+__device__ __forceinline__ void join_lanes(const Place& p, const float (&s)[8],
+                                           const float (&t)[8], float2* out, int C, Join&& join)
+{
+    __shared__ float2 all[kGnThreads * kRowV];
+    const int c0 = int(blockIdx.z) * kBlockC, cols = min(C - c0, kBlockC);
+    const int wide = (cols + kRowV - 1) / kRowV * kRowV;          // lanes * wide <= 256 * 8
+    if (p.nv > 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) all[p.lane * wide + p.c - c0 + e] = make_float2(s[e], t[e]);
+    }
+    __syncthreads();
+    for (int c = int(threadIdx.x); c < cols; c += kGnThreads) {
+        float2 v = all[c];
+        for (int l = 1; l < p.lanes; ++l) join(v, all[l * wide + c], l);
+        out[c0 + c] = v;
+    }
+}
+
+// part[n][chunk][c]: the mean of the chunk's rows, less its first, and the sum of squares about
+// the mean.
+template <int DT, bool WHOLE>
+__global__ __launch_bounds__(kGnThreads) void k_gn_stats(GnArgs a, GnGrid gr, float2* part)
+{
+    const int64_t n = gr.n0 + blockIdx.y;
+    const Place p = place_of(a, gr);
+    const int C = int(a.C);
+    const int rows = int(p.row1 - p.row0);
+    auto count = [&](int lane) { return lane < rows ? (rows - lane + p.lanes - 1) / p.lanes : 0; };
+    float s[8] = {}, t[8] = {};
+    if (p.nv > 0 && p.lane < rows) {
+        // sums about the thread's first value, which take no digits from the squares; means
+        // from the chunk's first value, which keeps those of means far from zero
+        float pivot[8], first[8];
+        int64_t row = p.row0 + p.lane;
+        widen8<DT>(load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, p.row0), uint32_t(p.c), C), first);
+        widen8<DT>(load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row), uint32_t(p.c), C), pivot);
+        row += p.lanes;
+        auto add = [&](const Raw8<DT>& r) {
+            float v[8];
+            widen8<DT>(r, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = v[e] - pivot[e];
+                s[e] += d;
+                t[e] = fmaf(d, d, t[e]);
+            }
+        };
+        for (; row + 3 * p.lanes < p.row1; row += 4 * p.lanes) {
+            Raw8<DT> r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                r[u] = load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row + u * p.lanes),
+                                        uint32_t(p.c), C);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(r[u]);
+        }
+        for (; row < p.row1; row += p.lanes)
+            add(load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row), uint32_t(p.c), C));
+        const float inv = 1.f / float(count(p.lane));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float q = fmaf(-s[e] * inv, s[e], t[e]);
+            t[e] = q < 0.f ? 0.f : q;
+            s[e] = fmaf(s[e], inv, pivot[e] - first[e]);
+        }
+    }
+    join_lanes(p, s, t, part + (n * gr.chunks + blockIdx.x) * a.C, C,
+               [&](float2& v, const float2& o, int l) {
+        const int nb = count(l);
+        if (nb == 0) return;
+        // rows of the lanes before: whole rounds of them, and of the last round min(l, rest)
+        const int na = rows / p.lanes * l + min(l, rows % p.lanes);
+        const float f = float(nb) / float(na + nb), d = o.x - v.x;
+        v.x = fmaf(d, f, v.x);
+        v.y += o.y + d * d * float(na) * f;
+    });
+}
+
+// The sum over a workgroup, in every thread.
+__device__ __forceinline__ double block_sum(double v)
+{
+    __shared__ double all[kGnThreads / 64];
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) all[threadIdx.x / 64] = v;
+    __syncthreads();
+    double s = 0.;
+#pragma unroll
+    for (int i = 0; i < kGnThreads / 64; ++i) s += all[i];
+    return s;
+}
+
+// Statistics of a group from its channels' moments in each chunk; one workgroup a group.
+template <int DT>
+__global__ __launch_bounds__(kGnThreads) void k_gn_finish(GnArgs a, GnGrid gr, const float2* part)
+{
+    const int64_t g = blockIdx.x, n = gr.n0 + blockIdx.y, cg = a.C / a.G, c0 = g * cg;
+    const float2* p = part + n * gr.chunks * a.C + c0;
+    const double M = double(a.HW) * double(cg);
+    const int64_t all = cg * gr.chunks;
+    auto rows = [&](int64_t i) { return double(dmin(gr.chunk, a.HW - i * gr.chunk)); };
+    auto first = [&](int64_t i, int64_t c) {
+        const char* row = sample_row<DT>(a.x, a.ldx, a, n, i * gr.chunk);
+        if constexpr (DT == kF32) return double(reinterpret_cast<const float*>(row)[c0 + c]);
+        else return double(unpack1<DT>(reinterpret_cast<const uint16_t*>(row)[c0 + c]));
+    };
+    double mean = 0., var = 0.;
+#pragma unroll 4
+    for (int64_t k = threadIdx.x; k < all; k += kGnThreads) {
+        const int64_t i = k / cg;
+        const int64_t c = k - i * cg;
+        mean += (first(i, c) + double(p[i * a.C + c].x)) * rows(i);
+    }
+    mean = block_sum(mean) / M;
+#pragma unroll 4
+    for (int64_t k = threadIdx.x; k < all; k += kGnThreads) {
+        const int64_t i = k / cg;
+        const int64_t c = k - i * cg;
+        const float2 v = p[i * a.C + c];
+        const double d = first(i, c) + double(v.x) - mean;
+        var += double(v.y) + d * d * rows(i);
+    }
+    var = block_sum(var) / M;
+    if (threadIdx.x == 0)
+        reinterpret_cast<float2*>(a.stats)[n * a.G + g] =
+            make_float2(float(mean), float(1. / sqrt(var + double(a.eps))));
+}
+
+template <int DT, int ACT, bool WHOLE>
+__global__ __launch_bounds__(kGnThreads) void k_gn_apply(GnArgs a, GnGrid gr)
+{
+    const int64_t n = gr.n0 + blockIdx.y;
+    const Place p = place_of(a, gr);
+    const int C = int(a.C);
+    if (p.nv == 0) return;
+    Channel ch;
+    load_channels<WHOLE>(a, gr.width, n, p.c, p.nv, ch);
+    auto one = [&](const Raw8<DT>& r, int64_t row) {
+        float v[8], d;
+        widen8<DT>(r, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            gn_act<ACT>(fmaf((v[e] - ch.mean[e]) * ch.rstd[e], ch.w[e], ch.b[e]), a.param, v[e], d);
+        store8<DT, WHOLE>(sample_row<DT>(a.out, a.ldo, a, n, row), uint32_t(p.c), C, v);
+    };
+    int64_t row = p.row0 + p.lane;
+    for (; row + 3 * p.lanes < p.row1; row += 4 * p.lanes) {
+        Raw8<DT> r[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            r[u] = load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row + u * p.lanes),
+                                    uint32_t(p.c), C);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) one(r[u], row + u * p.lanes);
+    }
+    for (; row < p.row1; row += p.lanes)
+        one(load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row), uint32_t(p.c), C), row);
+}
+
+// xhat and dz of 8 channels.
+template <int DT, int ACT>
+__device__ __forceinline__ void gn_grad(const Raw8<DT>& rx, const Raw8<DT>& rg, const Channel& ch,
+                                        float param, float (&xhat)[8], float (&dz)[8])
+{
+    float g[8], f, d;
+    widen8<DT>(rx, xhat);
+    widen8<DT>(rg, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        xhat[e] = (xhat[e] - ch.mean[e]) * ch.rstd[e];
+        gn_act<ACT>(fmaf(xhat[e], ch.w[e], ch.b[e]), param, f, d);
+        dz[e] = g[e] * d;
+    }
+}
+
+// part[n][chunk][c]: sums of dz and of dz * xhat.
+template <int DT, int ACT, bool WHOLE>
+__global__ __launch_bounds__(kGnThreads) void k_gn_sums(GnArgs a, GnGrid gr, float2* part)
+{
+    const int64_t n = gr.n0 + blockIdx.y;
+    const Place p = place_of(a, gr);
+    const int C = int(a.C);
+    float s[8] = {}, t[8] = {};
+    if (p.nv > 0) {
+        Channel ch;
+        load_channels<WHOLE>(a, gr.width, n, p.c, p.nv, ch);
+        auto add = [&](const Raw8<DT>& rx, const Raw8<DT>& rg) {
+            float xhat[8], dz[8];
+            gn_grad<DT, ACT>(rx, rg, ch, a.param, xhat, dz);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s[e] += dz[e];
+                t[e] = fmaf(dz[e], xhat[e], t[e]);
+            }
+        };
+        int64_t row = p.row0 + p.lane;
+        for (; row + p.lanes < p.row1; row += 2 * p.lanes) {
+            Raw8<DT> rx[2], rg[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                rx[u] = load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row + u * p.lanes),
+                                         uint32_t(p.c), C);
+                rg[u] = load8<DT, WHOLE>(sample_row<DT>(a.dy, a.lddy, a, n, row + u * p.lanes),
+                                         uint32_t(p.c), C);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) add(rx[u], rg[u]);
+        }
+        for (; row < p.row1; row += p.lanes)
+            add(load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row), uint32_t(p.c), C),
+                load8<DT, WHOLE>(sample_row<DT>(a.dy, a.lddy, a, n, row), uint32_t(p.c), C));
+    }
+    join_lanes(p, s, t, part + (n * gr.chunks + blockIdx.x) * a.C, C,
+               [](float2& v, const float2& o, int) {
+        v.x += o.x;
+        v.y += o.y;
+    });
+}
+
+// sums[n][c] over the chunks, and coef[n][g] = (<w dz>, <w dz xhat>).
+__global__ __launch_bounds__(kGnThreads) void k_gn_finish_sums(GnArgs a, GnGrid gr,
+                                                              const float2* part, float2* sums,
+                                                              float2* coef)
+{
+    const int64_t g = blockIdx.x, n = gr.n0 + blockIdx.y, cg = a.C / a.G, c0 = g * cg;
+    __shared__ double2 all[kGnThreads];
+    double u = 0., v = 0.;
+    for (int64_t cb = 0; cb < cg; cb += kGnThreads) {             // 256 channels at a time
+        const int wide = int(dmin(cg - cb, kGnThreads)), lanes = kGnThreads / wide;
+        const int lane = int(threadIdx.x) / wide, c = int(threadIdx.x) - lane * wide;
+        double s = 0., t = 0.;
+        if (lane < lanes) {
+            const float2* p = part + n * gr.chunks * a.C + c0 + cb + c;
+#pragma unroll 4
+            for (int i = lane; i < gr.chunks; i += lanes) {
+                const float2 x = p[i * a.C];
+                s += double(x.x);
+                t += double(x.y);
+            }
+        }
+        __syncthreads();
+        all[threadIdx.x] = make_double2(s, t);
+        __syncthreads();
+        if (lane == 0) {
+            for (int l = 1; l < lanes; ++l) {
+                s += all[l * wide + c].x;
+                t += all[l * wide + c].y;
+            }
+            const double w = a.weight ? double(a.weight[c0 + cb + c]) : 1.;
+            sums[n * a.C + c0 + cb + c] = make_float2(float(s), float(t));
+            u += w * s;
+            v += w * t;
+        }
+    }
+    const double M = double(a.HW) * double(cg);
+    u = block_sum(u) / M;
+    v = block_sum(v) / M;
+    if (threadIdx.x == 0) coef[n * a.G + g] = make_float2(float(u), float(v));
+}
+
+// dw and db: the samples' sums, in their order.
+__global__ __launch_bounds__(kGnThreads) void k_gn_dparams(GnArgs a, const float2* sums)
+{
+    const int64_t c = int64_t(blockIdx.x) * kGnThreads + threadIdx.x;
+    if (c >= a.C) return;
+    double s = 0., t = 0.;
+#pragma unroll 4
+    for (int64_t n = 0; n < a.N; ++n) {
+        const float2 v = sums[n * a.C + c];
+        s += double(v.x);
+        t += double(v.y);
+    }
+    if (a.dbias) a.dbias[c] = float(s);
+    if (a.dweight) a.dweight[c] = float(t);
+}
+
+template <int DT, int ACT, bool WHOLE>
+__global__ __launch_bounds__(kGnThreads) void k_gn_dx(GnArgs a, GnGrid gr, const float2* coef)
+{
+    const int64_t n = gr.n0 + blockIdx.y;
+    const Place p = place_of(a, gr);
+    const int C = int(a.C);
+    if (p.nv == 0) return;
+    Channel ch;
+    load_channels<WHOLE>(a, gr.width, n, p.c, p.nv, ch);
+    float u[8], v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float2 k = coef[n * a.G + ch.group[e]];
+        u[e] = k.x;
+        v[e] = k.y;
+    }
+    auto one = [&](const Raw8<DT>& rx, const Raw8<DT>& rg, int64_t row) {
+        float xhat[8], dz[8];
+        gn_grad<DT, ACT>(rx, rg, ch, a.param, xhat, dz);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            dz[e] = ch.rstd[e] * (fmaf(ch.w[e], dz[e], -u[e]) - xhat[e] * v[e]);
+        store8<DT, WHOLE>(sample_row<DT>(a.out, a.ldo, a, n, row), uint32_t(p.c), C, dz);
+    };
+    int64_t row = p.row0 + p.lane;
+    for (; row + p.lanes < p.row1; row += 2 * p.lanes) {
+        Raw8<DT> rx[2], rg[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            rx[k] = load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row + k * p.lanes),
+                                     uint32_t(p.c), C);
+            rg[k] = load8<DT, WHOLE>(sample_row<DT>(a.dy, a.lddy, a, n, row + k * p.lanes),
+                                     uint32_t(p.c), C);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) one(rx[k], rg[k], row + k * p.lanes);
+    }
+    for (; row < p.row1; row += p.lanes)
+        one(load8<DT, WHOLE>(sample_row<DT>(a.x, a.ldx, a, n, row), uint32_t(p.c), C),
+            load8<DT, WHOLE>(sample_row<DT>(a.dy, a.lddy, a, n, row), uint32_t(p.c), C), row);
+}
+
+// Workgroups of rows: four a CU where the rows give them, each at least 8 rows a lane.
+GnGrid make_grid(int64_t N, int64_t HW, int64_t C, int64_t G, int64_t cus)
+{
+    GnGrid gr{};
+    gr.width = make_fast_div(uint32_t(C / G));
+    gr.blocks = int(ceil_div(C, kBlockC));
+    const int64_t lanes = max64(1, kGnThreads / ceil_div(min64(C, kBlockC), kRowV));
+    const int64_t want = max64(1, ceil_div(4 * cus, N * gr.blocks));
+    gr.chunk = max64(8 * lanes, ceil_div(HW, want));
+    gr.chunks = int(ceil_div(HW, gr.chunk));
+    return gr;
+}
+
+// Calls f(grid of a run of samples, its workgroups of rows, its groups).
+template <class F>
+void each_samples(const GnArgs& a, GnGrid gr, F&& f)
+{
+    constexpr int64_t kMost = 32768;               // of a grid's second extent
+    for (gr.n0 = 0; gr.n0 < a.N; gr.n0 += kMost) {
+        const unsigned n = unsigned(min64(kMost, a.N - gr.n0));
+        f(gr, dim3(unsigned(gr.chunks), n, unsigned(gr.blocks)), dim3(unsigned(a.G), n));
+    }
+}
+
+// Calls f(std::integral_constant<int, ACT>).
+template <class F>
+void with_gn_act(int act, F&& f)
+{
+    switch (act) {
+    case kGnSilu: f(std::integral_constant<int, kGnSilu>{}); break;
+    case kGnGelu: f(std::integral_constant<int, kGnGelu>{}); break;
+    case kGnGeluTanh: f(std::integral_constant<int, kGnGeluTanh>{}); break;
+    case kGnIdentity: f(std::integral_constant<int, kGnIdentity>{}); break;
+    case kGnLeaky: f(std::integral_constant<int, kGnLeaky>{}); break;
+    default: break;
+    }
+}
+
+}  // namespace
+
+// part [N][chunks][C], sums [N][C], coef [N][G] (float2 each); the forward's statistics
+// where the caller wants none take sums' place.
+size_t gn_workspace_bytes(int64_t N, int64_t HW, int64_t C, int64_t G, int64_t cus)
+{
+    const GnGrid gr = make_grid(N, HW, C, G, cus);
+    return size_t(N) * 8 * (size_t(gr.chunks) * size_t(C) + size_t(C) + size_t(G));
+}
+
+void launch_gn_forward(const GnArgs& a0, int dtype, int64_t cus, void* ws, hipStream_t s)
+{
+    GnArgs a = a0;
+    const GnGrid gr = make_grid(a.N, a.HW, a.C, a.G, cus);
+    float2* part = static_cast<float2*>(ws);
+    if (!a.stats) a.stats = reinterpret_cast<float*>(part + a.N * gr.chunks * a.C);
+    with_dtype(dtype, [&](auto d) {
+        constexpr int DT = decltype(d)::value;
+        with_whole(a.C, [&](auto wh) {
+            constexpr bool W = decltype(wh)::value;
+            each_samples(a, gr, [&](const GnGrid& g, dim3 grid, dim3 groups) {
+                hipLaunchKernelGGL((k_gn_stats<DT, W>), grid, dim3(kGnThreads), 0, s, a, g, part);
+                hipLaunchKernelGGL((k_gn_finish<DT>), groups, dim3(kGnThreads), 0, s, a, g, part);
+                with_gn_act(a.act, [&](auto act) {
+                    hipLaunchKernelGGL((k_gn_apply<DT, decltype(act)::value, W>), grid,
+                                       dim3(kGnThreads), 0, s, a, g);
+                });
+            });
+        });
+    });
+}
+
+void launch_gn_backward(const GnArgs& a, int dtype, int64_t cus, void* ws, hipStream_t s)
+{
+    auto params = [&](const float2* sums, int64_t n) {
+        GnArgs b = a;
+        b.N = n;
+        if (a.dweight || a.dbias)
+            hipLaunchKernelGGL(k_gn_dparams, dim3(unsigned(ceil_div(a.C, kGnThreads))),
+                               dim3(kGnThreads), 0, s, b, sums);
+    };
+    if (a.N == 0 || a.HW == 0) return params(nullptr, 0);         // zeros
+    const GnGrid gr = make_grid(a.N, a.HW, a.C, a.G, cus);
+    float2* part = static_cast<float2*>(ws);
+    float2* sums = part + a.N * gr.chunks * a.C;
+    float2* coef = sums + a.N * a.C;
+    with_dtype(dtype, [&](auto d) {
+        constexpr int DT = decltype(d)::value;
+        with_whole(a.C, [&](auto wh) {
+            constexpr bool W = decltype(wh)::value;
+            with_gn_act(a.act, [&](auto act) {
+                constexpr int A = decltype(act)::value;
+                each_samples(a, gr, [&](const GnGrid& g, dim3 grid, dim3 groups) {
+                    hipLaunchKernelGGL((k_gn_sums<DT, A, W>), grid, dim3(kGnThreads), 0, s, a, g,
+                                       part);
+                    hipLaunchKernelGGL(k_gn_finish_sums, groups, dim3(kGnThreads), 0, s, a, g,
+                                       part, sums, coef);
+                    if (a.out)
+                        hipLaunchKernelGGL((k_gn_dx<DT, A, W>), grid, dim3(kGnThreads), 0, s, a, g,
+                                           coef);
+                });
+            });
+        });
+    });
+    params(sums, a.N);
+}
+
+}  // namespace iabn
