@@ -87,30 +87,38 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
     using F = DqShape<DT, DP>;
     using S = TileShape<DT, DP>;
     constexpr int ES = S::ES, KS = DP / 16, DB = DP / 32, KB = F::KT / 32;
-    __shared__ uint4 lds[4 * F::SLOTS];
+    __shared__ uint4 space[4 * F::SLOTS];
+    char* const lds = reinterpret_cast<char*>(space);
 
     const int lane = threadIdx.x % 64, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     uint32_t head, tile;
-    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), head, tile);
+    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), false, head, tile);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
     tile = uint32_t(tiles) - 1 - tile;             // causal rows with many keys first
     const Sequence sq = sequence_of(a, b);
     const int rows = sq.lq * a.G, all_rows = a.Sq * a.G;
     const int row0 = int(tile) * 128, r0 = row0 + wave * 32, r = r0 + lane % 32;
     const int tok = int(fast_div(uint32_t(r), a.group)), hq = hk * a.G + r - tok * a.G;
-    const bool packed_q = a.q_starts != nullptr, packed_k = a.k_starts != nullptr;
+    const bool packed_q = a.q_starts != nullptr;
 
-    int lo = 0, hi = 0;                            // keys that the workgroup's rows see
+    // the keys that some of the workgroup's rows see, that all of them see, and that some
+    // of this wave's
+    int lo = 0, hi = 0, all_lo = 0, all_hi = 0, lo_min = 0, hi_max = 0;
     if (row0 < rows) {
-        int x;
-        visible(a, sq, int(fast_div(uint32_t(row0), a.group)), lo, x);
-        visible(a, sq, int(fast_div(uint32_t(min(row0 + 128, rows) - 1), a.group)), x, hi);
+        visible(a, sq, int(fast_div(uint32_t(row0), a.group)), lo, all_hi);
+        visible(a, sq, int(fast_div(uint32_t(min(row0 + 128, rows) - 1), a.group)), all_lo, hi);
+        lo = scalar(lo);
+        hi = scalar(hi);
+        all_lo = scalar(all_lo);
+        all_hi = scalar(all_hi);
     }
-    int lo_min = 0, lo_max = 0, hi_min = 0, hi_max = 0;          // the wave's rows
     if (r0 < rows) {
-        visible(a, sq, int(fast_div(uint32_t(r0), a.group)), lo_min, hi_min);
-        visible(a, sq, int(fast_div(uint32_t(min(r0 + 32, rows) - 1), a.group)), lo_max, hi_max);
+        int x;
+        visible(a, sq, int(fast_div(uint32_t(r0), a.group)), lo_min, x);
+        visible(a, sq, int(fast_div(uint32_t(min(r0 + 32, rows) - 1), a.group)), x, hi_max);
+        lo_min = scalar(lo_min);
+        hi_max = scalar(hi_max);
     }
     int row_lo = 0, row_hi = 0;
     float lse2 = INFINITY, dl = 0.f;               // a row that sees nothing: P = 0
@@ -123,9 +131,10 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
     }
     if (r < rows) {
         visible(a, sq, tok, row_lo, row_hi);
-        const char* qp = group_rows(a, a.q, b, sq, hk, ES)(r);
-        const char* op = group_rows(a, a.out, b, sq, hk, ES)(r);
-        const char* gp = group_rows(a, g.dout, b, sq, hk, ES)(r);
+        row_hi = max(row_lo, row_hi);
+        const char* qp = group_row(a, a.q, b, sq, hk, r, ES);
+        const char* op = group_row(a, a.out, b, sq, hk, r, ES);
+        const char* gp = group_row(a, g.dout, b, sq, hk, r, ES);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const int d = 16 * ks + 8 * h;
@@ -143,69 +152,112 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
     dl = both_sum(dl);
     if (r < rows && h == 0) delta[(int64_t(b) * a.KV + hk) * all_rows + r] = dl;
 
-    const char* kp = head_of(a.k, packed_k, b, sq.k0, hk, ES);
-    const char* vp = head_of(a.v, packed_k, b, sq.k0, hk, ES);
-    const int64_t kpitch = a.k.row * ES, vpitch = a.v.row * ES;
+    using T = Tiles<DT, DP, F::KT, F::NT>;
+    const T keys = key_tiles<T>(a, a.k, b, sq, hk, ES), vals = key_tiles<T>(a, a.v, b, sq, hk, ES);
+    const RowFrags<DT, DP> rf;
+    const ColFrags<DT, DP> cf;
 
     f32x16_t dq[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i) zero(dq[i]);
     Scaled<DT> scaled;
 
-    TileLoad<DT, DP, F::KT, F::NT> kl, vl;
-    auto k_tile = [&](int st) { return lds + st * 2 * F::SLOTS; };
-    auto v_tile = [&](int st) { return lds + (st * 2 + 1) * F::SLOTS; };
-    auto block = [&](int k0, int kb, int st) {     // 32 keys
-        if (k0 >= hi_max || k0 + 32 <= lo_min) return;
-        f32x16_t s, ds;
-        zero(s);
-        zero(ds);
+    auto tile_at = [&](int st, int v) { return lds + (2 * st + v) * F::SLOTS * 16; };
+    auto fetch = [&](int i, int st) __attribute__((always_inline)) {
+        keys.load(tile_at(st, 0), lo + i * F::KT, hi, a.D);
+        vals.load(tile_at(st, 1), lo + i * F::KT, hi, a.D);
+    };
+    // A tile, 32 keys after another: a block's exponentials among the next one's products, and
+    // fragments read ahead of theirs.
+    auto step_of = [&](int k0, int st, auto some) __attribute__((always_inline)) {
+        const char *K = tile_at(st, 0), *V = tile_at(st, 1);
+        f32x16_t s[KB], ds[KB];
+        const uint32_t at = uint32_t(k0 + 4 * h - row_lo), n = uint32_t(row_hi - row_lo);
+        auto probs = [&](int kb, int from, int to) {             // dS of some of a block
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            s = mma(row_frag<DT, DP>(k_tile(st), kb * 32, ks), q[ks], s);
-            ds = mma(row_frag<DT, DP>(v_tile(st), kb * 32, ks), go[ks], ds);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(s[i], a.c, -lse2));
-            ds[i] = p * (ds[i] - dl);
-        }
-        if (k0 < lo_max || k0 + 32 > hi_min) {     // some row does not see all
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int j = k0 + 8 * (i / 4) + 4 * h + i % 4;
-                if (j < row_lo || j >= row_hi) ds[i] = 0.f;
+            for (int i = from; i < to; ++i) {
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[kb][i], a.c, -lse2));
+                ds[kb][i] = p * (ds[kb][i] - dl);
+                if (decltype(some)::value && at + uint32_t(kb * 32 + 8 * (i / 4) + i % 4) >= n)
+                    ds[kb][i] = 0.f;
             }
+        };
+        Frag<DT> f[2][2];
+        auto read = [&](int g) {
+            f[g & 1][0] = rf.read(K, g / KS * 32, g % KS);
+            f[g & 1][1] = rf.read(V, g / KS * 32, g % KS);
+        };
+        read(0);
+#pragma unroll
+        for (int g = 0; g < KB * KS; ++g) {
+            const int kb = g / KS, ks = g % KS;
+            if (g + 1 < KB * KS) read(g + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            if (ks == 0) {
+                zero(s[kb]);
+                zero(ds[kb]);
+            }
+            s[kb] = mma(f[g & 1][0], q[ks], s[kb]);
+            ds[kb] = mma(f[g & 1][1], go[ks], ds[kb]);
+            if (kb > 0) probs(kb - 1, 16 * ks / KS, 16 * (ks + 1) / KS);
         }
-        scaled.apply(ds, dq);
+        constexpr int CS = DB % 2 == 0 ? 2 : 3, CG = 2 * DB / CS;          // of a block
+        Frag<DT> c[2][CS];
+        auto read_c = [&](int g) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const Frag<DT> f = results<DT>(ds, t);
+            for (int i = 0; i < CS; ++i)
+                c[g & 1][i] = cf.read(K, (g * CS + i) / DB * 16, (g * CS + i) % DB);
+        };
+        read_c(0);
+        if (KB == 1) probs(0, 0, 16);
 #pragma unroll
-            for (int i = 0; i < DB; ++i)
-                dq[i] = mma(col_frag<DT, DP>(k_tile(st), kb * 32 + 16 * t, i), f, dq[i]);
+        for (int kb = 0; kb < KB; ++kb) {
+            scaled.apply(ds[kb], dq);
+            Frag<DT> x = results<DT>(ds[kb], 0);
+#pragma unroll
+            for (int g = 0; g < CG; ++g) {
+                if (kb * CG + g + 1 < KB * CG) read_c(kb * CG + g + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < CS; ++i) {
+                    const int t = (g * CS + i) / DB, db = (g * CS + i) % DB;
+                    if (db == 0 && t == 1) x = results<DT>(ds[kb], 1);
+                    dq[db] = mma(c[(kb * CG + g) & 1][i], x, dq[db]);
+                }
+                if (KB > 1 && kb == KB - 2) probs(KB - 1, 16 * g / CG, 16 * (g + 1) / CG);
+            }
         }
     };
     const int steps = hi > lo ? (hi - lo + F::KT - 1) / F::KT : 0;
     if (steps > 0) {
-        kl.load(kp, kpitch, lo, hi, a.D);
-        vl.load(vp, vpitch, lo, hi, a.D);
-        kl.store(k_tile(0));
-        vl.store(v_tile(0));
-        __syncthreads();
-        for (int i = 0; i < steps; ++i) {
-            const int st = i & 1, k0 = lo + i * F::KT;
-            const bool more = i + 1 < steps;
-            if (more) kl.load(kp, kpitch, k0 + F::KT, hi, a.D);
-            block(k0, 0, st);
-            if (more) {
-                kl.store(k_tile(st ^ 1));
-                vl.load(vp, vpitch, k0 + F::KT, hi, a.D);
-            }
-#pragma unroll
-            for (int kb = 1; kb < KB; ++kb) block(k0 + kb * 32, kb, st);
-            if (more) vl.store(v_tile(st ^ 1));
+        if (a.D < DP) {
+            clear<F::NT>(lds, 4 * F::SLOTS * 16);
             __syncthreads();
+        }
+        fetch(0, 0);
+        auto step = [&](int i, auto st, auto some) __attribute__((always_inline)) {
+            arrived();
+            __syncthreads();
+            if (i + 1 < steps) fetch(i + 1, 1 - st);
+            const int k0 = lo + i * F::KT;
+            if (!decltype(some)::value || (k0 < hi_max && k0 + F::KT > lo_min))
+                step_of(k0, st, some);
+        };
+        // pairs of tiles that all rows see whole in a loop of their own, as in the forward
+        auto whole = [&](int i) {
+            return lo + i * F::KT >= all_lo && lo + (i + 1) * F::KT <= all_hi;
+        };
+        for (int i = 0; i < steps;) {
+            if ((i & 1) == 0) {
+                while (i + 1 < steps && whole(i) && whole(i + 1)) {
+                    step(i, std::integral_constant<int, 0>{}, std::false_type{});
+                    step(i + 1, std::integral_constant<int, 1>{}, std::false_type{});
+                    i += 2;
+                }
+                if (i >= steps) break;
+            }
+            step(i, i & 1, std::true_type{});
+            ++i;
         }
     }
     // rows of a padded batch behind its length are written too, as zeros
@@ -225,26 +277,62 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
 // ---------------------------------------------------------------------------
 // dK and dV
 
+// A key tile's rows cut among workgroups: `chunk` rows each, whose shares of dK and dV go
+// through the workspace where a tile's rows take more than one.
+struct DkvParts {
+    int parts, chunk;
+    float* share;                     // [head][tile][part][dK, dV][128 keys][D]
+};
+
+__device__ __forceinline__ float* share_of(const DkvParts& pt, uint32_t head, uint32_t tiles,
+                                           uint32_t tile, int part, int D)
+{
+    return pt.share + ((int64_t(head) * tiles + tile) * pt.parts + part) * 2 * 128 * D;
+}
+
+// Rows [lo, hi) of the group that see key x.
+__device__ __forceinline__ void seen_by(const AttnArgs& a, const Sequence& s, int x, int& lo, int& hi)
+{
+    const int off = s.lk - s.lq;
+    lo = max(0, x - off - a.right);
+    hi = max(lo, min(s.lq, x - off + a.left + 1));
+    lo *= a.G;
+    hi *= a.G;
+}
+
 template <int DT, int DP>
 struct DkvShape {
-    static constexpr int NT = 256, QT = DT == kF32 ? 32 : 64;
-    static constexpr int SLOTS = QT * TileShape<DT, DP>::NC;
+    static constexpr int NT = 256;
+    // 16-bit types keep the values in LDS instead of registers and rows in tiles of 8 KB, so
+    // that two workgroups run on a CU
+    static constexpr bool VL = DT != kF32;
+    static constexpr int QT = DT == kF32 || DP > 64 ? 32 : 64;
+    static constexpr int TILE = QT * TileShape<DT, DP>::PITCH;
+    static constexpr int VTILE = VL ? 128 * TileShape<DT, DP>::PITCH : 0;
+    static constexpr int WAVES = VL ? 2 : 1;
 };
 
 template <int DT, int DP>
-__global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnArgs a, AttnGrads g, const float* delta,
-                                                     int tiles)
+__global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(AttnArgs a,
+                                                                            AttnGrads g,
+                                                                            const float* delta,
+                                                                            DkvParts pt,
+                                                                            int tiles)
 {
     using F = DkvShape<DT, DP>;
     using S = TileShape<DT, DP>;
     constexpr int ES = S::ES, KS = DP / 16, DB = DP / 32, QB = F::QT / 32;
-    __shared__ uint4 lds[4 * F::SLOTS];
+    __shared__ uint4 space[(4 * F::TILE + F::VTILE) / 16];
     __shared__ alignas(16) float info[2][2][F::QT];              // lse * log2(e), delta
+    char* const lds = reinterpret_cast<char*>(space);
 
     const int lane = threadIdx.x % 64, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     uint32_t head, tile;
-    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), head, tile);
+    // Causal keys are seen by ever fewer rows: the long tiles of all heads first (head by head, the
+    // last one's would end alone: 850 us against 640 for twice 4096 tokens of 32 heads on 8).
+    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles),
+                  a.left < kAttnMaxLen || a.right < kAttnMaxLen, head, tile);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
     const Sequence sq = sequence_of(a, b);
     const int all_rows = a.Sq * a.G;
@@ -252,34 +340,41 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnArgs a, AttnGrads g, co
     const bool packed_k = a.k_starts != nullptr;
     if (packed_k && key0 >= sq.lk) return;
 
-    // rows [lo, hi) that see key x
-    const int off = sq.lk - sq.lq;
-    auto seen_by = [&](int x, int& lo, int& hi) {
-        lo = max(0, x - off - a.right);
-        hi = max(lo, min(sq.lq, x - off + a.left + 1));
-        lo *= a.G;
-        hi *= a.G;
-    };
-    int lo = 0, hi = 0;                            // the workgroup's keys
+    // the rows that see some of the workgroup's keys, all of them, and some of this wave's
+    int lo = 0, hi = 0, all_lo = 0, all_hi = 0, lo_min = 0, hi_max = 0;
     if (key0 < sq.lk) {
-        int x;
-        seen_by(key0, lo, x);
-        seen_by(min(key0 + 128, sq.lk) - 1, x, hi);
+        seen_by(a, sq, key0, lo, all_hi);
+        seen_by(a, sq, min(key0 + 128, sq.lk) - 1, all_lo, hi);
+        lo = scalar(lo);
+        hi = scalar(hi);
+        all_lo = scalar(all_lo);
+        all_hi = scalar(all_hi);
     }
-    int lo_min = 0, lo_max = 0, hi_min = 0, hi_max = 0;          // the wave's
     if (j0 < sq.lk) {
-        seen_by(j0, lo_min, hi_min);
-        seen_by(min(j0 + 32, sq.lk) - 1, lo_max, hi_max);
+        int x;
+        seen_by(a, sq, j0, lo_min, x);
+        seen_by(a, sq, min(j0 + 32, sq.lk) - 1, x, hi_max);
+        lo_min = scalar(lo_min);
+        hi_max = scalar(hi_max);
+    }
+    // this workgroup's part of the rows
+    bool shared = false;
+    if (pt.parts > 1) {
+        shared = hi - lo > pt.chunk;
+        const int64_t end = int64_t(hi) - int64_t(blockIdx.y) * pt.chunk;
+        if (blockIdx.y > 0 && end <= lo) return;
+        hi = int(end);
+        lo = int(max(int64_t(lo), end - pt.chunk));
     }
     int key_lo = 0, key_hi = 0;
-    Frag<DT> k[KS], v[KS];
+    Frag<DT> k[KS], v[F::VL ? 1 : KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         zero(k[ks]);
-        zero(v[ks]);
+        if constexpr (!F::VL) zero(v[ks]);
     }
     if (j < sq.lk) {
-        seen_by(j, key_lo, key_hi);
+        seen_by(a, sq, j, key_lo, key_hi);
         const char* kp = head_of(a.k, packed_k, b, sq.k0, hk, ES) + int64_t(j) * a.k.row * ES;
         const char* vp = head_of(a.v, packed_k, b, sq.k0, hk, ES) + int64_t(j) * a.v.row * ES;
 #pragma unroll
@@ -287,7 +382,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnArgs a, AttnGrads g, co
             const int d = 16 * ks + 8 * h;
             if (d >= a.D) continue;
             k[ks] = frag_of<DT>(kp + d * ES);
-            v[ks] = frag_of<DT>(vp + d * ES);
+            if constexpr (!F::VL) v[ks] = frag_of<DT>(vp + d * ES);
         }
     }
     f32x16_t dk[DB], dv[DB];
@@ -298,13 +393,21 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnArgs a, AttnGrads g, co
     }
     Scaled<DT> scaled;
 
-    const GroupRows qrows = group_rows(a, a.q, b, sq, hk, ES);
-    const GroupRows grows = group_rows(a, g.dout, b, sq, hk, ES);
-    TileLoad<DT, DP, F::QT, F::NT> ql, gl;
+    using T = Tiles<DT, DP, F::QT, F::NT>;
+    const T qrows = group_tiles<T>(a, a.q, b, sq, hk, ES), grows = group_tiles<T>(a, g.dout, b, sq, hk, ES);
+    const RowFrags<DT, DP> rows_at;
+    const ColFrags<DT, DP> cols_at;
+    char* const values = lds + 4 * F::TILE;
     float il = 0.f, id = 0.f;                      // of the next tile, one row a thread
-    auto q_tile = [&](int st) { return lds + st * 2 * F::SLOTS; };
-    auto g_tile = [&](int st) { return lds + (st * 2 + 1) * F::SLOTS; };
-    auto fetch_info = [&](int first) {
+    auto tile_at = [&](int st, int v) { return lds + (2 * st + v) * F::TILE; };
+    // From the last rows to the first: under a causal mask key tiles begin at different rows, and
+    // all of a head's workgroups read the same ones from L2 only if they start at the end.
+    const int steps = hi > lo ? (hi - lo + F::QT - 1) / F::QT : 0;
+    auto row_of = [&](int i) { return lo + (steps - 1 - i) * F::QT; };
+    auto fetch = [&](int i, int st) __attribute__((always_inline)) {
+        const int first = row_of(i);
+        qrows.load(tile_at(st, 0), first, hi, a.D);
+        grows.load(tile_at(st, 1), first, hi, a.D);
         const int r = first + int(threadIdx.x);
         il = INFINITY;                             // no row: P = 0
         id = 0.f;
@@ -315,86 +418,127 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnArgs a, AttnGrads g, co
             id = delta[(int64_t(b) * a.KV + hk) * all_rows + r];
         }
     };
-    auto put_info = [&](int st) {
-        if (threadIdx.x < F::QT) {
-            info[st][0][threadIdx.x] = il;
-            info[st][1][threadIdx.x] = id;
-        }
-    };
-    auto block = [&](int r0, int qb, int st) {     // 32 rows
-        if (r0 >= hi_max || r0 + 32 <= lo_min) return;
-        f32x16_t p, ds;
-        zero(p);
-        zero(ds);
+    auto step_of = [&](int r0, int st, auto some) __attribute__((always_inline)) {
+        const char *Q = tile_at(st, 0), *O = tile_at(st, 1);
+        const uint32_t n = uint32_t(key_hi - key_lo);
+        // the addresses' XORs are made anew each time: kept, they would take the registers
+        // that the sums need
+        RowFrags<DT, DP> rf = rows_at;
+        ColFrags<DT, DP> cf = cols_at;
+        asm volatile("" : "+v"(rf.at), "+v"(cf.at));
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            p = mma(row_frag<DT, DP>(q_tile(st), qb * 32, ks), k[ks], p);
-            ds = mma(row_frag<DT, DP>(g_tile(st), qb * 32, ks), v[ks], ds);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            const float4 ls = *reinterpret_cast<const float4*>(&info[st][0][qb * 32 + 2 * i + 4 * h]);
-            const float4 de = *reinterpret_cast<const float4*>(&info[st][1][qb * 32 + 2 * i + 4 * h]);
-            const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                p[i + e] = __builtin_amdgcn_exp2f(fmaf(p[i + e], a.c, -l4[e]));
-                ds[i + e] = p[i + e] * (ds[i + e] - d4[e]);
-            }
-        }
-        if (r0 < lo_max || r0 + 32 > hi_min) {     // some key is not seen by all
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int r = r0 + 8 * (i / 4) + 4 * h + i % 4;
-                if (r < key_lo || r >= key_hi) p[i] = ds[i] = 0.f;
-            }
-        }
-        scaled.apply(ds, dk);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const Frag<DT> fp = results<DT>(p, t), fs = results<DT>(ds, t);
-#pragma unroll
-            for (int i = 0; i < DB; ++i) {
-                dv[i] = mma(col_frag<DT, DP>(g_tile(st), qb * 32 + 16 * t, i), fp, dv[i]);
-                dk[i] = mma(col_frag<DT, DP>(q_tile(st), qb * 32 + 16 * t, i), fs, dk[i]);
-            }
-        }
-    };
-    const int steps = hi > lo ? (hi - lo + F::QT - 1) / F::QT : 0;
-    if (steps > 0) {
-        ql.load_at(qrows, lo, hi, a.D);
-        gl.load_at(grows, lo, hi, a.D);
-        fetch_info(lo);
-        ql.store(q_tile(0));
-        gl.store(g_tile(0));
-        put_info(0);
-        __syncthreads();
-        for (int i = 0; i < steps; ++i) {
-            const int st = i & 1, r0 = lo + i * F::QT;
-            const bool more = i + 1 < steps;
-            auto fetch = [&]() {
-                ql.load_at(qrows, r0 + F::QT, hi, a.D);
-                gl.load_at(grows, r0 + F::QT, hi, a.D);
-                fetch_info(r0 + F::QT);
+        for (int qb = 0; qb < QB; ++qb) {          // 32 rows after another
+            const uint32_t at = uint32_t(r0 + qb * 32 + 4 * h - key_lo);
+            f32x16_t p, ds;
+            zero(p);
+            zero(ds);
+            Frag<DT> f[2][2], w[2];
+            auto read = [&](int ks) {
+                f[ks & 1][0] = rf.read(Q, qb * 32, ks);
+                f[ks & 1][1] = rf.read(O, qb * 32, ks);
+                if constexpr (F::VL) w[ks & 1] = rf.read(values, wave * 32, ks);
             };
-            // float32 has no registers for the next tile over the products, which take 16
-            // times as long as loads of the same elements would leave uncovered
-            if (more && DT != kF32) fetch();
+            read(0);
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb) block(r0 + qb * 32, qb, st);
-            if (more) {
-                if (DT == kF32) fetch();
-                ql.store(q_tile(st ^ 1));
-                gl.store(g_tile(st ^ 1));
-                put_info(st ^ 1);
+            for (int ks = 0; ks < KS; ++ks) {
+                if (ks + 1 < KS) read(ks + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                p = mma(f[ks & 1][0], k[ks], p);
+                if constexpr (F::VL) ds = mma(f[ks & 1][1], w[ks & 1], ds);
+                else ds = mma(f[ks & 1][1], v[ks], ds);
             }
+            Frag<DT> c[2][2];
+            auto read_c = [&](int i) {             // element block i % DB of 16 rows
+                c[i & 1][0] = cf.read(O, qb * 32 + i / DB * 16, i % DB);
+                c[i & 1][1] = cf.read(Q, qb * 32 + i / DB * 16, i % DB);
+            };
+            read_c(0);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 ls = *reinterpret_cast<const float4*>(&info[st][0][qb * 32 + 2 * i + 4 * h]);
+                const float4 de = *reinterpret_cast<const float4*>(&info[st][1][qb * 32 + 2 * i + 4 * h]);
+                const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[i + e] = __builtin_amdgcn_exp2f(fmaf(p[i + e], a.c, -l4[e]));
+                    ds[i + e] = p[i + e] * (ds[i + e] - d4[e]);
+                    if (decltype(some)::value && at + uint32_t(2 * i + e) >= n)
+                        p[i + e] = ds[i + e] = 0.f;
+                }
+            }
+            scaled.apply(ds, dk);
+            Frag<DT> fp, fs;
+#pragma unroll
+            for (int i = 0; i < 2 * DB; ++i) {
+                const int t = i / DB, db = i % DB;
+                if (i + 1 < 2 * DB) read_c(i + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                if (db == 0) {
+                    fp = results<DT>(p, t);
+                    fs = results<DT>(ds, t);
+                }
+                dv[db] = mma(c[i & 1][0], fp, dv[db]);
+                dk[db] = mma(c[i & 1][1], fs, dk[db]);
+            }
+        }
+    };
+    if (steps > 0) {
+        if (a.D < DP) {
+            clear<F::NT>(lds, 4 * F::TILE + F::VTILE);
             __syncthreads();
         }
+        if constexpr (F::VL) {
+            using TV = Tiles<DT, DP, 128, F::NT>;
+            key_tiles<TV>(a, a.v, b, sq, hk, ES).load(values, key0, sq.lk, a.D);
+        }
+        fetch(0, 0);
+        auto step = [&](int i, auto st, auto some) __attribute__((always_inline)) {
+            if (threadIdx.x < F::QT) {
+                info[st][0][threadIdx.x] = il;
+                info[st][1][threadIdx.x] = id;
+            }
+            arrived();
+            __syncthreads();
+            if (i + 1 < steps) fetch(i + 1, 1 - st);
+            const int r0 = row_of(i);
+            if (!decltype(some)::value || (r0 < hi_max && r0 + F::QT > lo_min))
+                step_of(r0, st, some);
+        };
+        // pairs of tiles whose rows see all keys in a loop of their own, as in the forward
+        auto whole = [&](int i) {
+            return row_of(i) >= all_lo && row_of(i) + F::QT <= min(hi, all_hi);
+        };
+        for (int i = 0; i < steps;) {
+            if ((i & 1) == 0) {
+                while (i + 1 < steps && whole(i) && whole(i + 1)) {
+                    step(i, std::integral_constant<int, 0>{}, std::false_type{});
+                    step(i + 1, std::integral_constant<int, 1>{}, std::false_type{});
+                    i += 2;
+                }
+                if (i >= steps) break;
+            }
+            step(i, i & 1, std::true_type{});
+            ++i;
+        }
+    }
+    const float up = DT == kF16 ? 0x1p-10f : 1.f, f = a.scale * up / scaled.up;
+    if (shared) {
+        if (j >= sq.lk) return;
+        float* share = share_of(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) + (j - key0) * a.D;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = 32 * db + 8 * i + 4 * h;
+                if (d >= a.D) continue;
+                store_scaled<kF32>(reinterpret_cast<char*>(share), d, dk[db], i, f, true);
+                store_scaled<kF32>(reinterpret_cast<char*>(share + 128 * a.D), d, dv[db], i, up, true);
+            }
+        return;
     }
     if (packed_k ? j >= sq.lk : j >= a.Sk) return;
     char* dkp = head_of(g.dk, packed_k, b, sq.k0, hk, ES) + int64_t(j) * g.dk.row * ES;
     char* dvp = head_of(g.dv, packed_k, b, sq.k0, hk, ES) + int64_t(j) * g.dv.row * ES;
-    const float up = DT == kF16 ? 0x1p-10f : 1.f, f = a.scale * up / scaled.up;
     const bool live = key_lo < key_hi;             // is seen
 #pragma unroll
     for (int db = 0; db < DB; ++db)
@@ -407,17 +551,82 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnArgs a, AttnGrads g, co
         }
 }
 
-}  // namespace
-
-size_t attn_bwd_workspace_bytes(const AttnArgs& a, int64_t)
+// Adds the shares of the key tiles whose rows were parted, in their order: a thread 4
+// elements of a key.
+template <int DT>
+__global__ __launch_bounds__(256) void k_attn_dkv_join(AttnArgs a, AttnGrads g, DkvParts pt,
+                                                       int tiles)
 {
-    return size_t(a.B) * size_t(a.KV) * size_t(a.G) * size_t(a.Sq) * 4;        // delta
+    constexpr int ES = DT == kF32 ? 4 : 2;
+    const uint32_t head = blockIdx.x / uint32_t(tiles), tile = blockIdx.x % uint32_t(tiles);
+    const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
+    const Sequence sq = sequence_of(a, b);
+    const int key0 = int(tile) * 128, quads = a.D / 4;
+    if (key0 >= sq.lk) return;
+    int lo, hi, x;
+    seen_by(a, sq, key0, lo, x);
+    seen_by(a, sq, min(key0 + 128, sq.lk) - 1, x, hi);
+    if (hi - lo <= pt.chunk) return;
+    const int parts = (hi - lo + pt.chunk - 1) / pt.chunk;
+    const bool packed_k = a.k_starts != nullptr;
+    for (int i = int(threadIdx.x); i < min(128, sq.lk - key0) * quads; i += 256) {
+        const int j = i / quads, d = i % quads * 4;
+        seen_by(a, sq, key0 + j, lo, hi);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lo < hi) {
+                for (int p = 0; p < parts; ++p) {
+                    const float4 u = *reinterpret_cast<const float4*>(
+                        share_of(pt, head, uint32_t(tiles), tile, p, a.D) + (which * 128 + j) * a.D + d);
+                    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+                }
+            }
+            const Heads& out = which ? g.dv : g.dk;
+            store4<DT>(head_of(out, packed_k, b, sq.k0, hk, ES) + int64_t(key0 + j) * out.row * ES, d,
+                       v.x, v.y, v.z, v.w);
+        }
+    }
 }
 
-void launch_attn_backward(const AttnArgs& a, const AttnGrads& g, int dtype, int64_t, void* ws,
+// Workgroups of a key tile's rows: two for every CU in all, and twice as many where a window
+// gives key tiles different numbers of rows, which two resident workgroups a CU do not even
+// out (twice 4096 causal tokens of 32 heads on 8: 890 us in one part, 640 in two and 28 to
+// join them); each part at least 512 rows.
+DkvParts make_parts(const AttnArgs& a, int64_t cus)
+{
+    DkvParts pt{};
+    const int64_t wgs = int64_t(a.B) * a.KV * ceil_div(a.Sk, 128), rows = int64_t(a.Sq) * a.G;
+    const bool uneven = a.left < kAttnMaxLen || a.right < kAttnMaxLen;
+    const int64_t want = wgs > 0 ? ceil_div((uneven ? 4 : 2) * cus, wgs) : 1;
+    const int64_t parts = max64(1, min64(want, rows / 512));
+    // whole tiles of rows and whole groups
+    pt.chunk = int(max64(1, ceil_div(ceil_div(a.Sq, parts), 64)) * 64 * a.G);
+    pt.parts = int(max64(1, ceil_div(rows, pt.chunk)));
+    return pt;
+}
+
+size_t delta_bytes(const AttnArgs& a)
+{
+    return size_t(ceil_div(int64_t(a.B) * a.KV * a.G * a.Sq, 4)) * 16;
+}
+
+}  // namespace
+
+size_t attn_bwd_workspace_bytes(const AttnArgs& a, int64_t cus)
+{
+    const DkvParts pt = make_parts(a, cus);
+    const size_t shares = pt.parts < 2 ? 0 : size_t(a.B) * a.KV * size_t(ceil_div(a.Sk, 128)) *
+                                                 pt.parts * 2 * 128 * a.D * 4;
+    return delta_bytes(a) + shares;
+}
+
+void launch_attn_backward(const AttnArgs& a, const AttnGrads& g, int dtype, int64_t cus, void* ws,
                           hipStream_t s)
 {
     float* delta = static_cast<float*>(ws);
+    DkvParts pt = make_parts(a, cus);
+    pt.share = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(a));
     const int row_tiles = int(ceil_div(int64_t(a.Sq) * a.G, 128)), key_tiles = int(ceil_div(a.Sk, 128));
     const int64_t heads = int64_t(a.B) * a.KV;
     with_dtype(dtype, [&](auto d) {
@@ -428,12 +637,16 @@ void launch_attn_backward(const AttnArgs& a, const AttnGrads& g, int dtype, int6
                 hipLaunchKernelGGL((k_attn_dq<DT, DP>), dim3(unsigned(heads * row_tiles)),
                                    dim3(256), 0, s, a, g, delta, row_tiles);
             if (key_tiles > 0)
-                hipLaunchKernelGGL((k_attn_dkv<DT, DP>), dim3(unsigned(heads * key_tiles)),
-                                   dim3(256), 0, s, a, g, delta, key_tiles);
+                hipLaunchKernelGGL((k_attn_dkv<DT, DP>),
+                                   dim3(unsigned(heads * key_tiles), unsigned(pt.parts)), dim3(256),
+                                   0, s, a, g, delta, pt, key_tiles);
         };
         if (a.D <= 64) go(std::integral_constant<int, 64>{});
         else if (a.D <= 96) go(std::integral_constant<int, 96>{});
         else go(std::integral_constant<int, 128>{});
+        if (key_tiles > 0 && pt.parts > 1)
+            hipLaunchKernelGGL((k_attn_dkv_join<DT>), dim3(unsigned(heads * key_tiles)), dim3(256),
+                               0, s, a, g, pt, key_tiles);
     });
 }
 

@@ -33,16 +33,15 @@ struct FwdShape {
     static constexpr int NT = 64 * WQ * WK;
     static constexpr int KW = WK > 1 || DT == kF32 ? 32 : 64;    // keys of a wave's tile
     static constexpr int KT = KW * WK;
-    static constexpr int STAGES = WK > 1 ? 1 : 2;
-    static constexpr int SLOTS = KT * TileShape<DT, DP>::NC;     // of a tile
-    static constexpr int JOIN = WK > 1 ? WK * DP * 32 * 4 / 16 + WK * 32 * 8 / 16 : 0;
-    static constexpr int LDS = STAGES * 2 * SLOTS > JOIN ? STAGES * 2 * SLOTS : JOIN;
-    static constexpr int WAVES = DT == kF32 ? 1 : 2;             // of a SIMD at once
-};
-
-// What a wave knows of its rows.
-struct RowRange {
-    int lo_min, lo_max, hi_min, hi_max;      // of the visible keys' ends over its rows
+    // a tile in LDS; waves with keys of their own each fill theirs
+    static constexpr int ROWS = WK > 1 ? KW : KT, LOADERS = WK > 1 ? 64 : NT;
+    static constexpr int TILE = ROWS * TileShape<DT, DP>::PITCH;
+    static constexpr int STAGES = WK > 1 && DT == kF32 && DP > 64 ? 1 : 2;       // LDS ends there
+    static constexpr int WAVE = WK > 1 ? STAGES * 2 * TILE : 0;  // bytes of a wave
+    static constexpr int TILES = WK > 1 ? WK * WAVE : STAGES * 2 * TILE;
+    static constexpr int JOIN = WK > 1 ? WK * DP * 32 * 4 + WK * 32 * 8 : 0;
+    static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
+    static constexpr int WAVES = DT == kF32 || (WK > 1 && DP > 64) ? 1 : 2;      // of a SIMD
 };
 
 // The results of one row, d = d0 .. d0 + 3 of it at a time.
@@ -67,13 +66,14 @@ __global__ __launch_bounds__(64 * WQ * WK, (FwdShape<DT, DP, WQ, WK>::WAVES)) vo
     using F = FwdShape<DT, DP, WQ, WK>;
     using S = TileShape<DT, DP>;
     constexpr int ES = S::ES, KS = DP / 16, DB = DP / 32, KB = F::KW / 32;
-    __shared__ uint4 lds[F::LDS];
+    __shared__ uint4 space[F::LDS / 16];
+    char* const lds = reinterpret_cast<char*>(space);
 
     const int lane = threadIdx.x % 64, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wq = wave % WQ, wk = wave / WQ;
     uint32_t head, tile;
-    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), head, tile);
+    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), false, head, tile);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
     tile = uint32_t(tiles) - 1 - tile;             // causal rows with many keys first
     const Sequence sq = sequence_of(a, b);
@@ -82,21 +82,30 @@ __global__ __launch_bounds__(64 * WQ * WK, (FwdShape<DT, DP, WQ, WK>::WAVES)) vo
     const int tok = int(fast_div(uint32_t(r), a.group)), hq = hk * a.G + r - tok * a.G;
     const bool packed_q = a.q_starts != nullptr;
 
-    // the keys that the workgroup's rows see, and this wave's
-    int lo = 0, hi = 0;
+    // the keys that some of the workgroup's rows see, that all of them see, and that some
+    // of this wave's
+    int lo = 0, hi = 0, all_lo = 0, all_hi = 0;
     if (row0 < rows) {
-        int x;
-        visible(a, sq, int(fast_div(uint32_t(row0), a.group)), lo, x);
-        visible(a, sq, int(fast_div(uint32_t(min(row0 + 32 * WQ, rows) - 1), a.group)), x, hi);
+        visible(a, sq, int(fast_div(uint32_t(row0), a.group)), lo, all_hi);
+        visible(a, sq, int(fast_div(uint32_t(min(row0 + 32 * WQ, rows) - 1), a.group)), all_lo, hi);
+        lo = scalar(lo);
+        hi = scalar(hi);
+        all_lo = scalar(all_lo);
+        all_hi = scalar(all_hi);
     }
-    RowRange w{0, 0, 0, 0};
+    int lo_min = 0, hi_max = 0;
     if (r0 < rows) {
-        visible(a, sq, int(fast_div(uint32_t(r0), a.group)), w.lo_min, w.hi_min);
-        visible(a, sq, int(fast_div(uint32_t(min(r0 + 32, rows) - 1), a.group)), w.lo_max,
-                w.hi_max);
+        int x;
+        visible(a, sq, int(fast_div(uint32_t(r0), a.group)), lo_min, x);
+        visible(a, sq, int(fast_div(uint32_t(min(r0 + 32, rows) - 1), a.group)), x, hi_max);
+        lo_min = scalar(lo_min);
+        hi_max = scalar(hi_max);
     }
     int row_lo = 0, row_hi = 0;
-    if (r < rows) visible(a, sq, tok, row_lo, row_hi);
+    if (r < rows) {
+        visible(a, sq, tok, row_lo, row_hi);
+        row_hi = max(row_lo, row_hi);
+    }
 
     int steps = hi > lo ? (hi - lo + F::KT - 1) / F::KT : 0, step0 = 0;
     if (sp.splits > 1) {
@@ -114,109 +123,138 @@ __global__ __launch_bounds__(64 * WQ * WK, (FwdShape<DT, DP, WQ, WK>::WAVES)) vo
             if (r < rows && 16 * ks + 8 * h < a.D) q[ks] = frag_of<DT>(p + (16 * ks + 8 * h) * ES);
         }
     }
-    const char* kp = head_of(a.k, a.k_starts != nullptr, b, sq.k0, hk, ES);
-    const char* vp = head_of(a.v, a.k_starts != nullptr, b, sq.k0, hk, ES);
-    const int64_t kpitch = a.k.row * ES, vpitch = a.v.row * ES;
+    using T = Tiles<DT, DP, F::ROWS, F::LOADERS>;
+    const T keys = key_tiles<T>(a, a.k, b, sq, hk, ES), vals = key_tiles<T>(a, a.v, b, sq, hk, ES);
+    const RowFrags<DT, DP> rf;
+    const ColFrags<DT, DP> cf;
 
     f32x16_t o[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i) zero(o[i]);
     float m = -INFINITY, l = 0.f;
 
-    // A step: the next tile's keys are loaded over this tile's scores and its values over the
-    // rest, so that one set of registers carries both.
-    TileLoad<DT, DP, F::KT, F::NT> kl, vl;
-    auto fetch_k = [&](int step) { kl.load(kp, kpitch, lo + step * F::KT, hi, a.D); };
-    auto fetch_v = [&](int step) { vl.load(vp, vpitch, lo + step * F::KT, hi, a.D); };
-    auto k_tile = [&](int st) { return lds + st * 2 * F::SLOTS; };
-    auto v_tile = [&](int st) { return lds + (st * 2 + 1) * F::SLOTS; };
-
-    f32x16_t s[KB];
-    auto scores = [&](int k0, int st) {
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            zero(s[kb]);
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                s[kb] = mma(row_frag<DT, DP>(k_tile(st), wk * F::KW + kb * 32, ks), q[ks], s[kb]);
-        }
-        if (k0 < w.lo_max || k0 + F::KW > w.hi_min) {            // some row does not see all
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = k0 + kb * 32 + 8 * (i / 4) + 4 * h + i % 4;
-                    if (j < row_lo || j >= row_hi) s[kb][i] = -INFINITY;
-                }
-        }
+    auto tile_at = [&](int st, int v) { return lds + wk * F::WAVE + (2 * st + v) * F::TILE; };
+    auto fetch = [&](int step, int st) __attribute__((always_inline)) {
+        const int first = lo + step * F::KT + (WK > 1 ? wk * F::KW : 0);
+        keys.load(tile_at(st, 0), first, hi, a.D);
+        vals.load(tile_at(st, 1), first, hi, a.D);
     };
-    auto softmax = [&]() {
-        float mx = s[0][0];
+    // 32 keys of this wave after another, their fragments read a group ahead of the products
+    constexpr int GS = 2, NG = KB * KS / GS, VS = DB % 2 == 0 ? 2 : 3, VG = 2 * KB * DB / VS;
+    auto step_of = [&](int k0, int st, auto some) __attribute__((always_inline)) {
+        const char *K = tile_at(st, 0), *V = tile_at(st, 1);
+        f32x16_t s[KB];
+        Frag<DT> f[2][GS];
+        auto read = [&](int g) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+            for (int i = 0; i < GS; ++i)
+                f[g & 1][i] = rf.read(K, (g * GS + i) / KS * 32, (g * GS + i) % KS);
+        };
+        float mx = -INFINITY;
+        const uint32_t at = uint32_t(k0 + 4 * h - row_lo), n = uint32_t(row_hi - row_lo);
+        auto finish = [&](int kb) {                // hides keys, finds the largest score
+            if (decltype(some)::value) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (at + uint32_t(kb * 32 + 8 * (i / 4) + i % 4) >= n) s[kb][i] = -INFINITY;
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
+        };
+        read(0);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (g + 1 < NG) read(g + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < GS; ++i) {
+                const int kb = (g * GS + i) / KS, ks = (g * GS + i) % KS;
+                if (ks == 0) zero(s[kb]);
+                s[kb] = mma(f[g & 1][i], q[ks], s[kb]);
+                if (ks == 0 && kb > 0) finish(kb - 1);
+            }
+        }
+        finish(KB - 1);
+        Frag<DT> vf[2][VS];
+        auto read_v = [&](int g) {
+#pragma unroll
+            for (int i = 0; i < VS; ++i)
+                vf[g & 1][i] = cf.read(V, (g * VS + i) / DB * 16, (g * VS + i) % DB);
+        };
+        read_v(0);
         mx = both_max(mx);
         if (__any((mx - m) * a.c > kLazy)) {
             const float nm = fmaxf(m, mx);
-            const float f = __builtin_amdgcn_exp2f((m - (nm == -INFINITY ? 0.f : nm)) * a.c);
+            const float e = __builtin_amdgcn_exp2f((m - (nm == -INFINITY ? 0.f : nm)) * a.c);
             m = nm;
-            l *= f;
+            l *= e;
 #pragma unroll
             for (int i = 0; i < DB; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[i][e] *= f;
+                for (int j = 0; j < 16; ++j) o[i][j] *= e;
         }
         const float base = m == -INFINITY ? 0.f : m * a.c;
+        auto probs = [&](int t) {                  // of 16 keys
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], a.c, -base));
-                l += s[kb][i];
+            for (int i = 0; i < 8; ++i) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[t / 2][t % 2 * 8 + i], a.c, -base));
+                s[t / 2][t % 2 * 8 + i] = e;
+                l += e;
             }
-    };
-    auto values = [&](int st) {
+            return results<DT>(s[t / 2], t % 2);
+        };
+        Frag<DT> p = probs(0), next{};
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int g = 0; g < VG; ++g) {
+            if (g + 1 < VG) read_v(g + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const Frag<DT> p = results<DT>(s[kb], t);
-#pragma unroll
-                for (int i = 0; i < DB; ++i)
-                    o[i] = mma(col_frag<DT, DP>(v_tile(st), wk * F::KW + kb * 32 + 16 * t, i), p,
-                               o[i]);
+            for (int i = 0; i < VS; ++i) {
+                const int t = (g * VS + i) / DB, db = (g * VS + i) % DB;
+                if (db == 0 && t > 0) p = next;
+                o[db] = mma(vf[g & 1][i], p, o[db]);
+                if (db == 0 && t + 1 < 2 * KB) next = probs(t + 1);
             }
+        }
     };
 
     if (step0 < steps) {
-        fetch_k(step0);
-        fetch_v(step0);
-        kl.store(k_tile(0));
-        vl.store(v_tile(0));
-        __syncthreads();
-        for (int i = step0; i < steps; ++i) {
-            const int st = F::STAGES == 2 ? (i - step0) & 1 : 0, next = F::STAGES == 2 ? st ^ 1 : 0;
-            const int k0 = lo + i * F::KT + wk * F::KW;          // of this wave
-            const bool seen = k0 < w.hi_max && k0 + F::KW > w.lo_min, more = i + 1 < steps;
-            if (more) fetch_k(i + 1);
-            if (seen) scores(k0, st);
-            if (more && F::STAGES == 2) {
-                kl.store(k_tile(next));
-                fetch_v(i + 1);
-            }
-            if (more && F::STAGES == 1) fetch_v(i + 1);
-            if (seen) {
-                softmax();
-                values(st);
-            }
-            if (F::STAGES == 1) {
-                __syncthreads();                                 // all have read the tile
-                if (more) kl.store(k_tile(next));
-            }
-            if (more) vl.store(v_tile(next));
+        if (a.D < DP) {
+            clear<F::NT>(lds, F::TILES);
             __syncthreads();
         }
+        fetch(step0, 0);
+        auto step = [&](int i, auto st, auto some) __attribute__((always_inline)) {
+            arrived();
+            if (WK == 1) __syncthreads();          // here, and the other stage read by all
+            if (F::STAGES == 2 && i + 1 < steps) fetch(i + 1, 1 - st);
+            const int k0 = lo + i * F::KT + wk * F::KW;          // of this wave
+            if (!decltype(some)::value || (k0 < hi_max && k0 + F::KW > lo_min))
+                step_of(k0, st, some);
+            if (F::STAGES == 1 && i + 1 < steps) {
+                arrived();
+                fetch(i + 1, 0);
+            }
+        };
+        // Pairs of tiles that all rows see whole in a loop of their own, without masks and with
+        // constant stages.
+        const int first = lo + (WK > 1 ? wk * F::KW : 0);
+        auto whole = [&](int i) {
+            return first + i * F::KT >= all_lo && first + i * F::KT + (WK > 1 ? F::KW : F::KT) <= all_hi;
+        };
+        for (int i = step0; i < steps;) {
+            if (F::STAGES == 2 && ((i - step0) & 1) == 0) {
+                while (i + 1 < steps && whole(i) && whole(i + 1)) {
+                    step(i, std::integral_constant<int, 0>{}, std::false_type{});
+                    step(i + 1, std::integral_constant<int, 1>{}, std::false_type{});
+                    i += 2;
+                }
+                if (i >= steps) break;
+            }
+            step(i, F::STAGES == 2 ? (i - step0) & 1 : 0, std::true_type{});
+            ++i;
+        }
+        __syncthreads();
     }
     l = both_sum(l);
     if (r >= rows) {                               // of a tile's other rows' keys

@@ -56,11 +56,18 @@ __device__ __forceinline__ void sequence_side(const int32_t* starts, const int32
     }
 }
 
+// The same in every lane, and in scalar registers.
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 __device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int b)
 {
     Sequence s;
     sequence_side(a.q_starts, a.q_lens, b, a.q_rows, a.Sq, s.q0, s.lq);
     sequence_side(a.k_starts, a.k_lens, b, a.k_rows, a.Sk, s.k0, s.lk);
+    s.q0 = uint32_t(scalar(int(s.q0)));            // starts are below 2^31
+    s.k0 = uint32_t(scalar(int(s.k0)));
+    s.lq = scalar(s.lq);
+    s.lk = scalar(s.lk);
     return s;
 }
 
@@ -169,114 +176,200 @@ __device__ __forceinline__ float both_sum(float v)
 // ---------------------------------------------------------------------------
 // tiles of rows in LDS
 
+__device__ __forceinline__ uint32_t lds_address(const char* p)
+{
+    return uint32_t(uintptr_t((const __attribute__((address_space(3))) char*)p));
+}
+
+// 16 bytes a lane from base + offset to LDS, lane l's to dst + 16 * l (dst the same in all
+// lanes).  In assembly, since the compiler would wait for it before any other access to
+// LDS; the wait is arrived()'s.
+__device__ __forceinline__ void to_lds(const char* base, uint32_t offset, uint32_t dst)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(dst), "v"(offset), "s"(base)
+                 : "memory");
+}
+
 // DP: the head's elements as the kernel counts them, a multiple of 32 (those past D are
 // zeros).  Rows are NC 16-byte chunks apart, a power of two; chunk c of row r lies at
 // place c XOR a mix of r, so that
 //   - 16 lanes that read one chunk of 16 neighbouring rows meet 16 different bank quads,
 //   - 32 lanes that read 64 bytes of each of 4 neighbouring rows (a transposing read)
 //     cover all 64 banks.
+// (No bank conflicts by the counters.)  A lane's reads of a tile are then one address XOR
+// constants plus constants.
 template <int DT, int DP>
 struct TileShape {
     static constexpr int ES = DT == kF32 ? 4 : 2;
     static constexpr int E = 16 / ES;                            // elements of a chunk
     static constexpr int USED = DP / E;                          // chunks of a row
     static constexpr int NC = (DP <= 64 ? 64 : 128) / E;
+    static constexpr int PITCH = NC * 16;                        // bytes
     static_assert(DP % 32 == 0 && DP <= 128, "head sizes");
 
-    static __device__ __forceinline__ int slot(int r, int c)
+    static __device__ __forceinline__ uint32_t mix(uint32_t r)
     {
-        if constexpr (NC == 8) return r * 8 + (c ^ (((r & 2) << 1) | ((r >> 2) & 3)));
-        else if constexpr (DT == kF32) return r * NC + (c ^ (((r & 7) << 1) | ((r >> 3) & 1)));
-        else return r * NC + (c ^ (((r & 3) << 2) | ((r >> 2) & 3)));
+        if constexpr (NC == 8) return ((r & 2) << 1) | ((r >> 2) & 3);
+        else if constexpr (DT == kF32) return ((r & 7) << 1) | ((r >> 3) & 1);
+        else return ((r & 3) << 2) | ((r >> 2) & 3);
+    }
+    static __device__ __forceinline__ uint32_t place(uint32_t r, uint32_t c)
+    {
+        return r * PITCH + 16 * (c ^ mix(r));
     }
 };
 
-// ROWS rows on their way from global memory to LDS through NT threads' registers.
+// Rows of a head, or of a group of heads (attn.hpp), in global memory, and how NT threads
+// take ROWS of them to LDS: thread t has place t % NC of row t / NC of each pass of PER rows.
+//
+// Whole tiles of aligned rows go there directly, without registers, each wave writing the
+// 64 chunks from a scalar place on: the mix is undone in the addresses that the lanes read.
+// The caller waits for them (arrived()).  Everything else (the end of a sequence, rows not
+// at 16-byte distances) goes through registers before load() returns; rows from `end` on
+// and elements from D on are zeros there.  (Elements from D on of direct tiles are not
+// written at all: clear() the stages first.)
 template <int DT, int DP, int ROWS, int NT>
-struct TileLoad {
+struct Tiles {
     using S = TileShape<DT, DP>;
-    static constexpr int PER = NT / S::NC;                       // rows a pass
-    static constexpr int N = ROWS / PER;
+    static constexpr int PER = NT / S::NC, N = ROWS / PER;
     static_assert(NT % S::NC == 0 && ROWS % PER == 0, "threads for a tile");
-    uint4 q[N];
 
-    // rows first .. first + ROWS - 1, row r at at(r); those from `end` on, and elements from
-    // D on, are zeros
-    template <class At>
-    __device__ __forceinline__ void load_at(At&& at, int first, int end, int D)
+    const char* p;                    // the (first query) head
+    int64_t row, head;                // bytes
+    FastDiv group;
+    int G;
+    uint32_t offset;                  // of this thread's row within a pass
+    bool direct;
+
+    __device__ __forceinline__ Tiles(const char* p_, int64_t row_, int64_t head_, FastDiv group_,
+                                     int G_)
+        : p(p_), row(row_), head(head_), group(group_), G(G_), offset(0)
     {
-        const int c = threadIdx.x % S::NC, r = first + int(threadIdx.x) / S::NC;
-        const bool in = c * S::E < D;
+        const int64_t most = row * (PER / G + 1) + head * G;     // of a pass's offsets
+        direct = PER % G == 0 && most < (int64_t(1) << 31) &&
+                 ((reinterpret_cast<uintptr_t>(p) | uintptr_t(row) | uintptr_t(head)) & 15) == 0;
+        if (direct) {
+            const uint32_t r = threadIdx.x % NT / S::NC, t = G == 1 ? r : fast_div(r, group);
+            offset = t * uint32_t(row) + (r - t * G) * uint32_t(head);
+        }
+    }
+
+    // rows first .. first + ROWS - 1, first a multiple of the group, D elements of each
+    __device__ __forceinline__ void load(char* tile, int first, int end, int D) const
+    {
+        const uint32_t th = threadIdx.x % NT, c = th % S::NC, r = th / S::NC;
+        if (direct && first + ROWS <= end) {
+            const char* base = p + int64_t(G == 1 ? first : scalar(int(fast_div(uint32_t(first), group)))) * row;
+            const uint32_t dst = uint32_t(scalar(int(lds_address(tile) + th / 64 * 1024)));
+            const int64_t pass = PER / G * row;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t chunk = c ^ S::mix(r + i * PER);
+                if (S::USED == S::NC ? int(chunk) * S::E < D || D == DP
+                                     : int(chunk) * S::E < D)
+                    to_lds(base + i * pass, offset + 16 * chunk, dst + i * NT * 16);
+            }
+            return;
+        }
+        uint4 q[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            const int at = first + int(r) + i * PER;
             q[i] = make_uint4(0, 0, 0, 0);
-            if (in && r + i * PER < end) q[i] = load16_any(at(r + i * PER) + c * 16);
+            if (int(c) * S::E < D && at < end) {
+                const int t = G == 1 ? at : int(fast_div(uint32_t(at), group));
+                q[i] = load16_any(p + t * row + int64_t(at - t * G) * head + c * 16);
+            }
         }
-    }
-    // rows `pitch` bytes apart
-    __device__ __forceinline__ void load(const char* head, int64_t pitch, int first, int end,
-                                         int D)
-    {
-        load_at([&](int r) { return head + int64_t(r) * pitch; }, first, end, D);
-    }
-    __device__ __forceinline__ void store(uint4* tile) const
-    {
-        const int c = threadIdx.x % S::NC, r = int(threadIdx.x) / S::NC;
-        if (S::USED < S::NC && c >= S::USED) return;
 #pragma unroll
-        for (int i = 0; i < N; ++i) tile[S::slot(r + i * PER, c)] = q[i];
+        for (int i = 0; i < N; ++i)
+            if (S::USED == S::NC || c < S::USED)
+                *reinterpret_cast<uint4*>(tile + S::place(r + i * PER, c)) = q[i];
     }
 };
 
-// Operand A of rows row0 .. row0 + 31 at elements 16 * ks .. 16 * ks + 15.
-template <int DT, int DP>
-__device__ __forceinline__ Frag<DT> row_frag(const uint4* tile, int row0, int ks)
+// Zeros in `bytes` (a multiple of 16) of LDS.
+template <int NT>
+__device__ __forceinline__ void clear(char* p, int bytes)
 {
-    using S = TileShape<DT, DP>;
-    const int lane = threadIdx.x % 64, r = row0 + lane % 32, h = lane / 32;
-    Frag<DT> f;
-#pragma unroll
-    for (int i = 0; i < (DT == kF32 ? 2 : 1); ++i) {
-        const uint4 q = tile[S::slot(r, DT == kF32 ? 4 * ks + 2 * h + i : 2 * ks + h)];
-        f.w[4 * i] = q.x; f.w[4 * i + 1] = q.y; f.w[4 * i + 2] = q.z; f.w[4 * i + 3] = q.w;
-    }
-    return f;
+    for (int i = int(threadIdx.x) * 16; i < bytes; i += NT * 16)
+        *reinterpret_cast<uint4*>(p + i) = make_uint4(0, 0, 0, 0);
 }
 
-// Operand A of the transposed tile: elements 32 * db .. 32 * db + 31, summed over the 16
-// rows from row0 in the order in which a lane holds a product's results: element i of half
-// h is row row0 + 8 * (i / 4) + 4 * h + i % 4.
-template <int DT, int DP>
-__device__ __forceinline__ Frag<DT> col_frag(const uint4* tile, int row0, int db)
+// Every direct load of this wave has arrived, and every read of LDS has returned (so that a
+// direct load may take its place).
+__device__ __forceinline__ void arrived()
 {
-    using S = TileShape<DT, DP>;
-    const int lane = threadIdx.x % 64, h = lane / 32;
-    Frag<DT> f;
-    if constexpr (DT == kF32) {
-        const int d = 32 * db + lane % 32;
-        const float* t = reinterpret_cast<const float*>(tile);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = row0 + 8 * (i / 4) + 4 * h + i % 4;
-            f.w[i] = __float_as_uint(t[S::slot(r, d / 4) * 4 + d % 4]);
-        }
-    } else {
-        // 16 lanes read 16 columns of 4 rows, 4 columns each, and get one column's 4 rows
-        const int l = lane % 16, col = 32 * db + (lane & 16) + 4 * (l % 4);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = row0 + 8 * j + 4 * h + l / 4;
-            const char* p = reinterpret_cast<const char*>(tile + S::slot(r, col / 8)) +
-                            (col & 4) * 2;
-            const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4_t*)p);
-            const uint2 u = __builtin_bit_cast(uint2, v);
-            f.w[2 * j] = u.x;
-            f.w[2 * j + 1] = u.y;
-        }
-    }
-    return f;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
+
+// A lane's operand A of rows row0 .. row0 + 31 at elements 16 * ks .. 16 * ks + 15, row0 a
+// multiple of 16: at(lane) once, then read.
+template <int DT, int DP>
+struct RowFrags {
+    using S = TileShape<DT, DP>;
+    uint32_t at;
+
+    __device__ __forceinline__ RowFrags()
+    {
+        const uint32_t lane = threadIdx.x % 64, h = lane / 32;
+        at = S::place(lane % 32, DT == kF32 ? 2 * h : h);
+    }
+    __device__ __forceinline__ Frag<DT> read(const char* tile, int row0, int ks) const
+    {
+        Frag<DT> f;
+#pragma unroll
+        for (int i = 0; i < (DT == kF32 ? 2 : 1); ++i) {
+            const uint32_t x = DT == kF32 ? at ^ uint32_t(64 * ks + 16 * i) : at ^ uint32_t(32 * ks);
+            const uint4 q = *reinterpret_cast<const uint4*>(tile + row0 * S::PITCH + x);
+            f.w[4 * i] = q.x; f.w[4 * i + 1] = q.y; f.w[4 * i + 2] = q.z; f.w[4 * i + 3] = q.w;
+        }
+        return f;
+    }
+};
+
+// A lane's operand A of the transposed tile: elements 32 * db .. 32 * db + 31, summed over
+// the 16 rows from row0 (a multiple of 16) in the order in which a lane holds a product's
+// results: element i of half h is row row0 + 8 * (i / 4) + 4 * h + i % 4.
+template <int DT, int DP>
+struct ColFrags {
+    using S = TileShape<DT, DP>;
+    uint32_t at;
+
+    __device__ __forceinline__ ColFrags()
+    {
+        const uint32_t lane = threadIdx.x % 64, h = lane / 32, l = lane % 16;
+        if constexpr (DT == kF32)
+            at = S::place(4 * h, (lane % 32) / 4) + 4 * (lane % 4);
+        else          // 16 lanes read 16 columns of 4 rows, 4 columns each, and get one column's 4
+            at = S::place(4 * h + l / 4, ((lane / 16) & 1) * 2 + (l % 4) / 2) + 8 * (l % 2);
+    }
+    __device__ __forceinline__ Frag<DT> read(const char* tile, int row0, int db) const
+    {
+        Frag<DT> f;
+        if constexpr (DT == kF32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x = at ^ uint32_t(128 * db + 32 * (i % 4) + 16 * (i / 4));
+                f.w[i] = *reinterpret_cast<const uint32_t*>(
+                    tile + (row0 + 8 * (i / 4) + i % 4) * S::PITCH + x);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t x = at ^ uint32_t(64 * db + 32 * j);
+                const char* p = tile + (row0 + 8 * j) * S::PITCH + x;
+                const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4_t*)p);
+                const uint2 u = __builtin_bit_cast(uint2, v);
+                f.w[2 * j] = u.x;
+                f.w[2 * j + 1] = u.y;
+            }
+        }
+        return f;
+    }
+};
 
 // Four consecutive elements d .. d + 3 of a row, rounded.
 template <int DT>
@@ -292,25 +385,28 @@ __device__ __forceinline__ void store4(char* row, int d, float a, float b, float
     }
 }
 
-// Rows of a key head's group (attn.hpp) in global memory.
-struct GroupRows {
-    const char* p;                    // the first query head of the group
-    int64_t row, head;                // bytes
-    FastDiv group;
-    int G;
-
-    __device__ __forceinline__ const char* operator()(int r) const
-    {
-        const int t = int(fast_div(uint32_t(r), group));
-        return p + int64_t(t) * row + int64_t(r - t * G) * head;
-    }
-};
-
-__device__ __forceinline__ GroupRows group_rows(const AttnArgs& a, const Heads& t, int b,
-                                                const Sequence& s, int hk, int es)
+// A row of a key head's group (attn.hpp) in global memory, and tiles of such rows.
+__device__ __forceinline__ const char* group_row(const AttnArgs& a, const Heads& t, int b,
+                                                 const Sequence& s, int hk, int r, int es)
 {
-    return GroupRows{head_of(t, a.q_starts != nullptr, b, s.q0, hk * a.G, es), t.row * es,
-                     t.head * es, a.group, a.G};
+    const int tok = int(fast_div(uint32_t(r), a.group));
+    return head_of(t, a.q_starts != nullptr, b, s.q0, hk * a.G + r - tok * a.G, es) +
+           int64_t(tok) * t.row * es;
+}
+
+template <class T>
+__device__ __forceinline__ T group_tiles(const AttnArgs& a, const Heads& t, int b,
+                                         const Sequence& s, int hk, int es)
+{
+    return T(head_of(t, a.q_starts != nullptr, b, s.q0, hk * a.G, es), t.row * es, t.head * es,
+             a.group, a.G);
+}
+
+template <class T>
+__device__ __forceinline__ T key_tiles(const AttnArgs& a, const Heads& t, int b, const Sequence& s,
+                                       int hk, int es)
+{
+    return T(head_of(t, a.k_starts != nullptr, b, s.k0, hk, es), t.row * es, 0, FastDiv{}, 1);
 }
 
 // The place of a row's log-sum-exp.
@@ -323,17 +419,19 @@ __device__ __forceinline__ int64_t lse_index(const AttnArgs& a, const Sequence& 
 
 // Which workgroup of a key head, and which key head, blockIdx.x stands for: consecutive
 // workgroups go to the 8 XCDs in turn, so where the heads divide by 8 all workgroups of
-// one run on one XCD, whose L2 then holds its keys once.
-__device__ __forceinline__ void head_and_tile(uint32_t heads, uint32_t tiles, uint32_t& head,
-                                              uint32_t& tile)
+// one run on one XCD, whose L2 then holds its keys once.  An XCD takes its heads one after
+// another, or (across) their first tiles before their second ones.
+__device__ __forceinline__ void head_and_tile(uint32_t heads, uint32_t tiles, bool across,
+                                              uint32_t& head, uint32_t& tile)
 {
-    const uint32_t b = blockIdx.x;
-    if (heads % 8 == 0) {
-        head = b % 8 + 8 * (b / 8 / tiles);
-        tile = b / 8 % tiles;
+    const uint32_t xcds = heads % 8 == 0 ? 8 : 1;
+    const uint32_t x = blockIdx.x % xcds, i = blockIdx.x / xcds;
+    if (across) {
+        tile = i / (heads / xcds);
+        head = x + xcds * (i % (heads / xcds));
     } else {
-        head = b / tiles;
-        tile = b % tiles;
+        head = x + xcds * (i / tiles);
+        tile = i % tiles;
     }
 }
 
