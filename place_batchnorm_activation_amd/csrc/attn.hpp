@@ -38,9 +38,6 @@ struct AttnGrads {
     Heads dout, dq, dk, dv;
 };
 
-// Workgroups that share a key head's work along its keys (forward) or rows (backward).
-int attn_fwd_splits(const AttnArgs& a, int64_t cus);
-int attn_bwd_splits(const AttnArgs& a, int64_t cus);
 size_t attn_fwd_workspace_bytes(const AttnArgs& a, int64_t cus);
 size_t attn_bwd_workspace_bytes(const AttnArgs& a, int64_t cus);
 void launch_attn_forward(const AttnArgs& a, int dtype, int64_t cus, void* ws, hipStream_t s);

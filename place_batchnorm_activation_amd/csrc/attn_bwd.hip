@@ -70,6 +70,48 @@ __device__ __forceinline__ void store_scaled(char* row, int d, const f32x16_t& v
     else store4<DT>(row, d, 0.f, 0.f, 0.f, 0.f);
 }
 
+// A tile of 128 rows (keys) whose keys (rows) are cut among workgroups, `chunk` each: where a
+// tile takes more than one, their shares of its gradients go through the workspace.
+struct Parts {
+    int parts, chunk;
+    float* share;                     // [head][tile][part][dQ, or dK and dV][128][D]
+};
+
+template <int N>
+__device__ __forceinline__ float* share_of(const Parts& pt, uint32_t head, uint32_t tiles,
+                                           uint32_t tile, int part, int D)
+{
+    return pt.share + ((int64_t(head) * tiles + tile) * pt.parts + part) * N * 128 * D;
+}
+
+// The sum of a tile's shares of four elements, in their order.
+template <int N>
+__device__ __forceinline__ float4 sum_shares(const Parts& pt, uint32_t head, uint32_t tiles,
+                                             uint32_t tile, int parts, int D, int at)
+{
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const float4 u = *reinterpret_cast<const float4*>(
+            share_of<N>(pt, head, tiles, tile, p, D) + at);
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    }
+    return v;
+}
+
+// Keys [lo, hi) that some of rows row0 .. row0 + 127 see.
+__device__ __forceinline__ void seen_keys(const AttnArgs& a, const Sequence& s, int row0, int& lo,
+                                          int& hi)
+{
+    const int rows = s.lq * a.G;
+    lo = hi = 0;
+    if (row0 >= rows) return;
+    int x;
+    visible(a, s, int(fast_div(uint32_t(row0), a.group)), lo, x);
+    visible(a, s, int(fast_div(uint32_t(min(row0 + 128, rows) - 1), a.group)), x, hi);
+    hi = max(lo, hi);
+}
+
 // ---------------------------------------------------------------------------
 // dQ and delta
 
@@ -82,7 +124,8 @@ struct DqShape {
 
 template <int DT, int DP>
 __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnArgs a, AttnGrads g,
-                                                                          float* delta, int tiles)
+                                                                          float* delta, Parts pt,
+                                                                          int tiles)
 {
     using F = DqShape<DT, DP>;
     using S = TileShape<DT, DP>;
@@ -104,14 +147,24 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
 
     // the keys that some of the workgroup's rows see, that all of them see, and that some
     // of this wave's
-    int lo = 0, hi = 0, all_lo = 0, all_hi = 0, lo_min = 0, hi_max = 0;
+    int lo, hi, all_lo = 0, all_hi = 0, lo_min = 0, hi_max = 0;
+    seen_keys(a, sq, row0, lo, hi);
+    lo = scalar(lo);
+    hi = scalar(hi);
     if (row0 < rows) {
-        visible(a, sq, int(fast_div(uint32_t(row0), a.group)), lo, all_hi);
-        visible(a, sq, int(fast_div(uint32_t(min(row0 + 128, rows) - 1), a.group)), all_lo, hi);
-        lo = scalar(lo);
-        hi = scalar(hi);
+        int x;
+        visible(a, sq, int(fast_div(uint32_t(row0), a.group)), x, all_hi);
+        visible(a, sq, int(fast_div(uint32_t(min(row0 + 128, rows) - 1), a.group)), all_lo, x);
         all_lo = scalar(all_lo);
         all_hi = scalar(all_hi);
+    }
+    // this workgroup's part of the keys
+    const bool shared = pt.parts > 1 && hi - lo > pt.chunk;
+    if (pt.parts > 1) {
+        const int64_t first = int64_t(lo) + int64_t(blockIdx.y) * pt.chunk;
+        if (blockIdx.y > 0 && first >= hi) return;
+        lo = int(first);
+        hi = int(min(int64_t(hi), first + pt.chunk));
     }
     if (r0 < rows) {
         int x;
@@ -150,7 +203,7 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
         lse2 = lse == -INFINITY ? INFINITY : lse * kLog2eA;
     }
     dl = both_sum(dl);
-    if (r < rows && h == 0) delta[(int64_t(b) * a.KV + hk) * all_rows + r] = dl;
+    if (r < rows && h == 0 && blockIdx.y == 0) delta[(int64_t(b) * a.KV + hk) * all_rows + r] = dl;
 
     using T = Tiles<DT, DP, F::KT, F::NT>;
     const T keys = key_tiles<T>(a, a.k, b, sq, hk, ES), vals = key_tiles<T>(a, a.v, b, sq, hk, ES);
@@ -236,7 +289,7 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
         }
         fetch(0, 0);
         auto step = [&](int i, auto st, auto some) __attribute__((always_inline)) {
-            arrived();
+            arrived<>();
             __syncthreads();
             if (i + 1 < steps) fetch(i + 1, 1 - st);
             const int k0 = lo + i * F::KT;
@@ -245,7 +298,7 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
         };
         // pairs of tiles that all rows see whole in a loop of their own, as in the forward
         auto whole = [&](int i) {
-            return lo + i * F::KT >= all_lo && lo + (i + 1) * F::KT <= all_hi;
+            return lo + i * F::KT >= all_lo && lo + (i + 1) * F::KT <= min(hi, all_hi);
         };
         for (int i = 0; i < steps;) {
             if ((i & 1) == 0) {
@@ -259,6 +312,20 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
             step(i, i & 1, std::true_type{});
             ++i;
         }
+    }
+    if (shared) {
+        float* share = share_of<1>(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) + (r - row0) * a.D;
+        if (r >= rows) return;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int d = 32 * db + 8 * i + 4 * h;
+                if (d < a.D)
+                    store_scaled<kF32>(reinterpret_cast<char*>(share), d, dq[db], i,
+                                       a.scale / scaled.up, true);
+            }
+        return;
     }
     // rows of a padded batch behind its length are written too, as zeros
     if (packed_q ? r >= rows : r >= all_rows) return;
@@ -274,21 +341,35 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
         }
 }
 
+// Adds the shares of the row tiles whose keys were parted: a thread 4 elements of a row.
+template <int DT>
+__global__ __launch_bounds__(256) void k_attn_dq_join(AttnArgs a, AttnGrads g, Parts pt, int tiles)
+{
+    constexpr int ES = DT == kF32 ? 4 : 2;
+    const uint32_t head = blockIdx.x / uint32_t(tiles), tile = blockIdx.x % uint32_t(tiles);
+    const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
+    const Sequence sq = sequence_of(a, b);
+    const int row0 = int(tile) * 128, quads = a.D / 4, all_rows = a.Sq * a.G, rows = sq.lq * a.G;
+    int lo, hi;
+    seen_keys(a, sq, row0, lo, hi);
+    if (hi - lo <= pt.chunk) return;
+    const int parts = (hi - lo + pt.chunk - 1) / pt.chunk;
+    const int end = min(128, (a.q_starts ? rows : all_rows) - row0);
+    const int i = int(blockIdx.y) * 256 + int(threadIdx.x);
+    if (i < end * quads) {
+        const int r = i / quads, d = i % quads * 4;
+        const int tok = int(fast_div(uint32_t(row0 + r), a.group)), hq = hk * a.G + row0 + r - tok * a.G;
+        // a row that sees no key holds 0 * infinity of its tile's others
+        const bool live = row0 + r < rows && a.lse[lse_index(a, sq, b, hq, tok)] != -INFINITY;
+        const float4 v = sum_shares<1>(pt, head, uint32_t(tiles), tile, live ? parts : 0, a.D,
+                                       r * a.D + d);
+        store4<DT>(head_of(g.dq, a.q_starts != nullptr, b, sq.q0, hq, ES) + int64_t(tok) * g.dq.row * ES,
+                   d, v.x, v.y, v.z, v.w);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // dK and dV
-
-// A key tile's rows cut among workgroups: `chunk` rows each, whose shares of dK and dV go
-// through the workspace where a tile's rows take more than one.
-struct DkvParts {
-    int parts, chunk;
-    float* share;                     // [head][tile][part][dK, dV][128 keys][D]
-};
-
-__device__ __forceinline__ float* share_of(const DkvParts& pt, uint32_t head, uint32_t tiles,
-                                           uint32_t tile, int part, int D)
-{
-    return pt.share + ((int64_t(head) * tiles + tile) * pt.parts + part) * 2 * 128 * D;
-}
 
 // Rows [lo, hi) of the group that see key x.
 __device__ __forceinline__ void seen_by(const AttnArgs& a, const Sequence& s, int x, int& lo, int& hi)
@@ -316,7 +397,7 @@ template <int DT, int DP>
 __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(AttnArgs a,
                                                                             AttnGrads g,
                                                                             const float* delta,
-                                                                            DkvParts pt,
+                                                                            Parts pt,
                                                                             int tiles)
 {
     using F = DkvShape<DT, DP>;
@@ -497,7 +578,7 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
                 info[st][0][threadIdx.x] = il;
                 info[st][1][threadIdx.x] = id;
             }
-            arrived();
+            arrived<>();
             __syncthreads();
             if (i + 1 < steps) fetch(i + 1, 1 - st);
             const int r0 = row_of(i);
@@ -524,7 +605,7 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
     const float up = DT == kF16 ? 0x1p-10f : 1.f, f = a.scale * up / scaled.up;
     if (shared) {
         if (j >= sq.lk) return;
-        float* share = share_of(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) + (j - key0) * a.D;
+        float* share = share_of<2>(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) + (j - key0) * a.D;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -554,7 +635,7 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
 // Adds the shares of the key tiles whose rows were parted, in their order: a thread 4
 // elements of a key.
 template <int DT>
-__global__ __launch_bounds__(256) void k_attn_dkv_join(AttnArgs a, AttnGrads g, DkvParts pt,
+__global__ __launch_bounds__(256) void k_attn_dkv_join(AttnArgs a, AttnGrads g, Parts pt,
                                                        int tiles)
 {
     constexpr int ES = DT == kF32 ? 4 : 2;
@@ -569,84 +650,107 @@ __global__ __launch_bounds__(256) void k_attn_dkv_join(AttnArgs a, AttnGrads g, 
     if (hi - lo <= pt.chunk) return;
     const int parts = (hi - lo + pt.chunk - 1) / pt.chunk;
     const bool packed_k = a.k_starts != nullptr;
-    for (int i = int(threadIdx.x); i < min(128, sq.lk - key0) * quads; i += 256) {
+    const int end = min(128, (packed_k ? sq.lk : a.Sk) - key0);
+    const int i = int(blockIdx.y) * 256 + int(threadIdx.x), which = int(blockIdx.z);
+    if (i < end * quads) {
         const int j = i / quads, d = i % quads * 4;
         seen_by(a, sq, key0 + j, lo, hi);
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (lo < hi) {
-                for (int p = 0; p < parts; ++p) {
-                    const float4 u = *reinterpret_cast<const float4*>(
-                        share_of(pt, head, uint32_t(tiles), tile, p, a.D) + (which * 128 + j) * a.D + d);
-                    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-                }
-            }
-            const Heads& out = which ? g.dv : g.dk;
-            store4<DT>(head_of(out, packed_k, b, sq.k0, hk, ES) + int64_t(key0 + j) * out.row * ES, d,
-                       v.x, v.y, v.z, v.w);
-        }
+        const bool live = key0 + j < sq.lk && lo < hi;
+        const float4 v = sum_shares<2>(pt, head, uint32_t(tiles), tile, live ? parts : 0, a.D,
+                                       (which * 128 + j) * a.D + d);
+        const Heads& out = which ? g.dv : g.dk;
+        store4<DT>(head_of(out, packed_k, b, sq.k0, hk, ES) + int64_t(key0 + j) * out.row * ES, d,
+                   v.x, v.y, v.z, v.w);
     }
+}
+
+// Workgroups of a row tile's keys: two for every CU in all, each part at least 128 keys.
+Parts dq_parts(const AttnArgs& a, int64_t cus)
+{
+    Parts pt{};
+    const int64_t wgs = int64_t(a.B) * a.KV * ceil_div(int64_t(a.Sq) * a.G, 128);
+    const int64_t want = wgs > 0 && wgs < cus ? ceil_div(2 * cus, wgs) : 1;
+    const int64_t parts = max64(1, min64(want, a.Sk / 128));
+    pt.chunk = int(max64(1, ceil_div(ceil_div(a.Sk, parts), 64)) * 64);
+    pt.parts = int(max64(1, ceil_div(a.Sk, pt.chunk)));
+    return pt;
 }
 
 // Workgroups of a key tile's rows: two for every CU in all, and twice as many where a window
 // gives key tiles different numbers of rows, which two resident workgroups a CU do not even
 // out (twice 4096 causal tokens of 32 heads on 8: 890 us in one part, 640 in two and 28 to
-// join them); each part at least 512 rows.
-DkvParts make_parts(const AttnArgs& a, int64_t cus)
+// join them); each part at least 128 rows.
+Parts dkv_parts(const AttnArgs& a, int64_t cus)
 {
-    DkvParts pt{};
+    Parts pt{};
     const int64_t wgs = int64_t(a.B) * a.KV * ceil_div(a.Sk, 128), rows = int64_t(a.Sq) * a.G;
     const bool uneven = a.left < kAttnMaxLen || a.right < kAttnMaxLen;
     const int64_t want = wgs > 0 ? ceil_div((uneven ? 4 : 2) * cus, wgs) : 1;
-    const int64_t parts = max64(1, min64(want, rows / 512));
+    const int64_t parts = max64(1, min64(want, rows / 128));
     // whole tiles of rows and whole groups
-    pt.chunk = int(max64(1, ceil_div(ceil_div(a.Sq, parts), 64)) * 64 * a.G);
+    pt.chunk = int(max64(1, ceil_div(ceil_div(rows, parts), 64 * a.G)) * 64 * a.G);
     pt.parts = int(max64(1, ceil_div(rows, pt.chunk)));
     return pt;
 }
 
-size_t delta_bytes(const AttnArgs& a)
+// delta [B][KV][rows], the shares of dQ, the shares of dK and dV
+struct BwdSpace {
+    Parts dq, dkv;
+    size_t bytes;
+};
+
+BwdSpace bwd_space(const AttnArgs& a, int64_t cus, void* ws)
 {
-    return size_t(ceil_div(int64_t(a.B) * a.KV * a.G * a.Sq, 4)) * 16;
+    BwdSpace w{dq_parts(a, cus), dkv_parts(a, cus), 0};
+    const size_t heads = size_t(a.B) * a.KV, tile = size_t(128) * a.D * 4;
+    const int64_t rows = int64_t(a.Sq) * a.G;
+    auto take = [&](size_t bytes) {
+        char* p = static_cast<char*>(ws) + w.bytes;
+        w.bytes += (bytes + 15) / 16 * 16;
+        return reinterpret_cast<float*>(p);
+    };
+    take(heads * size_t(rows) * 4);
+    w.dq.share = take(w.dq.parts > 1 ? heads * ceil_div(rows, 128) * w.dq.parts * tile : 0);
+    w.dkv.share = take(w.dkv.parts > 1 ? heads * ceil_div(a.Sk, 128) * w.dkv.parts * 2 * tile : 0);
+    return w;
 }
 
 }  // namespace
 
 size_t attn_bwd_workspace_bytes(const AttnArgs& a, int64_t cus)
 {
-    const DkvParts pt = make_parts(a, cus);
-    const size_t shares = pt.parts < 2 ? 0 : size_t(a.B) * a.KV * size_t(ceil_div(a.Sk, 128)) *
-                                                 pt.parts * 2 * 128 * a.D * 4;
-    return delta_bytes(a) + shares;
+    return bwd_space(a, cus, nullptr).bytes;
 }
 
 void launch_attn_backward(const AttnArgs& a, const AttnGrads& g, int dtype, int64_t cus, void* ws,
                           hipStream_t s)
 {
     float* delta = static_cast<float*>(ws);
-    DkvParts pt = make_parts(a, cus);
-    pt.share = reinterpret_cast<float*>(static_cast<char*>(ws) + delta_bytes(a));
+    const BwdSpace w = bwd_space(a, cus, ws);
     const int row_tiles = int(ceil_div(int64_t(a.Sq) * a.G, 128)), key_tiles = int(ceil_div(a.Sk, 128));
     const int64_t heads = int64_t(a.B) * a.KV;
+    const unsigned row_wgs = unsigned(heads * row_tiles), key_wgs = unsigned(heads * key_tiles);
+    const unsigned slices = unsigned(ceil_div(128 * (a.D / 4), 256));
     with_dtype(dtype, [&](auto d) {
         constexpr int DT = decltype(d)::value;
         auto go = [&](auto p) {
             constexpr int DP = decltype(p)::value;
             if (row_tiles > 0)
-                hipLaunchKernelGGL((k_attn_dq<DT, DP>), dim3(unsigned(heads * row_tiles)),
-                                   dim3(256), 0, s, a, g, delta, row_tiles);
+                hipLaunchKernelGGL((k_attn_dq<DT, DP>), dim3(row_wgs, unsigned(w.dq.parts)),
+                                   dim3(256), 0, s, a, g, delta, w.dq, row_tiles);
             if (key_tiles > 0)
-                hipLaunchKernelGGL((k_attn_dkv<DT, DP>),
-                                   dim3(unsigned(heads * key_tiles), unsigned(pt.parts)), dim3(256),
-                                   0, s, a, g, delta, pt, key_tiles);
+                hipLaunchKernelGGL((k_attn_dkv<DT, DP>), dim3(key_wgs, unsigned(w.dkv.parts)),
+                                   dim3(256), 0, s, a, g, delta, w.dkv, key_tiles);
         };
         if (a.D <= 64) go(std::integral_constant<int, 64>{});
         else if (a.D <= 96) go(std::integral_constant<int, 96>{});
         else go(std::integral_constant<int, 128>{});
-        if (key_tiles > 0 && pt.parts > 1)
-            hipLaunchKernelGGL((k_attn_dkv_join<DT>), dim3(unsigned(heads * key_tiles)), dim3(256),
-                               0, s, a, g, pt, key_tiles);
+        if (row_tiles > 0 && w.dq.parts > 1)
+            hipLaunchKernelGGL((k_attn_dq_join<DT>), dim3(row_wgs, slices), dim3(256), 0, s, a, g, w.dq,
+                               row_tiles);
+        if (key_tiles > 0 && w.dkv.parts > 1)
+            hipLaunchKernelGGL((k_attn_dkv_join<DT>), dim3(key_wgs, slices, 2), dim3(256), 0, s, a, g, w.dkv,
+                               key_tiles);
     });
 }
 

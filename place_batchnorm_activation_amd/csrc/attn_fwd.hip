@@ -9,39 +9,34 @@
 // lane, one exchange with the other half of the wave a tile.
 //
 // Many rows: a workgroup of 4 waves x 32 rows shares the tiles of keys in LDS, two stages,
-// the next tile's loads in flight.  At most 32 rows (single tokens): the 4 waves take the
-// same rows and a quarter of each tile's keys, and their shares are joined in LDS.  Few
+// the next tile's loads in flight.  At most 32 rows (single tokens): workgroups of one wave,
+// three stages, no barriers: what counts there is bytes in flight (96 KB a CU; with 64 KB in
+// groups of four waves the same caches were read at 4.6 instead of 5.1 TB/s).  Few
 // workgroups: the keys are cut among several, whose shares (O, m, l in fp32) go through
-// the workspace and are joined in their order by a second kernel.
+// the workspace and are joined by a second kernel.
 #include "attn_tile.hpp"
 
 namespace iabn {
 
 namespace {
-
 constexpr float kLazy = 8.f;         // binary orders that the running maximum may lag behind
 
 struct FwdSplit {
-    int splits;
+    int splits, chunk;               // workgroups of the keys, and keys of each
     float* o;                        // [split][row][D]
     float2* ml;                      // [split][row]
     int64_t rows;                    // B * KV * Sq * G
 };
 
-template <int DT, int DP, int WQ, int WK>
+// WQ waves of 32 rows.
+template <int DT, int DP, int WQ>
 struct FwdShape {
-    static constexpr int NT = 64 * WQ * WK;
-    static constexpr int KW = WK > 1 || DT == kF32 ? 32 : 64;    // keys of a wave's tile
-    static constexpr int KT = KW * WK;
-    // a tile in LDS; waves with keys of their own each fill theirs
-    static constexpr int ROWS = WK > 1 ? KW : KT, LOADERS = WK > 1 ? 64 : NT;
-    static constexpr int TILE = ROWS * TileShape<DT, DP>::PITCH;
-    static constexpr int STAGES = WK > 1 && DT == kF32 && DP > 64 ? 1 : 2;       // LDS ends there
-    static constexpr int WAVE = WK > 1 ? STAGES * 2 * TILE : 0;  // bytes of a wave
-    static constexpr int TILES = WK > 1 ? WK * WAVE : STAGES * 2 * TILE;
-    static constexpr int JOIN = WK > 1 ? WK * DP * 32 * 4 + WK * 32 * 8 : 0;
-    static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
-    static constexpr int WAVES = DT == kF32 || (WK > 1 && DP > 64) ? 1 : 2;      // of a SIMD
+    static constexpr int NT = 64 * WQ;
+    static constexpr int KT = WQ == 1 || DT == kF32 ? 32 : 64;   // keys of a tile
+    static constexpr int TILE = KT * TileShape<DT, DP>::PITCH;
+    static constexpr int STAGES = WQ == 1 && DT != kF32 ? 3 : 2;
+    static constexpr int LDS = STAGES * 2 * TILE;
+    static constexpr int WAVES = WQ == 1 || DT == kF32 ? 1 : 2;  // of a SIMD
 };
 
 // The results of one row, d = d0 .. d0 + 3 of it at a time.
@@ -59,26 +54,25 @@ struct RowOut {
     }
 };
 
-template <int DT, int DP, int WQ, int WK>
-__global__ __launch_bounds__(64 * WQ * WK, (FwdShape<DT, DP, WQ, WK>::WAVES)) void k_attn_fwd(
+template <int DT, int DP, int WQ>
+__global__ __launch_bounds__(64 * WQ, (FwdShape<DT, DP, WQ>::WAVES)) void k_attn_fwd(
     AttnArgs a, FwdSplit sp, int tiles)
 {
-    using F = FwdShape<DT, DP, WQ, WK>;
+    using F = FwdShape<DT, DP, WQ>;
     using S = TileShape<DT, DP>;
-    constexpr int ES = S::ES, KS = DP / 16, DB = DP / 32, KB = F::KW / 32;
+    constexpr int ES = S::ES, KS = DP / 16, DB = DP / 32, KB = F::KT / 32;
     __shared__ uint4 space[F::LDS / 16];
     char* const lds = reinterpret_cast<char*>(space);
 
     const int lane = threadIdx.x % 64, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int wq = wave % WQ, wk = wave / WQ;
     uint32_t head, tile;
     head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), false, head, tile);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
     tile = uint32_t(tiles) - 1 - tile;             // causal rows with many keys first
     const Sequence sq = sequence_of(a, b);
     const int rows = sq.lq * a.G, all_rows = a.Sq * a.G;
-    const int row0 = int(tile) * 32 * WQ, r0 = row0 + wq * 32, r = r0 + lane % 32;
+    const int row0 = int(tile) * 32 * WQ, r0 = row0 + wave * 32, r = r0 + lane % 32;
     const int tok = int(fast_div(uint32_t(r), a.group)), hq = hk * a.G + r - tok * a.G;
     const bool packed_q = a.q_starts != nullptr;
 
@@ -107,13 +101,32 @@ __global__ __launch_bounds__(64 * WQ * WK, (FwdShape<DT, DP, WQ, WK>::WAVES)) vo
         row_hi = max(row_lo, row_hi);
     }
 
-    int steps = hi > lo ? (hi - lo + F::KT - 1) / F::KT : 0, step0 = 0;
-    if (sp.splits > 1) {
-        const int per = (steps + sp.splits - 1) / sp.splits;
-        step0 = min(steps, int(blockIdx.y) * per);
-        steps = min(steps, step0 + per);
+    if (sp.splits > 1) {                           // this workgroup's part of them
+        const int64_t first = int64_t(lo) + int64_t(blockIdx.y) * sp.chunk;
+        hi = first < hi ? int(min(int64_t(hi), first + sp.chunk)) : lo;
+        lo = first < hi ? int(first) : hi;
     }
+    const int steps = hi > lo ? (hi - lo + F::KT - 1) / F::KT : 0;
 
+    using T = Tiles<DT, DP, F::KT, F::NT>;
+    const T keys = key_tiles<T>(a, a.k, b, sq, hk, ES), vals = key_tiles<T>(a, a.v, b, sq, hk, ES);
+    const RowFrags<DT, DP> rf;
+    const ColFrags<DT, DP> cf;
+
+    auto tile_at = [&](int st, int v) { return lds + (2 * st + v) * F::TILE; };
+    auto fetch = [&](int step, int st) __attribute__((always_inline)) {
+        keys.load(tile_at(st, 0), lo + step * F::KT, hi, a.D);
+        vals.load(tile_at(st, 1), lo + step * F::KT, hi, a.D);
+    };
+    if (steps > 0) {
+        if (a.D < DP) {
+            clear<F::NT>(lds, F::LDS);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i + 1 < F::STAGES; ++i)
+            if (i < steps) fetch(i, i);
+    }
     Frag<DT> q[KS];
     {
         const char* p = head_of(a.q, packed_q, b, sq.q0, hq, ES) + int64_t(tok) * a.q.row * ES;
@@ -123,22 +136,11 @@ __global__ __launch_bounds__(64 * WQ * WK, (FwdShape<DT, DP, WQ, WK>::WAVES)) vo
             if (r < rows && 16 * ks + 8 * h < a.D) q[ks] = frag_of<DT>(p + (16 * ks + 8 * h) * ES);
         }
     }
-    using T = Tiles<DT, DP, F::ROWS, F::LOADERS>;
-    const T keys = key_tiles<T>(a, a.k, b, sq, hk, ES), vals = key_tiles<T>(a, a.v, b, sq, hk, ES);
-    const RowFrags<DT, DP> rf;
-    const ColFrags<DT, DP> cf;
-
     f32x16_t o[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i) zero(o[i]);
     float m = -INFINITY, l = 0.f;
 
-    auto tile_at = [&](int st, int v) { return lds + wk * F::WAVE + (2 * st + v) * F::TILE; };
-    auto fetch = [&](int step, int st) __attribute__((always_inline)) {
-        const int first = lo + step * F::KT + (WK > 1 ? wk * F::KW : 0);
-        keys.load(tile_at(st, 0), first, hi, a.D);
-        vals.load(tile_at(st, 1), first, hi, a.D);
-    };
     // 32 keys of this wave after another, their fragments read a group ahead of the products
     constexpr int GS = 2, NG = KB * KS / GS, VS = DB % 2 == 0 ? 2 : 3, VG = 2 * KB * DB / VS;
     auto step_of = [&](int k0, int st, auto some) __attribute__((always_inline)) {
@@ -218,43 +220,34 @@ __global__ __launch_bounds__(64 * WQ * WK, (FwdShape<DT, DP, WQ, WK>::WAVES)) vo
         }
     };
 
-    if (step0 < steps) {
-        if (a.D < DP) {
-            clear<F::NT>(lds, F::TILES);
-            __syncthreads();
-        }
-        fetch(step0, 0);
-        auto step = [&](int i, auto st, auto some) __attribute__((always_inline)) {
-            arrived();
-            if (WK == 1) __syncthreads();          // here, and the other stage read by all
-            if (F::STAGES == 2 && i + 1 < steps) fetch(i + 1, 1 - st);
-            const int k0 = lo + i * F::KT + wk * F::KW;          // of this wave
-            if (!decltype(some)::value || (k0 < hi_max && k0 + F::KW > lo_min))
-                step_of(k0, st, some);
-            if (F::STAGES == 1 && i + 1 < steps) {
-                arrived();
-                fetch(i + 1, 0);
+    // Step i: its tile is here (the next ones may be on their way), the last one's stage is free
+    // for the tile STAGES - 1 ahead.
+    auto step = [&](int i, auto st, auto some) __attribute__((always_inline)) {
+        if (F::STAGES > 2 && i + 1 < steps) arrived<(F::STAGES - 2) * 2 * T::N>();
+        else arrived<0>();
+        if (WQ > 1) __syncthreads();
+        if (i + F::STAGES - 1 < steps) fetch(i + F::STAGES - 1, (st + F::STAGES - 1) % F::STAGES);
+        const int k0 = lo + i * F::KT;
+        if (!decltype(some)::value || (k0 < hi_max && k0 + F::KT > lo_min)) step_of(k0, st, some);
+    };
+    // Runs of tiles that all rows see whole in a loop of their own, without masks and with
+    // constant stages.
+    auto whole = [&](int i) {
+        return lo + i * F::KT >= all_lo && lo + (i + 1) * F::KT <= min(hi, all_hi);
+    };
+    for (int i = 0; i < steps;) {
+        if (i % F::STAGES == 0) {
+            while (i + F::STAGES <= steps && whole(i) && whole(i + F::STAGES - 1)) {
+                step(i, std::integral_constant<int, 0>{}, std::false_type{});
+                step(i + 1, std::integral_constant<int, 1>{}, std::false_type{});
+                if constexpr (F::STAGES > 2)
+                    step(i + 2, std::integral_constant<int, 2>{}, std::false_type{});
+                i += F::STAGES;
             }
-        };
-        // Pairs of tiles that all rows see whole in a loop of their own, without masks and with
-        // constant stages.
-        const int first = lo + (WK > 1 ? wk * F::KW : 0);
-        auto whole = [&](int i) {
-            return first + i * F::KT >= all_lo && first + i * F::KT + (WK > 1 ? F::KW : F::KT) <= all_hi;
-        };
-        for (int i = step0; i < steps;) {
-            if (F::STAGES == 2 && ((i - step0) & 1) == 0) {
-                while (i + 1 < steps && whole(i) && whole(i + 1)) {
-                    step(i, std::integral_constant<int, 0>{}, std::false_type{});
-                    step(i + 1, std::integral_constant<int, 1>{}, std::false_type{});
-                    i += 2;
-                }
-                if (i >= steps) break;
-            }
-            step(i, F::STAGES == 2 ? (i - step0) & 1 : 0, std::true_type{});
-            ++i;
+            if (i >= steps) break;
         }
-        __syncthreads();
+        step(i, i % F::STAGES, std::true_type{});
+        ++i;
     }
     l = both_sum(l);
     if (r >= rows) {                               // of a tile's other rows' keys
@@ -281,64 +274,32 @@ __global__ __launch_bounds__(64 * WQ * WK, (FwdShape<DT, DP, WQ, WK>::WAVES)) vo
         }
     };
     auto write = [&](int db, const f32x16_t& v) {
-        if (!mine) return;
+        if (!mine || (sp.splits > 1 && steps == 0)) return;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const int d = 32 * db + 8 * g + 4 * h;
             if (d < a.D) ro.put(d, v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
         }
     };
-    if constexpr (WK == 1) {
-        statistics(m, l);
+    statistics(m, l);
 #pragma unroll
-        for (int i = 0; i < DB; ++i) write(i, o[i]);
-    } else {
-        // the tiles have been read by all waves: their place holds the shares
-        float* share = reinterpret_cast<float*>(lds);            // [wave][db][16][64]
-        float2* ml = reinterpret_cast<float2*>(share + WK * DB * 16 * 64);
-        if (h == 0) ml[wk * 32 + lane] = make_float2(m, l);
-        __syncthreads();
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int k = 0; k < WK; ++k) M = fmaxf(M, ml[k * 32 + lane % 32].x);
-        const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-        for (int k = 0; k < WK; ++k) {
-            const float2 x = ml[k * 32 + lane % 32];
-            L += x.y * __builtin_amdgcn_exp2f((x.x - ref) * a.c);
-        }
-        const float f = __builtin_amdgcn_exp2f((m - ref) * a.c);
-#pragma unroll
-        for (int i = 0; i < DB; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) share[((wk * DB + i) * 16 + e) * 64 + lane] = o[i][e] * f;
-        __syncthreads();
-        if (wk < DB) {
-            f32x16_t v;
-            zero(v);
-#pragma unroll
-            for (int k = 0; k < WK; ++k)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += share[((k * DB + wk) * 16 + e) * 64 + lane];
-            statistics(M, L);                                    // every wave the same
-            write(wk, v);
-        }
-    }
+    for (int i = 0; i < DB; ++i) write(i, o[i]);
 }
 
-// Joins the shares of the key axis, in their order: a thread 4 elements of a row.
+// Joins the shares of the key axis.  Few shares: a thread 4 elements of a row, the shares in
+// their order.
 template <int DT>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, FwdSplit sp, int quads)
+__global__ __launch_bounds__(256) void k_attn_join_few(AttnArgs a, FwdSplit sp, int quads)
 {
     constexpr int ES = DT == kF32 ? 4 : 2;
     const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
     const int64_t id = i / quads;
     const int d = int(i % quads) * 4;
     if (id >= sp.rows) return;
-    const int all_rows = a.Sq * a.G;
-    const int64_t head = id / all_rows;
-    const int b = int(head / a.KV), hk = int(head % a.KV), r = int(id % all_rows);
-    const Sequence sq = sequence_of(a, b);
+    const int all = a.Sq * a.G;
+    const int64_t head = id / all;
+    const int b = int(head / a.KV), hk = int(head % a.KV), r = int(id % all);
+    const Sequence sq = lane_sequence(a, b);
     if (a.q_starts && r >= sq.lq * a.G) return;
     const int tok = int(fast_div(uint32_t(r), a.group)), hq = hk * a.G + r - tok * a.G;
     float M = -INFINITY;
@@ -347,6 +308,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, FwdSplit sp, int 
     float L = 0.f, v[4] = {};
     for (int s = 0; s < sp.splits; ++s) {
         const float2 x = sp.ml[s * sp.rows + id];
+        if (x.y == 0.f) continue;                  // saw no key
         const float f = __builtin_amdgcn_exp2f((x.x - ref) * a.c);
         const float4 p = *reinterpret_cast<const float4*>(sp.o + (s * sp.rows + id) * a.D + d);
         L += x.y * f;
@@ -363,6 +325,74 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, FwdSplit sp, int 
     }
 }
 
+// More: a wave a row, 4 elements a lane, the halves of the wave every other share, eight of
+// them in flight.
+template <int DT>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, FwdSplit sp)
+{
+    constexpr int ES = DT == kF32 ? 4 : 2;
+    const int64_t id = int64_t(blockIdx.x) * 4 + scalar(int(threadIdx.x / 64));
+    if (id >= sp.rows) return;
+    const int lane = threadIdx.x % 64, h = lane / 32, d = lane % 32 * 4;
+    const int all = a.Sq * a.G;
+    const int64_t head = id / all;
+    const int b = int(head / a.KV), hk = int(head % a.KV), r = int(id % all);
+    const Sequence sq = sequence_of(a, b);
+    if (a.q_starts && r >= sq.lq * a.G) return;
+    const int tok = int(fast_div(uint32_t(r), a.group)), hq = hk * a.G + r - tok * a.G;
+    const float2* ml = sp.ml + id;
+    const float* o = sp.o + id * a.D + d;
+    float M = -INFINITY;
+    for (int s = lane; s < sp.splits; s += 64) M = fmaxf(M, ml[s * sp.rows].x);
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor(M, x, 64));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f, v[4] = {};
+    for (int s0 = 0; s0 < sp.splits; s0 += 64) {   // 64 shares' weights, one a lane
+        float f = 0.f;
+        if (s0 + lane < sp.splits) {
+            const float2 x = ml[(s0 + lane) * sp.rows];
+            if (x.y != 0.f) f = __builtin_amdgcn_exp2f((x.x - ref) * a.c);      // 0: saw no key
+            L += x.y * f;
+        }
+        const int n = min(64, sp.splits - s0);
+        for (int s1 = 0; s1 < n; s1 += 16) {
+            float4 p[8];
+            float w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int s = s1 + 2 * u + h;
+                w[u] = __shfl(f, s, 64);           // past the last: 0
+                p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (d < a.D && w[u] != 0.f)
+                    p[u] = *reinterpret_cast<const float4*>(o + (s0 + s) * sp.rows * a.D);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                v[0] = fmaf(p[u].x, w[u], v[0]);
+                v[1] = fmaf(p[u].y, w[u], v[1]);
+                v[2] = fmaf(p[u].z, w[u], v[2]);
+                v[3] = fmaf(p[u].w, w[u], v[3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) L += __shfl_xor(L, x, 64);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = both_sum(v[e]);
+    if (h == 0 && d < a.D) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        char* out = head_of(a.out, a.q_starts != nullptr, b, sq.q0, hq, ES) +
+                    int64_t(tok) * a.out.row * ES;
+        if (inv == 0.f) store4<DT>(out, d, 0.f, 0.f, 0.f, 0.f);
+        else store4<DT>(out, d, v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    }
+    if (lane == 0 && a.lse) {
+        const float lse = L == 0.f ? -INFINITY : (M * a.c + __builtin_amdgcn_logf(L)) * kLn2A;
+        a.lse[lse_index(a, sq, b, hq, tok)] = lse;
+    }
+}
+
 // At most 32 rows a key head: the waves share the rows and part the keys.
 bool few_rows(const AttnArgs& a) { return int64_t(a.Sq) * a.G <= 32; }
 
@@ -373,27 +403,37 @@ int64_t row_tiles(const AttnArgs& a)
 
 int64_t all_rows(const AttnArgs& a) { return int64_t(a.B) * a.KV * a.Sq * a.G; }
 
-}  // namespace
-
-// Two workgroups a CU, each at least 256 keys.
-int attn_fwd_splits(const AttnArgs& a, int64_t cus)
+// Keys of a workgroup where the rows' tiles are too few for the card: two workgroups a CU in
+// all, four of the small ones for few rows, each at least 128 keys.  Sequences of other lengths have fewer parts of the same
+// size.  (us of both kernels for one token over 8 caches of up to 32768, 8 key heads of 128:
+// 2 a CU 195, 4 118, 8 125, 16 135.  Least keys 64, 128, 256: 517 keys of 8 heads of 64 11, 13, 16;
+// 8192 of 8 of 128 27, 20, 21; 1027 rows over 777 keys, f32, 36, 32, 40.)
+FwdSplit make_split(const AttnArgs& a, int64_t cus)
 {
+    FwdSplit sp{};
+    sp.splits = 1;
+    sp.chunk = a.Sk;
+    sp.rows = all_rows(a);
     const int64_t wgs = int64_t(a.B) * a.KV * row_tiles(a);
-    if (wgs >= cus || wgs == 0) return 1;
-    return int(max64(1, min64(min64(ceil_div(2 * cus, wgs), ceil_div(a.Sk, 256)), 512)));
+    if (wgs == 0 || wgs >= cus) return sp;
+    const int64_t parts = min64(ceil_div((few_rows(a) ? 4 : 2) * cus, wgs), 512);
+    const int64_t chunk = ceil_div(max64(128, ceil_div(a.Sk, parts)), 64) * 64;
+    sp.splits = int(max64(1, ceil_div(a.Sk, chunk)));
+    sp.chunk = int(chunk);
+    return sp;
 }
+
+}  // namespace
 
 size_t attn_fwd_workspace_bytes(const AttnArgs& a, int64_t cus)
 {
-    const int64_t splits = attn_fwd_splits(a, cus);
+    const int64_t splits = make_split(a, cus).splits;
     return splits > 1 ? size_t(splits) * size_t(all_rows(a)) * size_t(4 * a.D + 8) : 0;
 }
 
 void launch_attn_forward(const AttnArgs& a, int dtype, int64_t cus, void* ws, hipStream_t s)
 {
-    FwdSplit sp{};
-    sp.splits = attn_fwd_splits(a, cus);
-    sp.rows = all_rows(a);
+    FwdSplit sp = make_split(a, cus);
     sp.o = static_cast<float*>(ws);
     sp.ml = reinterpret_cast<float2*>(sp.o + sp.splits * sp.rows * a.D);
     const int tiles = int(row_tiles(a));
@@ -403,18 +443,21 @@ void launch_attn_forward(const AttnArgs& a, int dtype, int64_t cus, void* ws, hi
         auto go = [&](auto p) {
             constexpr int DP = decltype(p)::value;
             if (few_rows(a))
-                hipLaunchKernelGGL((k_attn_fwd<DT, DP, 1, 4>), grid, dim3(256), 0, s, a, sp, tiles);
+                hipLaunchKernelGGL((k_attn_fwd<DT, DP, 1>), grid, dim3(64), 0, s, a, sp, tiles);
             else
-                hipLaunchKernelGGL((k_attn_fwd<DT, DP, 4, 1>), grid, dim3(256), 0, s, a, sp, tiles);
+                hipLaunchKernelGGL((k_attn_fwd<DT, DP, 4>), grid, dim3(256), 0, s, a, sp, tiles);
         };
         if (a.D <= 64) go(std::integral_constant<int, 64>{});
         else if (a.D <= 96) go(std::integral_constant<int, 96>{});
         else go(std::integral_constant<int, 128>{});
-        if (sp.splits > 1) {
-            const int quads = a.D / 4;
-            hipLaunchKernelGGL((k_attn_join<DT>), dim3(unsigned(ceil_div(sp.rows * quads, 256))),
-                               dim3(256), 0, s, a, sp, quads);
-        }
+        // us for 4 shares of 12324 rows: 6 in order, 12 a wave a row; 16 of 256: 17 against 5
+        if (sp.splits > 1 && sp.splits < 8)
+            hipLaunchKernelGGL((k_attn_join_few<DT>),
+                               dim3(unsigned(ceil_div(sp.rows * (a.D / 4), 256))), dim3(256), 0, s,
+                               a, sp, a.D / 4);
+        else if (sp.splits > 1)
+            hipLaunchKernelGGL((k_attn_join<DT>), dim3(unsigned(ceil_div(sp.rows, 4))), dim3(256),
+                               0, s, a, sp);
     });
 }
 

@@ -59,11 +59,18 @@ __device__ __forceinline__ void sequence_side(const int32_t* starts, const int32
 // The same in every lane, and in scalar registers.
 __device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-__device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int b)
+__device__ __forceinline__ Sequence lane_sequence(const AttnArgs& a, int b)
 {
     Sequence s;
     sequence_side(a.q_starts, a.q_lens, b, a.q_rows, a.Sq, s.q0, s.lq);
     sequence_side(a.k_starts, a.k_lens, b, a.k_rows, a.Sk, s.k0, s.lk);
+    return s;
+}
+
+// b the same in all lanes
+__device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, int b)
+{
+    Sequence s = lane_sequence(a, b);
     s.q0 = uint32_t(scalar(int(s.q0)));            // starts are below 2^31
     s.k0 = uint32_t(scalar(int(s.k0)));
     s.lq = scalar(s.lq);
@@ -297,11 +304,12 @@ __device__ __forceinline__ void clear(char* p, int bytes)
         *reinterpret_cast<uint4*>(p + i) = make_uint4(0, 0, 0, 0);
 }
 
-// Every direct load of this wave has arrived, and every read of LDS has returned (so that a
-// direct load may take its place).
+// All but the last LEFT direct loads of this wave have arrived (loads return in their
+// order), and every read of LDS has returned, so that a direct load may take its place.
+template <int LEFT = 0>
 __device__ __forceinline__ void arrived()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LEFT) : "memory");
 }
 
 // A lane's operand A of rows row0 .. row0 + 31 at elements 16 * ks .. 16 * ks + 15, row0 a
