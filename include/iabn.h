@@ -567,7 +567,7 @@ typedef enum iabn_pos { IABN_POS_I32 = 0, IABN_POS_I64 = 1, IABN_POS_F32 = 2 } i
  * 2*pairs on are copied.  inv_freq float64 [pairs] (radians a step) and axis int32 [pairs] (NULL: all
  * 0; values are cut to [0, axes)) on the device.  positions: coordinate c of token (b, r)
  * at b*pos_batch + r*pos_row + c, of pos_type; pos_batch 0 shares them among the batch.
- * Angles are formed in float64. */
+ * Angles are formed in float64.  rows below 2^30. */
 typedef struct iabn_rotary_spec {
     int64_t batch, rows, head_dim, pairs, axes;
     iabn_dtype dtype;

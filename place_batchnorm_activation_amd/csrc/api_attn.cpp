@@ -313,7 +313,8 @@ iabn_status iabn_rotary(const iabn_rotary_spec* r, const iabn_heads* q, int64_t 
         return IABN_ERR_INVALID_ARG;
     if (r->head_dim > 65536 || r->axes > 65536 || q_heads + k_heads > 65536)
         return IABN_ERR_UNSUPPORTED;
-    if (double(r->batch) * double(r->rows) > 2147483647. * 4.) return IABN_ERR_UNSUPPORTED;
+    if (r->rows >= (int64_t(1) << 30) || double(r->batch) * double(r->rows) > 2147483647. * 4.)
+        return IABN_ERR_UNSUPPORTED;
     if (r->batch == 0 || r->rows == 0 || q_heads + k_heads == 0) return IABN_OK;
     const int64_t es = esize(r->dtype), D = r->head_dim, B = r->batch, S = r->rows;
     if (q_heads > 0) {

@@ -31,11 +31,23 @@ __device__ __forceinline__ double position(const void* p, int64_t i)
     else return double(static_cast<const float*>(p)[i]);
 }
 
+// cos and sin of pair p at position i (counted in coordinates).
+template <int POS>
+__device__ __forceinline__ void turn_of(const RotaryArgs& a, int64_t i, int p, float& co, float& si)
+{
+    double t = position<POS>(a.positions, i) * a.inv_freq[p] * kTurns;
+    t -= rint(t);
+    sincospif(2.f * float(t), &si, &co);
+    si *= a.sign;
+}
+
 struct RotarySplit {
     int slices;                       // threads that share a token's heads
     int turn, copy;                   // threads of a head: 8 pairs each, 8 of the rest each
-    FastDiv dslices, dchunks;
-    int64_t token0;
+    bool in_place;
+    FastDiv dslices, dchunks, drows;
+    int64_t b0;                       // the first token's sequence, and row in it (below 2^30,
+    uint32_t row0;                    // as the tokens of a launch are)
     uint32_t count;                   // threads of this launch
 };
 
@@ -48,7 +60,8 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a, RotarySplit s
     const uint32_t chunks = uint32_t(sp.turn + sp.copy);
     const uint32_t j = fast_div(i, sp.dchunks), chunk = i - j * chunks;
     const uint32_t tk = fast_div(j, sp.dslices), slice = j - tk * uint32_t(sp.slices);
-    const int64_t token = sp.token0 + tk, b = token / a.S, row = token - b * a.S;
+    const uint32_t r0 = sp.row0 + tk, db = fast_div(r0, sp.drows);
+    const int64_t b = sp.b0 + db, row = r0 - db * uint32_t(a.S);
     const int n = a.pairs, H = a.heads[0] + a.heads[1];
 
     auto x_of = [&](int h) {
@@ -71,21 +84,31 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a, RotarySplit s
         }
         return;
     }
-    const int p0 = 8 * int(chunk);
+    // A ragged last chunk begins early, inside the row: its loads stay wide, and what belongs to the
+    // chunk before it is written twice with the same values, or in place (where that one's
+    // thread may have turned it) not written.
+    const int own = 8 * int(chunk), p0 = WHOLE ? own : min(own, n - 8), skip = own - p0;
     float co[8], si[8];
     const int64_t at = b * a.pos_batch + row * a.pos_row;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const int p = min(p0 + e, n - 1);
-        const int axis = a.axis ? min(max(a.axis[p], 0), a.axes - 1) : 0;
-        double t = position<POS>(a.positions, at + axis) * a.inv_freq[p] * kTurns;
-        t -= rint(t);
-        sincospif(2.f * float(t), &si[e], &co[e]);
-        si[e] *= a.sign;
+        const int p = p0 + e, axis = a.axis ? min(max(a.axis[p], 0), a.axes - 1) : 0;
+        turn_of<POS>(a, at + axis, p, co[e], si[e]);
     }
-    // the two vectors of 8 that hold the pairs, in rows that end with what turns
-    const uint32_t c0 = INTER ? 2 * p0 : p0, c1 = INTER ? 2 * p0 + 8 : p0;
-    const int C = INTER ? 2 * n : n, second = INTER ? 0 : n * ES;
+    // the two vectors of 8 elements that hold the pairs
+    const int c0 = INTER ? 2 * p0 : p0, c1 = INTER ? 2 * p0 + 8 : n + p0;
+    auto put = [&](char* y, int first, const float (&v)[8], int from) {
+        if (WHOLE || from <= 0 || !sp.in_place) {
+            store8<DT, true>(y + first * ES, 0, 8, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e >= from) {
+                    if constexpr (DT == kF32) reinterpret_cast<float*>(y)[first + e] = v[e];
+                    else reinterpret_cast<uint16_t*>(y)[first + e] = pack1<DT>(v[e]);
+                }
+        }
+    };
     auto turn = [&](int h, const Raw8<DT>& r0, const Raw8<DT>& r1) {
         float u[8], v[8], f[8], g[8];
         widen8<DT>(r0, u);
@@ -104,9 +127,10 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a, RotarySplit s
             }
         }
         char* y = y_of(h);
-        store8<DT, WHOLE>(y, c0, C, f);
-        store8<DT, WHOLE>(y + second, c1, C, g);
+        put(y, c0, f, INTER ? 2 * skip : skip);
+        put(y, c1, g, INTER ? 2 * skip - 8 : skip);
     };
+    auto load = [&](const char* x, int first) { return load8<DT, true>(x + first * ES, 0, 8); };
     // four heads' loads in flight
     int h = int(slice);
     for (; h + 3 * sp.slices < H; h += 4 * sp.slices) {
@@ -114,24 +138,71 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a, RotarySplit s
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const char* x = x_of(h + u * sp.slices);
-            r[u][0] = load8<DT, WHOLE>(x, c0, C);
-            r[u][1] = load8<DT, WHOLE>(x + second, c1, C);
+            r[u][0] = load(x, c0);
+            r[u][1] = load(x, c1);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) turn(h + u * sp.slices, r[u][0], r[u][1]);
     }
     for (; h < H; h += sp.slices) {
         const char* x = x_of(h);
-        const Raw8<DT> r0 = load8<DT, WHOLE>(x, c0, C), r1 = load8<DT, WHOLE>(x + second, c1, C);
+        const Raw8<DT> r0 = load(x, c0), r1 = load(x, c1);
         turn(h, r0, r1);
     }
 }
 
-bool in_place(const RotaryArgs& a)
+// Fewer than 8 pairs: a thread one pair of a head.
+template <int DT, int POS, bool INTER>
+__global__ __launch_bounds__(kThreads) void k_rotary_few(RotaryArgs a, RotarySplit sp)
+{
+    constexpr int ES = DT == kF32 ? 4 : 2;
+    const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
+    if (i >= sp.count) return;
+    const uint32_t per = uint32_t(a.pairs + (sp.copy ? a.D - 2 * a.pairs : 0));
+    const uint32_t j = fast_div(i, sp.dchunks), p = i - j * per;
+    const uint32_t tk = fast_div(j, sp.dslices);
+    const int h = int(j - tk * uint32_t(sp.slices)), n = a.pairs;
+    const uint32_t r0 = sp.row0 + tk, db = fast_div(r0, sp.drows);
+    const int64_t b = sp.b0 + db, row = r0 - db * uint32_t(a.S);
+    const bool second = h >= a.heads[0];
+    const Heads& tx = second ? a.x[1] : a.x[0];
+    const Heads& ty = second ? a.y[1] : a.y[0];
+    const int hh = second ? h - a.heads[0] : h;
+    const char* x = tx.p + (b * tx.batch + row * tx.row + int64_t(hh) * tx.head) * ES;
+    char* y = ty.p + (b * ty.batch + row * ty.row + int64_t(hh) * ty.head) * ES;
+    auto get = [&](int d) {
+        if constexpr (DT == kF32) return reinterpret_cast<const float*>(x)[d];
+        else return unpack1<DT>(reinterpret_cast<const uint16_t*>(x)[d]);
+    };
+    auto put = [&](int d, float v) {
+        if constexpr (DT == kF32) reinterpret_cast<float*>(y)[d] = v;
+        else reinterpret_cast<uint16_t*>(y)[d] = pack1<DT>(v);
+    };
+    if (int(p) >= n) {
+        put(n + int(p), get(n + int(p)));
+        return;
+    }
+    float co, si;
+    const int axis = a.axis ? min(max(a.axis[p], 0), a.axes - 1) : 0;
+    turn_of<POS>(a, b * a.pos_batch + row * a.pos_row + axis, int(p), co, si);
+    const int d0 = INTER ? 2 * int(p) : int(p), d1 = INTER ? d0 + 1 : n + int(p);
+    const float u = get(d0), v = get(d1);
+    put(d0, fmaf(u, co, -(v * si)));
+    put(d1, fmaf(v, co, u * si));
+}
+
+bool all_in_place(const RotaryArgs& a)
 {
     for (int t = 0; t < 2; ++t)
         if (a.heads[t] > 0 && a.x[t].p != a.y[t].p) return false;
     return true;
+}
+
+bool any_in_place(const RotaryArgs& a)
+{
+    for (int t = 0; t < 2; ++t)
+        if (a.heads[t] > 0 && a.x[t].p == a.y[t].p) return true;
+    return false;
 }
 
 }  // namespace
@@ -141,16 +212,23 @@ void launch_rotary(const RotaryArgs& a, int dtype, int64_t cus, hipStream_t s)
     RotarySplit sp{};
     const int H = a.heads[0] + a.heads[1];
     const int64_t tokens = a.B * a.S;
+    const bool few = a.pairs < 8, inside = any_in_place(a);
+    sp.in_place = inside;
     sp.turn = int(ceil_div(a.pairs, 8));
-    sp.copy = in_place(a) ? 0 : int(ceil_div(a.D - 2 * a.pairs, 8));
-    const int64_t chunks = sp.turn + sp.copy;
-    // eighths of the heads, unless the tokens alone would not fill the card
-    sp.slices = tokens * chunks * 8 >= cus * 2048 ? int(min64(8, H)) : H;
+    sp.copy = all_in_place(a) ? 0 : int(ceil_div(a.D - 2 * a.pairs, 8));
+    const int64_t chunks = few ? a.pairs + (sp.copy ? a.D - 2 * a.pairs : 0) : sp.turn + sp.copy;
+    // Eighths of the heads, unless that leaves fewer than two waves a SIMD (3 x 1369 tokens of 24 heads
+    // of 72, f32: 17 us, 22 with a head a thread).
+    sp.slices = !few && tokens * chunks * 8 >= cus * 512 ? int(min64(8, H)) : H;
     sp.dslices = make_fast_div(uint32_t(sp.slices));
     sp.dchunks = make_fast_div(uint32_t(chunks));
-    const int64_t per = chunks * sp.slices, step = max64(1, ((int64_t(1) << 31) - 1) / per);
-    for (sp.token0 = 0; sp.token0 < tokens; sp.token0 += step) {
-        sp.count = uint32_t(min64(step, tokens - sp.token0) * per);
+    sp.drows = make_fast_div(uint32_t(a.S));
+    const int64_t per = chunks * sp.slices;
+    const int64_t step = max64(1, min64(int64_t(1) << 30, ((int64_t(1) << 31) - 1) / per));
+    for (int64_t first = 0; first < tokens; first += step) {
+        sp.b0 = first / a.S;
+        sp.row0 = uint32_t(first % a.S);
+        sp.count = uint32_t(min64(step, tokens - first) * per);
         const dim3 grid(unsigned(ceil_div(sp.count, kThreads)));
         with_dtype(dtype, [&](auto d) {
             constexpr int DT = decltype(d)::value;
@@ -160,6 +238,15 @@ void launch_rotary(const RotaryArgs& a, int dtype, int64_t cus, hipStream_t s)
                                    grid, dim3(kThreads), 0, s, a, sp);
             };
             auto shape = [&](auto pos) {
+                if (few) {
+                    if (a.interleaved)
+                        hipLaunchKernelGGL((k_rotary_few<DT, decltype(pos)::value, true>), grid,
+                                           dim3(kThreads), 0, s, a, sp);
+                    else
+                        hipLaunchKernelGGL((k_rotary_few<DT, decltype(pos)::value, false>), grid,
+                                           dim3(kThreads), 0, s, a, sp);
+                    return;
+                }
                 with_whole(a.pairs, [&](auto whole) {
                     if (a.interleaved) go(pos, std::true_type{}, whole);
                     else go(pos, std::false_type{}, whole);
