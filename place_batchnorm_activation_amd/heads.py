@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -21,8 +22,8 @@ GN_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "identity": 3, "leaky_relu": 4}
 _POS_TYPES = {torch.int32: 0, torch.int64: 1, torch.float32: 2}
 
 
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", _P), ("batch", _I64), ("row", _I64), ("head", _I64)]
+# iabn_heads: address and three strides, passed as the bytes of the struct
+_HEADS = struct.Struct("=4q").pack
 
 
 class _Problem(ctypes.Structure):
@@ -72,9 +73,9 @@ def _heads(t, name, shape, ref=None):
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1 and t.numel() > 0:
         raise ValueError("%s: a head's elements must be contiguous" % name)
-    if len(st) == 3:
-        return _Heads(t.data_ptr(), 0, st[0], st[1])
-    return _Heads(t.data_ptr(), st[0], st[1], st[2])
+    if len(st) == 4:
+        return _HEADS(t.data_ptr(), st[0], st[1], st[2])
+    return _HEADS(t.data_ptr(), 0, st[0], st[1])
 
 
 def _counts(t, name, n, ref):
@@ -164,13 +165,13 @@ def iabn_attention_forward(spec, q, k, v, out, lse=None, workspace=None, q_start
     Packed: [rows, heads, head_dim] with q_starts (k_starts) int32 [batch + 1] on the GPU
     and max_q (max_k), the most rows of a sequence."""
     p = spec._problem(q, k, q_starts, k_starts, q_lens, k_lens, max_q, max_k)
-    args = (_heads(q, "q", q.shape), _heads(k, "k", k.shape, q), _heads(v, "v", k.shape, q),
-            _heads(out, "out", q.shape, q))
+    at = (_heads(q, "q", q.shape), _heads(k, "k", k.shape, q), _heads(v, "v", k.shape, q),
+          _heads(out, "out", q.shape, q))
     lp = _lse(lse, q)
     ws, wb = _space(workspace, q)
     s = _stream(stream, q)
-    _check("iabn_attention_forward", lib.iabn_attention_forward(
-        ctypes.byref(p), *map(ctypes.byref, args), lp, ws, wb, s))
+    _check("iabn_attention_forward", lib.iabn_attention_forward(ctypes.byref(p), *at, lp, ws, wb,
+                                                                s))
 
 
 def iabn_attention_backward(spec, q, k, v, out, lse, dout, dq, dk, dv, workspace, q_starts=None,
@@ -179,18 +180,16 @@ def iabn_attention_backward(spec, q, k, v, out, lse, dout, dq, dk, dv, workspace
     """dq, dk and dv from dout and the forward's out and lse; workspace:
     attention_workspace(..., backward=True)."""
     p = spec._problem(q, k, q_starts, k_starts, q_lens, k_lens, max_q, max_k)
-    args = (_heads(q, "q", q.shape), _heads(k, "k", k.shape, q), _heads(v, "v", k.shape, q),
-            _heads(out, "out", q.shape, q))
-    grads = (_heads(dout, "dout", q.shape, q), _heads(dq, "dq", q.shape, q),
-             _heads(dk, "dk", k.shape, q), _heads(dv, "dv", k.shape, q))
+    at = (_heads(q, "q", q.shape), _heads(k, "k", k.shape, q), _heads(v, "v", k.shape, q),
+          _heads(out, "out", q.shape, q), _heads(dout, "dout", q.shape, q),
+          _heads(dq, "dq", q.shape, q), _heads(dk, "dk", k.shape, q), _heads(dv, "dv", k.shape, q))
     if lse is None:
         raise ValueError("the backward needs the forward's lse")
     lp = _lse(lse, q)
     ws, wb = _space(workspace, q)
     s = _stream(stream, q)
     _check("iabn_attention_backward", lib.iabn_attention_backward(
-        ctypes.byref(p), *map(ctypes.byref, args), lp, *map(ctypes.byref, grads), ws,
-        wb, s))
+        ctypes.byref(p), *at[:4], lp, *at[4:], ws, wb, s))
 
 
 # ---------------------------------------------------------------------------
@@ -254,39 +253,35 @@ def iabn_rotary(spec, positions, q, q_out, k=None, k_out=None, inverse=False, st
     if D != spec.head_dim:
         raise ValueError("the spec has heads of %d, q of %d" % (spec.head_dim, D))
     B, S = (1, lead[0]) if packed else lead
-    pos, shape = positions, tuple(positions.shape)
-    if spec.axes == 1 and shape in ((S,), lead):
-        pos = pos.unsqueeze(-1)
-    if tuple(pos.shape) not in ((S, spec.axes), lead + (spec.axes,)):
-        raise ValueError("positions are %s, expected %s" % (shape, lead + (spec.axes,)))
-    if pos.dtype not in _POS_TYPES:
-        raise TypeError("positions are int32, int64 or float32, got %s" % pos.dtype)
-    if pos.get_device() != dev:
-        raise TypeError("positions are on %s, q on %s" % (pos.device, q.device))
-    if spec.axes > 1 and pos.numel() and pos.stride(-1) != 1:
-        raise ValueError("a position's coordinates must be contiguous")
-    pos_batch, pos_row = (0, pos.stride(0)) if pos.dim() == 2 else pos.stride()[:2]
+    axes = spec.axes
+    shape, stride = tuple(positions.shape), positions.stride()
+    if shape == lead + (axes,) or shape == (S, axes):
+        if axes > 1 and positions.numel() and stride[-1] != 1:
+            raise ValueError("a position's coordinates must be contiguous")
+        stride = stride[:-1]
+    elif axes > 1 or shape not in (lead, (S,)):
+        raise ValueError("positions are %s, expected %s" % (shape, lead + (axes,)))
+    if positions.dtype not in _POS_TYPES:
+        raise TypeError("positions are int32, int64 or float32, got %s" % positions.dtype)
+    if positions.get_device() != dev:
+        raise TypeError("positions are on %s, q on %s" % (positions.device, q.device))
+    pos_batch, pos_row = stride if len(stride) == 2 else (0, stride[0])
     n = spec.inv_freq.numel()
-    r = _Rotary(B, S, D, n, spec.axes, _dtype_code(q), int(spec.interleaved),
+    r = _Rotary(B, S, D, n, axes, _dtype_code(q), int(spec.interleaved),
                 _flat(spec.inv_freq, "inv_freq", n, torch.float64, dev),
-                _flat(spec.axis, "axis", n, torch.int32, dev), pos.data_ptr(),
-                _POS_TYPES[pos.dtype], pos_batch, pos_row)
-    args = [_heads(q, "q", q.shape), _heads(q_out, "q_out", q.shape, q)]
-    kp = kop = None
-    KV = 0
-    if k is not None:
-        if k_out is None:
-            raise ValueError("k and k_out go together")
-        KV = k.shape[-2] if k.dim() == q.dim() else -1
-        k_shape = torch.Size(lead + (KV, D))
-        args += [_heads(k, "k", k_shape, q), _heads(k_out, "k_out", k_shape, q)]
-        kp, kop = ctypes.byref(args[2]), ctypes.byref(args[3])
-    elif k_out is not None:
+                _flat(spec.axis, "axis", n, torch.int32, dev), positions.data_ptr(),
+                _POS_TYPES[positions.dtype], pos_batch, pos_row)
+    qp, qo = _heads(q, "q", q.shape), _heads(q_out, "q_out", q.shape, q)
+    KV, kp, ko = 0, None, None
+    if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
+    if k is not None:
+        KV = k.shape[-2] if k.dim() == q.dim() else -1
+        k_shape = lead + (KV, D)
+        kp, ko = _heads(k, "k", k_shape, q), _heads(k_out, "k_out", k_shape, q)
     s = _stream(stream, q)
-    _check("iabn_rotary", lib.iabn_rotary(
-        ctypes.byref(r), ctypes.byref(args[0]), q.shape[-2], ctypes.byref(args[1]), kp, KV, kop,
-        int(bool(inverse)), s))
+    _check("iabn_rotary", lib.iabn_rotary(ctypes.byref(r), qp, q.shape[-2], qo, kp, KV, ko,
+                                          int(bool(inverse)), s))
 
 
 # ---------------------------------------------------------------------------
@@ -296,14 +291,18 @@ def _group_norm(x, groups, weight, bias, act, act_param, eps):
     """(layer, (address, ld) of x) of a tensor [samples, ..., channels]."""
     if x.dim() < 2:
         raise ValueError("x is %s, expected [samples, ..., channels]" % (tuple(x.shape),))
-    p, ld, T, C = _rows(x, "x")
-    N, dev = x.shape[0], x.get_device()
+    p, ld = _map(x, "x")
+    N, C, dev = x.shape[0], x.shape[-1], x.get_device()
     if groups < 1 or C % groups:
         raise ValueError("%d groups do not divide %d channels" % (groups, C))
-    hw = math.prod(x.shape[1:-1])
-    return _GroupNorm(N, hw, C, groups, _dtype_code(x), _cols(weight, "weight", C, dev),
-                      _cols(bias, "bias", C, dev), _name(act, GN_ACTS, "act"), act_param,
-                      eps), (p, ld)
+    return _GroupNorm(N, math.prod(x.shape[1:-1]), C, groups, _dtype_code(x),
+                      _cols(weight, "weight", C, dev), _cols(bias, "bias", C, dev),
+                      _name(act, GN_ACTS, "act"), act_param, eps), (p, ld)
+
+
+def _map(t, name):
+    """(address, ld) of a tensor as rows of channels."""
+    return (t.data_ptr(), t.shape[-1]) if t.is_contiguous() else _rows(t, name)[:2]
 
 
 def _of(t, name, x):
@@ -315,7 +314,7 @@ def _of(t, name, x):
     if t.dtype != x.dtype or t.get_device() != x.get_device():
         raise TypeError("%s is %s on %s, expected %s on %s" % (name, t.dtype, t.device, x.dtype,
                                                               x.device))
-    return _rows(t, name)[:2]
+    return _map(t, name)
 
 
 def _gn_stats(stats, x, groups):

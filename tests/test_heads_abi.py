@@ -22,11 +22,17 @@ def problem(**kw):
     return heads._Problem(**p)
 
 
+class Heads(ctypes.Structure):
+    """iabn_heads of include/iabn.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("row", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
+
+
 def place(data, B=2, S=300, H=4, D=64, layout="bshd", **kw):
     row, head = (H * D, D) if layout == "bshd" else (D, S * D)
     h = dict(data=data, batch=S * H * D, row=row, head=head)
     h.update(kw)
-    return heads._Heads(**h)
+    return Heads(**h)
 
 
 def ref(t):
@@ -117,7 +123,7 @@ def test_slices_of_one_buffer_are_apart():
     refused is the workspace, which is checked against them together."""
     H, KV, D, S = 4, 2, 64, 300
     row = (H + 2 * KV) * D
-    at = lambda first, n: heads._Heads(data=8 * M + 2 * first * D, batch=S * row, row=row,  # noqa: E731
+    at = lambda first, n: Heads(data=8 * M + 2 * first * D, batch=S * row, row=row,  # noqa: E731
                                        head=D)
     dq, dk, dv = at(0, H), at(H, KV), at(H + KV, KV)
     # every pair of them alone is apart; with the workspace over one of them, refused
