@@ -27,36 +27,44 @@ namespace {
 
 constexpr float kUpP = 10.f;                       // f16: binary orders that P is raised by
 
-// The factor of dS of a lane's column.
+// The factor of dS of a lane's column, a power of two.  It begins where no dS of float16
+// tensors overflows float32, and falls to where the largest so far is far inside float16.
 template <int DT>
 struct Scaled {
-    float up = DT == kF16 ? 0x1p100f : 1.f;
+    float up = DT == kF16 ? 0x1p60f : 1.f;
 
-    // Values of 32 rows of the column (16 in each half), scaled; sums: what was made of the
-    // column's values so far.
+    __device__ __forceinline__ float order() const           // log2(up)
+    {
+        return DT == kF16 ? float(int(__float_as_uint(up) >> 23) - 127) : 0.f;
+    }
+
+    // v: values of 32 rows of the column (16 in each half) times up.  Where one comes near
+    // float16's end, they and sums (what was made of the column's values so far) are brought
+    // to a lower factor; whether any lane's changed.
     template <int N>
-    __device__ __forceinline__ void apply(f32x16_t& v, f32x16_t (&sums)[N])
+    __device__ __forceinline__ bool check(f32x16_t& v, f32x16_t (&sums)[N])
     {
         if constexpr (DT == kF16) {
             float most = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(v[i]));
             most = both_max(most);
-            const bool change = most * up > 16384.f;
+            const bool change = most > 16384.f;
             if (__any(change)) {
-                // most * up in [2^6, 2^7): headroom of 2^7 before the next change
-                const int e = max(6, int(__float_as_uint(most) >> 23));
-                const float next = change ? __uint_as_float(uint32_t(127 + 127 + 6 - e) << 23) : up;
-                const float f = next / up;
+                // the largest in [2^6, 2^7): headroom of 2^7 before the next change
+                const int e = int(__float_as_uint(most) >> 23);
+                const float f = change ? __uint_as_float(uint32_t(127 + 127 + 6 - e) << 23) : 1.f;
 #pragma unroll
                 for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) sums[n][i] *= f;
-                up = next;
-            }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= up;
+                for (int i = 0; i < 16; ++i) v[i] *= f;
+                up *= f;
+                return true;
+            }
         }
+        return false;
     }
 };
 
@@ -214,6 +222,7 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
 #pragma unroll
     for (int i = 0; i < DB; ++i) zero(dq[i]);
     Scaled<DT> scaled;
+    float base = lse2 - scaled.order();            // P comes times the factor of dS
 
     auto tile_at = [&](int st, int v) { return lds + (2 * st + v) * F::SLOTS * 16; };
     auto fetch = [&](int i, int st) __attribute__((always_inline)) {
@@ -229,7 +238,7 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
         auto probs = [&](int kb, int from, int to) {             // dS of some of a block
 #pragma unroll
             for (int i = from; i < to; ++i) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(s[kb][i], a.c, -lse2));
+                const float p = __builtin_amdgcn_exp2f(fmaf(s[kb][i], a.c, -base));
                 ds[kb][i] = p * (ds[kb][i] - dl);
                 if (decltype(some)::value && at + uint32_t(kb * 32 + 8 * (i / 4) + i % 4) >= n)
                     ds[kb][i] = 0.f;
@@ -265,7 +274,7 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
         if (KB == 1) probs(0, 0, 16);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            scaled.apply(ds[kb], dq);
+            if (scaled.check(ds[kb], dq)) base = lse2 - scaled.order();
             Frag<DT> x = results<DT>(ds[kb], 0);
 #pragma unroll
             for (int g = 0; g < CG; ++g) {
@@ -542,12 +551,12 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     p[i + e] = __builtin_amdgcn_exp2f(fmaf(p[i + e], a.c, -l4[e]));
-                    ds[i + e] = p[i + e] * (ds[i + e] - d4[e]);
+                    ds[i + e] = p[i + e] * (DT == kF16 ? (ds[i + e] - d4[e]) * scaled.up : ds[i + e] - d4[e]);
                     if (decltype(some)::value && at + uint32_t(2 * i + e) >= n)
                         p[i + e] = ds[i + e] = 0.f;
                 }
             }
-            scaled.apply(ds, dk);
+            scaled.check(ds, dk);
             Frag<DT> fp, fs;
 #pragma unroll
             for (int i = 0; i < 2 * DB; ++i) {
