@@ -520,7 +520,8 @@ typedef struct iabn_heads {
  * left as they were.  Either side may be packed, padded or full by itself.  Values outside
  * the tensors are cut to them.
  *
- * q_len and k_len times heads / kv_heads stay at or below 2^29. scale > 0. */
+ * q_len and k_len times heads / kv_heads stay at or below 2^29, and
+ * batch * kv_heads * (2 max(q_len * heads / kv_heads, k_len) + 256) below 2^32.  scale > 0. */
 typedef struct iabn_attention {
     int64_t batch, heads, kv_heads, head_dim, q_len, k_len;
     iabn_dtype dtype;

@@ -133,9 +133,9 @@ iabn_status check_problem(const iabn_attention* p)
         const double group = double(p->heads / p->kv_heads), most = double(kAttnMaxLen);
         const double rows = double(p->q_len) * group, keys = double(p->k_len) * group;
         if (rows > most || keys > most) return IABN_ERR_UNSUPPORTED;
-        // workgroups, and rows of the workspace
+        // threads of a launch, two for a row or a key and a workgroup's for a head, in 32 bits
         const double heads = double(p->batch) * double(p->kv_heads);
-        if (heads * (rows / 32. + 1.) > 2.0e9 || heads * (keys / 128. + 1.) > 2.0e9)
+        if (heads * (2. * (rows > p->k_len ? rows : double(p->k_len)) + 256.) > 4294967295.)
             return IABN_ERR_UNSUPPORTED;
     }
     if ((p->q_starts && p->q_rows > kMaxExtent) || (p->k_starts && p->k_rows > kMaxExtent))

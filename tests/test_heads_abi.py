@@ -64,7 +64,8 @@ def test_attention_problem(call):
         assert call(problem(**bad)) == INVALID, bad
     for far in (dict(head_dim=136), dict(head_dim=60), dict(q_len=(1 << 29) + 1),
                 dict(k_len=(1 << 28) + 1), dict(batch=1 << 40), dict(heads=1 << 30, kv_heads=1),
-                dict(q_starts=M, q_rows=1 << 31)):
+                dict(q_starts=M, q_rows=1 << 31),
+                dict(batch=1 << 15, q_len=1 << 16), dict(batch=1 << 15, k_len=1 << 16)):
         assert call(problem(**far)) == UNSUPPORTED, far
     for odd in (dict(q_lens=M + 2), dict(k_starts=M + 1, k_rows=600)):
         assert call(problem(**odd)) == MISALIGNED, odd
