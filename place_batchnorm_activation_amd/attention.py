@@ -39,6 +39,13 @@ def _outputs(t, packed):
     return torch.zeros(t.shape, dtype=t.dtype, device=t.device) if packed else _fresh(t)
 
 
+def _kept(seq):
+    """A call's sequences as (names, tensors) and plain values, for autograd to keep the tensors
+    (which it checks for later writes)."""
+    names = [n for n, v in seq.items() if isinstance(v, torch.Tensor)]
+    return names, [seq[n] for n in names], {n: v for n, v in seq.items() if n not in names}
+
+
 class AttentionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, spec, seq):
@@ -49,15 +56,17 @@ class AttentionFunction(torch.autograd.Function):
         iabn_attention_forward(spec, q, k, v, out, lse, attention_workspace(spec, q, k, **seq),
                                **seq)
         if train:
-            ctx.save_for_backward(q, k, v, out, lse)
-        ctx.spec, ctx.seq = spec, seq
+            names, tensors, plain = _kept(seq)
+            ctx.save_for_backward(q, k, v, out, lse, *tensors)
+            ctx.cfg = (spec, names, plain)
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        q, k, v, out, lse = ctx.saved_tensors
-        spec, seq = ctx.spec, ctx.seq
+        q, k, v, out, lse, *tensors = ctx.saved_tensors
+        spec, names, plain = ctx.cfg
+        seq = dict(plain, **dict(zip(names, tensors)))
         packed_q, packed_k = seq.get("q_starts") is not None, seq.get("k_starts") is not None
         dq, dk, dv = _outputs(q, packed_q), _outputs(k, packed_k), _outputs(v, packed_k)
         iabn_attention_backward(spec, q, k, v, out, lse, _heads(dout), dq, dk, dv,
@@ -131,15 +140,17 @@ class QKVAttentionFunction(torch.autograd.Function):
         iabn_attention_forward(spec, q, k, v, out, lse, attention_workspace(spec, q, k, **seq),
                                **seq)
         if train:
-            ctx.save_for_backward(qkv, positions, out, lse)
-        ctx.cfg = (heads, kv_heads, turn, spec, seq)
+            names, tensors, plain = _kept(seq)
+            ctx.save_for_backward(qkv, positions, out, lse, *tensors)
+            ctx.cfg = (heads, kv_heads, turn, spec, names, plain)
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        qkv, positions, out, lse = ctx.saved_tensors
-        heads, kv_heads, turn, spec, seq = ctx.cfg
+        qkv, positions, out, lse, *tensors = ctx.saved_tensors
+        heads, kv_heads, turn, spec, names, plain = ctx.cfg
+        seq = dict(plain, **dict(zip(names, tensors)))
         parts = (heads, kv_heads, kv_heads)
         q, k, v = qkv.split(parts, -2)
         grad = _outputs(qkv, seq.get("q_starts") is not None)

@@ -192,6 +192,41 @@ def test_one_token_over_a_long_cache(dtype):
 
 
 @DT
+def test_a_very_long_cache(dtype):
+    """Hundreds of parts, and a window that leaves all but the last few of them nothing."""
+    q, k, v, _ = make(30, 1, 2, 150001, 2, 1, 64, dtype)
+    for left in (-1, 700):
+        spec = iabn.AttentionSpec(window=(left, 0))
+        out, lse = torch.full_like(q, math.nan), iabn.attention_lse(q).fill_(math.nan)
+        iabn.iabn_attention_forward(spec, q, k, v, out, lse, iabn.attention_workspace(spec, q, k))
+        val, bound = heads_ref.attention(q, k, v, left=left, right=0)
+        check(dict(out=out, lse=lse), val, bound)
+
+
+@DT
+@pytest.mark.parametrize("Sq,Sk,H,KV", ((24, 9000, 4, 1), (3000, 40, 8, 2), (1500, 1500, 2, 1)))
+def test_parted_gradients(dtype, Sq, Sk, H, KV):
+    """Few row tiles over many keys, few key tiles under many rows: shares that are joined."""
+    q, k, v, do = make(31, 1, Sq, Sk, H, KV, 64, dtype)
+    for right in (-1, 0):
+        spec = iabn.AttentionSpec(causal=right == 0)
+        check(both(q, k, v, do, spec), *heads_ref.attention(q, k, v, do, right=right))
+
+
+@DT
+def test_parted_padded_batch(dtype):
+    """Joined shares under lengths: tiles that end inside a length, padded keys and rows."""
+    ql, kl = [1400, 77, 0, 900], [1400, 500, 300, 0]
+    q, k, v, do = make(32, 4, 1400, 1400, 2, 1, 40, dtype)
+    for b in range(4):
+        q[b, ql[b]:] = do[b, ql[b]:] = math.nan
+        k[b, kl[b]:] = v[b, kl[b]:] = math.nan
+    spec = iabn.AttentionSpec(window=(600, 100))
+    got = both(q, k, v, do, spec, q_lens=lens(ql), k_lens=lens(kl))
+    check(got, *heads_ref.attention(q, k, v, do, left=600, right=100, q_lens=ql, k_lens=kl))
+
+
+@DT
 @pytest.mark.parametrize("Sq", (3, 40, 300))
 def test_cut_keys_with_several_tokens(dtype, Sq):
     q, k, v, _ = make(14, 1, Sq, 2000, 4, 2, 96, dtype)
