@@ -697,8 +697,9 @@ Parts dkv_parts(const AttnArgs& a, int64_t cus)
     const int64_t want = wgs > 0 ? ceil_div((uneven ? 4 : 2) * cus, wgs) : 1;
     const int64_t parts = max64(1, min64(want, rows / 128));
     // whole tiles of rows and whole groups
-    pt.chunk = int(max64(1, ceil_div(ceil_div(rows, parts), 64 * a.G)) * 64 * a.G);
-    pt.parts = int(max64(1, ceil_div(rows, pt.chunk)));
+    const int64_t unit = int64_t(64) * a.G, chunk = max64(1, ceil_div(ceil_div(rows, parts), unit)) * unit;
+    pt.parts = int(max64(1, ceil_div(rows, chunk)));
+    pt.chunk = int(min64(chunk, max64(1, rows)));
     return pt;
 }
 

@@ -121,7 +121,7 @@ class AttentionSpec:
             if starts is not None and most is None:
                 raise ValueError("packed %s needs max_%s, the most rows of a sequence"
                                  % (side, side))
-        scale = 1.0 / math.sqrt(D) if self.scale is None else self.scale
+        scale = 1.0 / math.sqrt(max(1, D)) if self.scale is None else self.scale
         return _Problem(
             batch, H, KV, D, q.shape[1] if q_starts is None else max_q,
             k.shape[1] if k_starts is None else max_k, _dtype_code(q), scale, self.left,

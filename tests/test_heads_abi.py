@@ -72,6 +72,13 @@ def test_attention_problem(call):
     assert lib.iabn_attention_forward(None, *[None] * 5, None, 0, None) == INVALID
 
 
+@pytest.mark.parametrize("heads", (1 << 25, 1 << 26, 1 << 29))
+def test_attention_of_one_token_and_the_most_heads(heads):
+    """64 groups of rows pass 32 bits; the workspace holds a number a row all the same."""
+    p = problem(batch=1, heads=heads, kv_heads=1, q_len=1, k_len=1)
+    assert lib.iabn_attention_workspace_size(ctypes.byref(p), 1) >= 4 * heads
+
+
 def test_attention_without_queries():
     assert forward(problem(q_len=0)) == OK
 
