@@ -227,6 +227,44 @@ def test_parted_padded_batch(dtype):
 
 
 @DT
+@pytest.mark.parametrize("H,KV,D", ((3, 1, 128), (10, 2, 64), (40, 1, 40)))
+def test_odd_groups_at_length(dtype, H, KV, D):
+    """Groups that divide no pass of a tile, over many tiles."""
+    q, k, v, do = make(33 + H, 1, 420, 640, H, KV, D, dtype)
+    spec = iabn.AttentionSpec(causal=True)
+    check(both(q, k, v, do, spec), *heads_ref.attention(q, k, v, do, right=0))
+
+
+@DT
+@pytest.mark.parametrize("shift", (1, 4))
+def test_unaligned_at_length(dtype, shift):
+    """Rows at no multiple of 16 bytes, over many tiles."""
+    B, S, H, KV, D = 2, 500, 4, 2, 64
+    wide = torch.randn(B, S, (H + 2 * KV) * D + shift, generator=torch.Generator().manual_seed(34))
+    wide = wide.to(dtype).cuda()
+    q, k, v = (t.unflatten(-1, (-1, D)) for t in
+               wide[..., shift:].split((H * D, KV * D, KV * D), -1))
+    do = make(35, B, S, S, H, KV, D, dtype)[3]
+    spec = iabn.AttentionSpec()
+    check(both(q, k, v, do, spec), *heads_ref.attention(q, k, v, do))
+
+
+@DT
+def test_packed_and_parted(dtype):
+    """Long and short packed sequences whose gradients are made in shares."""
+    ls, D = [1500, 0, 3, 800], 96
+    q, k, v, do = make(36, 4, 1500, 1500, 2, 1, D, dtype)
+    starts = lens([0, 1500, 1500, 1503, 2303])
+    flat = [torch.cat([t[b, :n] for b, n in enumerate(ls)]) for t in (q, k, v, do)]
+    spec = iabn.AttentionSpec(causal=True)
+    got = both(*flat, spec, q_starts=starts, k_starts=starts, max_q=1500, max_k=1500)
+    val, bound = heads_ref.attention(q, k, v, do, right=0, q_lens=ls, k_lens=ls)
+    for name in ("out", "dq", "dk", "dv"):
+        join = lambda t: torch.cat([t[b, :n] for b, n in enumerate(ls)])  # noqa: E731
+        heads_ref.within(got[name], join(val[name]), join(bound[name]), name)
+
+
+@DT
 @pytest.mark.parametrize("Sq", (3, 40, 300))
 def test_cut_keys_with_several_tokens(dtype, Sq):
     q, k, v, _ = make(14, 1, Sq, 2000, 4, 2, 96, dtype)

@@ -128,6 +128,30 @@ def test_in_place(dtype):
     assert torch.equal(x, want["y"]) and torch.equal(stats, want["stats"])
 
 
+@DT
+@pytest.mark.parametrize("N,HW,C,G", ((2, 300, 4104, 3), (1, 40, 2056, 257), (3, 9, 5000, 1)))
+def test_wide(dtype, N, HW, C, G):
+    """More channels than a workgroup has, groups across two workgroups' channels."""
+    x, dy, w, b = make(14, N, HW, C, dtype)
+    check(both(x, dy, G, w, b, "silu"), *heads_ref.group_norm(x, dy, G, w, b, "silu", 0, 1e-5))
+
+
+@DT
+@pytest.mark.parametrize("HW", (20, 5000))
+def test_gradients_in_place_of_the_parameters(dtype, HW):
+    x, dy, w, b = make(15, 2, HW, 64, dtype)
+    want = both(x, dy, 4, w, b, "silu")
+    for same in ("weight", "bias", "both"):
+        weight, bias, dx = w.clone(), b.clone(), torch.empty_like(x)
+        dw = torch.empty_like(w) if same == "bias" else weight
+        db = torch.empty_like(b) if same == "weight" else bias
+        iabn.iabn_group_norm_backward(x, dy, dx, 4, weight, bias, want["stats"],
+                                      iabn.group_norm_workspace(x, 4), act="silu", dweight=dw,
+                                      dbias=db)
+        for name, t in (("dx", dx), ("dweight", dw), ("dbias", db)):
+            assert torch.equal(t, want[name]), name
+
+
 def test_statistics_are_optional():
     x, dy, w, b = make(9, 3, 300, 64, F32)
     ws = iabn.group_norm_workspace(x, 8)
