@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
     const int lane = threadIdx.x % 64, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     uint32_t head, tile;
-    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), false, head, tile);
+    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), windowed(a), head, tile);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
     tile = uint32_t(tiles) - 1 - tile;             // causal rows with many keys first
     const Sequence sq = sequence_of(a, b);
@@ -419,10 +419,7 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
     const int lane = threadIdx.x % 64, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     uint32_t head, tile;
-    // Causal keys are seen by ever fewer rows: the long tiles of all heads first (head by head, the
-    // last one's would end alone: 850 us against 640 for twice 4096 tokens of 32 heads on 8).
-    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles),
-                  a.left < kAttnMaxLen || a.right < kAttnMaxLen, head, tile);
+    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), windowed(a), head, tile);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
     const Sequence sq = sequence_of(a, b);
     const int all_rows = a.Sq * a.G;

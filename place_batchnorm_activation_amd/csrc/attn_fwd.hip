@@ -67,7 +67,7 @@ __global__ __launch_bounds__(64 * WQ, (FwdShape<DT, DP, WQ>::WAVES)) void k_attn
     const int lane = threadIdx.x % 64, h = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     uint32_t head, tile;
-    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), false, head, tile);
+    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), windowed(a), head, tile);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
     tile = uint32_t(tiles) - 1 - tile;             // causal rows with many keys first
     const Sequence sq = sequence_of(a, b);
