@@ -508,9 +508,9 @@ typedef struct iabn_heads {
  *   i + (Lk - Lq) - left <= j <= i + (Lk - Lq) + right,
  * left or right < 0: unbounded on that side.  right = 0 is causal with the last query at
  * the last key (new tokens behind a cache).  A query that sees no key gets out = 0,
- * lse = -inf, and has no part in any gradient.  Hidden keys take no part, but a NaN or an infinity in k or v of a key
- * that a neighbouring query sees may reach queries that do not see it (0 * NaN); keys that lie
- * behind a sequence's length are not read.
+ * lse = -inf, and has no part in any gradient.  Keys behind a sequence's length are not read.
+ * Other hidden keys take no part while they are finite; a NaN or an infinity in a key or value
+ * (in the backward: in a query or dout too) may reach rows that do not see it, as 0 * NaN.
  *
  * Lengths: q_lens, k_lens int32 [batch] on the device, or NULL (the whole length).  Rows of
  * out and of gradients behind a length are written as zeros (lse: -inf).
@@ -551,8 +551,9 @@ iabn_status iabn_attention_forward(const iabn_attention *problem, const iabn_hea
  *   P = exp(scale * q k^T - lse), delta = sum_d dout * out, dS = P * (dout v^T - delta),
  *   dv = P^T dout, dq = scale * dS k, dk = scale * dS^T q,
  * dk and dv summed over the query heads of a key head.  dq, dk and dv overlap nothing else
- * of the call (slices of one buffer do not overlap).  For 16-bit types P and dS are rounded to them before their products
- * (float16: raised by powers of two first, so that small gradients keep their digits). */
+ * of the call (slices of one buffer do not overlap).  For 16-bit types P and dS are rounded to
+ * them before their products (float16: raised by powers of two first, so that small gradients
+ * keep their digits). */
 iabn_status iabn_attention_backward(const iabn_attention *problem, const iabn_heads *q,
                                     const iabn_heads *k, const iabn_heads *v,
                                     const iabn_heads *out, const float *lse,
@@ -565,8 +566,8 @@ typedef enum iabn_pos { IABN_POS_I32 = 0, IABN_POS_I64 = 1, IABN_POS_F32 = 2 } i
 /* Rotary positions with `axes` coordinates a token: pair p (of `pairs`) of every head turns by
  * angle = position[axis[p]] * inv_freq[p], (a, b) -> (a cos - b sin, b cos + a sin), a and b
  * the head's elements p and pairs + p, or with `interleaved` 2p and 2p + 1; elements from
- * 2*pairs on are copied.  inv_freq float64 [pairs] (radians a step) and axis int32 [pairs] (NULL: all
- * 0; values are cut to [0, axes)) on the device.  positions: coordinate c of token (b, r)
+ * 2*pairs on are copied.  inv_freq float64 [pairs] (radians a step) and axis int32 [pairs]
+ * (NULL: all 0; values are cut to [0, axes)) on the device.  positions: coordinate c of token (b, r)
  * at b*pos_batch + r*pos_row + c, of pos_type; pos_batch 0 shares them among the batch.
  * Angles are formed in float64.  rows below 2^30. */
 typedef struct iabn_rotary_spec {
@@ -608,8 +609,8 @@ size_t iabn_group_norm_workspace_size(const iabn_group_norm *layer);
 
 /* y = act(xhat * weight + bias), xhat = (x - mean) * rstd over a sample's group,
  * rstd = 1 / sqrt(biased variance + eps).  stats: fp32 [n, groups, 2], mean and rstd, or NULL.
- * y may be exactly x.  Rows n*hw below 2^31, c below 2^26.  workspace: device, 16-byte aligned; it carries no
- * status word. */
+ * y may be exactly x.  Rows n*hw below 2^31, c below 2^26.  workspace: device, 16-byte aligned;
+ * it carries no status word. */
 iabn_status iabn_group_norm_forward(const iabn_group_norm *layer, const void *x, int64_t ldx,
                                     void *y, int64_t ldy, float *stats, void *workspace,
                                     size_t workspace_bytes, hipStream_t stream);

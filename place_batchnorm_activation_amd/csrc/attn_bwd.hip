@@ -74,7 +74,8 @@ template <int DT>
 __device__ __forceinline__ void store_scaled(char* row, int d, const f32x16_t& v, int i, float f,
                                              bool live)
 {
-    if (live) store4<DT>(row, d, v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
+    if (live)
+        store4<DT>(row, d, v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
     else store4<DT>(row, d, 0.f, 0.f, 0.f, 0.f);
 }
 
@@ -323,7 +324,8 @@ __global__ __launch_bounds__(256, (DqShape<DT, DP>::WAVES)) void k_attn_dq(AttnA
         }
     }
     if (shared) {
-        float* share = share_of<1>(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) + (r - row0) * a.D;
+        float* share = share_of<1>(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) +
+                       (r - row0) * a.D;
         if (r >= rows) return;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
@@ -367,13 +369,15 @@ __global__ __launch_bounds__(256) void k_attn_dq_join(AttnArgs a, AttnGrads g, P
     const int i = int(blockIdx.y) * 256 + int(threadIdx.x);
     if (i < end * quads) {
         const int r = i / quads, d = i % quads * 4;
-        const int tok = int(fast_div(uint32_t(row0 + r), a.group)), hq = hk * a.G + row0 + r - tok * a.G;
+        const int tok = int(fast_div(uint32_t(row0 + r), a.group));
+        const int hq = hk * a.G + row0 + r - tok * a.G;
         // a row that sees no key holds 0 * infinity of its tile's others
         const bool live = row0 + r < rows && a.lse[lse_index(a, sq, b, hq, tok)] != -INFINITY;
         const float4 v = sum_shares<1>(pt, head, uint32_t(tiles), tile, live ? parts : 0, a.D,
                                        r * a.D + d);
-        store4<DT>(head_of(g.dq, a.q_starts != nullptr, b, sq.q0, hq, ES) + int64_t(tok) * g.dq.row * ES,
-                   d, v.x, v.y, v.z, v.w);
+        char* out = head_of(g.dq, a.q_starts != nullptr, b, sq.q0, hq, ES) +
+                    int64_t(tok) * g.dq.row * ES;
+        store4<DT>(out, d, v.x, v.y, v.z, v.w);
     }
 }
 
@@ -381,7 +385,8 @@ __global__ __launch_bounds__(256) void k_attn_dq_join(AttnArgs a, AttnGrads g, P
 // dK and dV
 
 // Rows [lo, hi) of the group that see key x.
-__device__ __forceinline__ void seen_by(const AttnArgs& a, const Sequence& s, int x, int& lo, int& hi)
+__device__ __forceinline__ void seen_by(const AttnArgs& a, const Sequence& s, int x, int& lo,
+                                        int& hi)
 {
     const int off = s.lk - s.lq;
     lo = max(0, x - off - a.right);
@@ -481,7 +486,8 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
     Scaled<DT> scaled;
 
     using T = Tiles<DT, DP, F::QT, F::NT>;
-    const T qrows = group_tiles<T>(a, a.q, b, sq, hk, ES), grows = group_tiles<T>(a, g.dout, b, sq, hk, ES);
+    const T qrows = group_tiles<T>(a, a.q, b, sq, hk, ES);
+    const T grows = group_tiles<T>(a, g.dout, b, sq, hk, ES);
     const RowFrags<DT, DP> rows_at;
     const ColFrags<DT, DP> cols_at;
     char* const values = lds + 4 * F::TILE;
@@ -542,13 +548,15 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
             read_c(0);
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
-                const float4 ls = *reinterpret_cast<const float4*>(&info[st][0][qb * 32 + 2 * i + 4 * h]);
-                const float4 de = *reinterpret_cast<const float4*>(&info[st][1][qb * 32 + 2 * i + 4 * h]);
+                const int at4 = qb * 32 + 2 * i + 4 * h;
+                const float4 ls = *reinterpret_cast<const float4*>(&info[st][0][at4]);
+                const float4 de = *reinterpret_cast<const float4*>(&info[st][1][at4]);
                 const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     p[i + e] = __builtin_amdgcn_exp2f(fmaf(p[i + e], a.c, -l4[e]));
-                    ds[i + e] = p[i + e] * (DT == kF16 ? (ds[i + e] - d4[e]) * scaled.up : ds[i + e] - d4[e]);
+                    const float d = ds[i + e] - d4[e];
+                    ds[i + e] = p[i + e] * (DT == kF16 ? d * scaled.up : d);
                     if (decltype(some)::value && at + uint32_t(2 * i + e) >= n)
                         p[i + e] = ds[i + e] = 0.f;
                 }
@@ -611,15 +619,17 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
     const float up = DT == kF16 ? 0x1p-10f : 1.f, f = a.scale * up / scaled.up;
     if (shared) {
         if (j >= sq.lk) return;
-        float* share = share_of<2>(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) + (j - key0) * a.D;
+        float* share = share_of<2>(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) +
+                       (j - key0) * a.D;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int d = 32 * db + 8 * i + 4 * h;
                 if (d >= a.D) continue;
-                store_scaled<kF32>(reinterpret_cast<char*>(share), d, dk[db], i, f, true);
-                store_scaled<kF32>(reinterpret_cast<char*>(share + 128 * a.D), d, dv[db], i, up, true);
+                char* p = reinterpret_cast<char*>(share);
+                store_scaled<kF32>(p, d, dk[db], i, f, true);
+                store_scaled<kF32>(p + 512 * a.D, d, dv[db], i, up, true);
             }
         return;
     }
@@ -694,7 +704,8 @@ Parts dkv_parts(const AttnArgs& a, int64_t cus)
     const int64_t want = wgs > 0 ? ceil_div((uneven ? 4 : 2) * cus, wgs) : 1;
     const int64_t parts = max64(1, min64(want, rows / 128));
     // whole tiles of rows and whole groups
-    const int64_t unit = int64_t(64) * a.G, chunk = max64(1, ceil_div(ceil_div(rows, parts), unit)) * unit;
+    const int64_t unit = int64_t(64) * a.G;
+    const int64_t chunk = max64(1, ceil_div(ceil_div(rows, parts), unit)) * unit;
     pt.parts = int(max64(1, ceil_div(rows, chunk)));
     pt.chunk = int(min64(chunk, max64(1, rows)));
     return pt;
@@ -734,7 +745,8 @@ void launch_attn_backward(const AttnArgs& a, const AttnGrads& g, int dtype, int6
 {
     float* delta = static_cast<float*>(ws);
     const BwdSpace w = bwd_space(a, cus, ws);
-    const int row_tiles = int(ceil_div(int64_t(a.Sq) * a.G, 128)), key_tiles = int(ceil_div(a.Sk, 128));
+    const int row_tiles = int(ceil_div(int64_t(a.Sq) * a.G, 128));
+    const int key_tiles = int(ceil_div(a.Sk, 128));
     const int64_t heads = int64_t(a.B) * a.KV;
     const unsigned row_wgs = unsigned(heads * row_tiles), key_wgs = unsigned(heads * key_tiles);
     const unsigned slices = unsigned(ceil_div(128 * (a.D / 4), 256));
@@ -753,11 +765,11 @@ void launch_attn_backward(const AttnArgs& a, const AttnGrads& g, int dtype, int6
         else if (a.D <= 96) go(std::integral_constant<int, 96>{});
         else go(std::integral_constant<int, 128>{});
         if (row_tiles > 0 && w.dq.parts > 1)
-            hipLaunchKernelGGL((k_attn_dq_join<DT>), dim3(row_wgs, slices), dim3(256), 0, s, a, g, w.dq,
-                               row_tiles);
+            hipLaunchKernelGGL((k_attn_dq_join<DT>), dim3(row_wgs, slices), dim3(256), 0, s, a, g,
+                               w.dq, row_tiles);
         if (key_tiles > 0 && w.dkv.parts > 1)
-            hipLaunchKernelGGL((k_attn_dkv_join<DT>), dim3(key_wgs, slices, 2), dim3(256), 0, s, a, g, w.dkv,
-                               key_tiles);
+            hipLaunchKernelGGL((k_attn_dkv_join<DT>), dim3(key_wgs, slices, 2), dim3(256), 0, s, a,
+                               g, w.dkv, key_tiles);
     });
 }
 

@@ -269,7 +269,8 @@ __global__ __launch_bounds__(64 * WQ, (FwdShape<DT, DP, WQ>::WAVES)) void k_attn
         if (sp.splits > 1) {
             sp.ml[int64_t(blockIdx.y) * sp.rows + id] = make_float2(m_, l_);
         } else if (a.lse) {
-            const float lse = l_ == 0.f ? -INFINITY : (m_ * a.c + __builtin_amdgcn_logf(l_)) * kLn2A;
+            const float lse =
+                l_ == 0.f ? -INFINITY : (m_ * a.c + __builtin_amdgcn_logf(l_)) * kLn2A;
             a.lse[lse_index(a, sq, b, hq, tok)] = lse;
         }
     };
@@ -404,10 +405,10 @@ int64_t row_tiles(const AttnArgs& a)
 int64_t all_rows(const AttnArgs& a) { return int64_t(a.B) * a.KV * a.Sq * a.G; }
 
 // Keys of a workgroup where the rows' tiles are too few for the card: two workgroups a CU in
-// all, four of the small ones for few rows, each at least 128 keys.  Sequences of other lengths have fewer parts of the same
-// size.  (us of both kernels for one token over 8 caches of up to 32768, 8 key heads of 128:
-// 2 a CU 195, 4 118, 8 125, 16 135.  Least keys 64, 128, 256: 517 keys of 8 heads of 64 11, 13, 16;
-// 8192 of 8 of 128 27, 20, 21; 1027 rows over 777 keys, f32, 36, 32, 40.)
+// all, four of the small ones for few rows, each at least 128 keys.  Shorter sequences have
+// fewer parts of the same size.  (us of both kernels for one token over 8 caches of up to 32768,
+// 8 key heads of 128: 2 a CU 195, 4 118, 8 125, 16 135.  Least keys 64, 128, 256: 517 keys of 8
+// heads of 64 11, 13, 16; 8192 of 8 of 128 27, 20, 21; 1027 rows over 777 keys, f32, 36, 32, 40.)
 FwdSplit make_split(const AttnArgs& a, int64_t cus)
 {
     FwdSplit sp{};

@@ -272,14 +272,14 @@ struct Tiles {
     {
         const uint32_t th = threadIdx.x % NT, c = th % S::NC, r = th / S::NC;
         if (direct && first + ROWS <= end) {
-            const char* base = p + int64_t(G == 1 ? first : scalar(int(fast_div(uint32_t(first), group)))) * row;
+            const int tok = G == 1 ? first : scalar(int(fast_div(uint32_t(first), group)));
+            const char* base = p + int64_t(tok) * row;
             const uint32_t dst = uint32_t(scalar(int(lds_address(tile) + th / 64 * 1024)));
             const int64_t pass = PER / G * row;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const uint32_t chunk = c ^ S::mix(r + i * PER);
-                if (S::USED == S::NC ? int(chunk) * S::E < D || D == DP
-                                     : int(chunk) * S::E < D)
+                if (int(chunk) * S::E < D)
                     to_lds(base + i * pass, offset + 16 * chunk, dst + i * NT * 16);
             }
             return;

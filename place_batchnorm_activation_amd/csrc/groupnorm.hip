@@ -17,8 +17,9 @@
 // from its L2, in one launch.
 //
 // Statistics: a thread's rows about its own first value in fp32, joined as mean and sum of
-// squares about it, the mean from the chunk's first value on (a mean far from zero takes no digits from the variance), the chunks in
-// fp64.  Gradients' sums: fp32 within a workgroup, fp64 over them.  All in a fixed order.
+// squares about it, the mean from the chunk's first value on (a mean far from zero takes no
+// digits from the variance), the chunks in fp64.  Gradients' sums: fp32 within a workgroup,
+// fp64 over them.  All in a fixed order.
 #include <hip/hip_runtime.h>
 
 #include "acts.hpp"
@@ -615,7 +616,8 @@ __global__ __launch_bounds__(kGroupThreads) void k_gn_group_grad(GnArgs a, float
         int row = p.lane;
         for (; row + p.lanes < HW; row += 2 * p.lanes) {
             const Raw8<DT> x0 = load(a.x, a.ldx, row), g0 = load(a.dy, a.lddy, row);
-            const Raw8<DT> x1 = load(a.x, a.ldx, row + p.lanes), g1 = load(a.dy, a.lddy, row + p.lanes);
+            const Raw8<DT> x1 = load(a.x, a.ldx, row + p.lanes);
+            const Raw8<DT> g1 = load(a.dy, a.lddy, row + p.lanes);
             add(x0, g0);
             add(x1, g1);
         }
@@ -678,8 +680,8 @@ __global__ __launch_bounds__(kGroupThreads) void k_gn_group_grad(GnArgs a, float
 // Whether a workgroup a group takes the map: up to 1024 of them (four a CU), whose elements, in
 // whole vectors and twice where the last one is ragged, are few.  us, one workgroup a group
 // against many, forward and backward, bf16: 8 x 32^2 x 512 in 32 groups 9 against 15, 14
-// against 19; 2 x 48^2 x 512 11, 15, 20, 19; 2 x 64^2 x 512 15, 17, 28, 19; 1 x 64^2 x 320 21, 17, 38, 19;
-// 64 x 32^2 x 256 (2048 groups) 31, 27, 72, 46.
+// against 19; 2 x 48^2 x 512 11, 15, 20, 19; 2 x 64^2 x 512 15, 17, 28, 19; 1 x 64^2 x 320 21,
+// 17, 38, 19; 64 x 32^2 x 256 (2048 groups) 31, 27, 72, 46.
 bool small_map(int64_t N, int64_t HW, int64_t C, int64_t G, int64_t most)
 {
     const int64_t cg = C / G, wide = ceil_div(cg, kRowV) * kRowV;

@@ -84,8 +84,8 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a, RotarySplit s
         }
         return;
     }
-    // A ragged last chunk begins early, inside the row: its loads stay wide, and what belongs to the
-    // chunk before it is written twice with the same values, or in place (where that one's
+    // A ragged last chunk begins early, inside the row: its loads stay wide, and what belongs to
+    // the chunk before it is written twice with the same values, or in place (where that one's
     // thread may have turned it) not written.
     const int own = 8 * int(chunk), p0 = WHOLE ? own : min(own, n - 8), skip = own - p0;
     float co[8], si[8];
@@ -217,8 +217,8 @@ void launch_rotary(const RotaryArgs& a, int dtype, int64_t cus, hipStream_t s)
     sp.turn = int(ceil_div(a.pairs, 8));
     sp.copy = all_in_place(a) ? 0 : int(ceil_div(a.D - 2 * a.pairs, 8));
     const int64_t chunks = few ? a.pairs + (sp.copy ? a.D - 2 * a.pairs : 0) : sp.turn + sp.copy;
-    // Eighths of the heads, unless that leaves fewer than two waves a SIMD (3 x 1369 tokens of 24 heads
-    // of 72, f32: 17 us, 22 with a head a thread).
+    // Eighths of the heads, unless that leaves fewer than two waves a SIMD (3 x 1369 tokens of 24
+    // heads of 72, f32: 17 us, 22 with a head a thread).
     sp.slices = !few && tokens * chunks * 8 >= cus * 512 ? int(min64(8, H)) : H;
     sp.dslices = make_fast_div(uint32_t(sp.slices));
     sp.dchunks = make_fast_div(uint32_t(chunks));

@@ -245,7 +245,8 @@ def iabn_rotary(spec, positions, q, q_out, k=None, k_out=None, inverse=False, st
     """q_out = q turned by the positions (k_out = k likewise, where given); inverse: by the
     negative angles, which is the gradient.  q [batch, rows, heads, head_dim] or packed
     [rows, heads, head_dim]; positions int32, int64 or float32 [rows] or [batch, rows] for
-    one axis, [rows, axes] or [batch, rows, axes] else (packed: [rows], [rows, axes]).  An output may be exactly its input."""
+    one axis, [rows, axes] or [batch, rows, axes] else (packed: [rows], [rows, axes]).  An
+    output may be exactly its input."""
     if q.dim() not in (3, 4):
         raise ValueError("q is %s, expected [batch, rows, heads, head_dim]" % (tuple(q.shape),))
     packed = q.dim() == 3
