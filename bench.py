@@ -100,8 +100,10 @@ def kernel_source_digest() -> str:
     """Digest of the kernel sources' code (comments excluded): the counter figures
     in profiles/traffic.json hold for the kernels built from code with this digest.
     The residual-block operators ("block.hpp", "rows.hpp", "codes.hip", "glu.hip",
-    "wgrad.hip", "resnorm.hip") add nothing to those kernels and take no part in any
-    workload measured here, so they are left out of it."""
+    "wgrad.hip", "resnorm.hip") and those of attention blocks ("attn.hpp", "attn_tile.hpp",
+    "attn_fwd.hip", "attn_bwd.hip", "rotary.hip", "gnorm.hpp", "groupnorm.hip", "acts.hpp",
+    "checks.hpp") add nothing to those kernels and take no part in any workload measured
+    here, so they are left out of it."""
     h = hashlib.sha256()
     for f in ("device.hpp", "plan.hpp", "fused.hpp", "group.hpp", "fwd.hip", "bwd.hip",
               "fused_nchw.hip", "fused_nhwc.hip", "ckpt.hip", "noalloc.hip"):
