@@ -409,6 +409,9 @@ int64_t all_rows(const AttnArgs& a) { return int64_t(a.B) * a.KV * a.Sq * a.G; }
 // fewer parts of the same size.  (us of both kernels for one token over 8 caches of up to 32768,
 // 8 key heads of 128: 2 a CU 195, 4 118, 8 125, 16 135.  Least keys 64, 128, 256: 517 keys of 8
 // heads of 64 11, 13, 16; 8192 of 8 of 128 27, 20, 21; 1027 rows over 777 keys, f32, 36, 32, 40.)
+// Few rows also where they give each CU one or two of the small workgroups, with at least 512
+// keys a part (us without and with parts: 32 caches of 4096, 8 heads of 128, 148, 118; of 1024
+// 39, 29; of 512 23, 26; 40 caches of 4096 163, 135; 64 of 2048 98, 117).
 FwdSplit make_split(const AttnArgs& a, int64_t cus)
 {
     FwdSplit sp{};
@@ -416,9 +419,10 @@ FwdSplit make_split(const AttnArgs& a, int64_t cus)
     sp.chunk = a.Sk;
     sp.rows = all_rows(a);
     const int64_t wgs = int64_t(a.B) * a.KV * row_tiles(a);
-    if (wgs == 0 || wgs >= cus) return sp;
+    if (wgs == 0 || wgs >= (few_rows(a) ? 2 : 1) * cus) return sp;
     const int64_t parts = min64(ceil_div((few_rows(a) ? 4 : 2) * cus, wgs), 512);
-    const int64_t chunk = ceil_div(max64(128, ceil_div(a.Sk, parts)), 64) * 64;
+    const int64_t least = wgs >= cus ? 512 : 128;
+    const int64_t chunk = ceil_div(max64(least, ceil_div(a.Sk, parts)), 64) * 64;
     sp.splits = int(max64(1, ceil_div(a.Sk, chunk)));
     sp.chunk = int(chunk);
     return sp;
