@@ -533,8 +533,8 @@ typedef struct iabn_attention {
 } iabn_attention;
 
 /* Bytes of workspace of iabn_attention_forward (backward == 0) or _backward; 0 when it needs
- * none (and for invalid arguments).  Depends on the arguments and the device's CU count,
- * not on lengths or starts. */
+ * none (and for invalid arguments).  Depends on the arguments and the device's CU count;
+ * of lengths and starts on whether there are any, not on their values. */
 size_t iabn_attention_workspace_size(const iabn_attention *problem, int backward);
 
 /* out = softmax(scale * q k^T) v over the visible keys; lse: fp32 [batch, heads, q_len]

@@ -404,14 +404,17 @@ int64_t row_tiles(const AttnArgs& a)
 
 int64_t all_rows(const AttnArgs& a) { return int64_t(a.B) * a.KV * a.Sq * a.G; }
 
-// Keys of a workgroup where the rows' tiles are too few for the card: two workgroups a CU in
-// all, four of the small ones for few rows, each at least 128 keys.  Shorter sequences have
-// fewer parts of the same size.  (us of both kernels for one token over 8 caches of up to 32768,
-// 8 key heads of 128: 2 a CU 195, 4 118, 8 125, 16 135.  Least keys 64, 128, 256: 517 keys of 8
-// heads of 64 11, 13, 16; 8192 of 8 of 128 27, 20, 21; 1027 rows over 777 keys, f32, 36, 32, 40.)
-// Few rows also where they give each CU one or two of the small workgroups, with at least 512
-// keys a part (us without and with parts: 32 caches of 4096, 8 heads of 128, 148, 118; of 1024
-// 39, 29; of 512 23, 26; 40 caches of 4096 163, 135; 64 of 2048 98, 117).
+// Parts of the keys where the rows' tiles are too few for the card, each at least 128 keys.
+// Many rows: two workgroups a CU in all.  Few rows: three of the small workgroups fit a CU, and
+// keys of one length come out even where all run in one round, or where one would leave a
+// tenth of the places free, in two: for one token over 8 caches of 32768, 8 key heads of 128, 12
+// parts 189 us, 16 (four a CU) 227; 32 caches of 4096 102, 118; 20 of 6000 in 4 parts 131, 7 108,
+// 9 97.  With lengths of their own part of the workgroups has nothing to do: four a CU (8
+// caches of up to 32768: 2 a CU 195, 3 130, 4 118, 6 142, 16 135).
+// Where each CU has one or two workgroups without parts, a part is at least 512 keys (us without and
+// with parts: 32 caches of 4096, 8 heads of 128, 148, 118; of 1024 39, 29; of 512 23, 26).
+// (Least keys 64, 128, 256: 517 keys of 8 heads of 64 11, 13, 16; 8192 of 8 of 128 27, 20, 21; 1027
+// rows over 777 keys, f32, 36, 32, 40.)
 FwdSplit make_split(const AttnArgs& a, int64_t cus)
 {
     FwdSplit sp{};
@@ -420,9 +423,17 @@ FwdSplit make_split(const AttnArgs& a, int64_t cus)
     sp.rows = all_rows(a);
     const int64_t wgs = int64_t(a.B) * a.KV * row_tiles(a);
     if (wgs == 0 || wgs >= (few_rows(a) ? 2 : 1) * cus) return sp;
-    const int64_t parts = min64(ceil_div((few_rows(a) ? 4 : 2) * cus, wgs), 512);
+    int64_t parts;
+    if (!few_rows(a)) {
+        parts = ceil_div(2 * cus, wgs);
+    } else if (a.k_starts || a.k_lens) {
+        parts = ceil_div(4 * cus, wgs);
+    } else {
+        parts = 3 * cus / wgs;
+        if (10 * parts * wgs < 9 * 3 * cus) parts = 6 * cus / wgs;
+    }
     const int64_t least = wgs >= cus ? 512 : 128;
-    const int64_t chunk = ceil_div(max64(least, ceil_div(a.Sk, parts)), 64) * 64;
+    const int64_t chunk = ceil_div(max64(least, ceil_div(a.Sk, min64(parts, 512))), 64) * 64;
     sp.splits = int(max64(1, ceil_div(a.Sk, chunk)));
     sp.chunk = int(chunk);
     return sp;
