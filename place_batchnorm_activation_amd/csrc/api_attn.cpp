@@ -217,7 +217,7 @@ size_t iabn_attention_workspace_size(const iabn_attention* p, int backward)
     if (check_problem(p) != IABN_OK || p->batch == 0 || p->heads == 0 || p->q_len == 0) return 0;
     const AttnArgs a = attn_args(p);
     return backward ? attn_bwd_workspace_bytes(a, device_cus())
-                    : attn_fwd_workspace_bytes(a, device_cus());
+                    : attn_fwd_workspace_bytes(a, p->dtype, device_cus());
 }
 
 iabn_status iabn_attention_forward(const iabn_attention* p, const iabn_heads* q,
@@ -236,7 +236,7 @@ iabn_status iabn_attention_forward(const iabn_attention* p, const iabn_heads* q,
     if (!aligned(lse, 4)) return IABN_ERR_MISALIGNED;
     AttnArgs a = attn_args(p);
     const int64_t cus = device_cus();
-    const size_t need = attn_fwd_workspace_bytes(a, cus);
+    const size_t need = attn_fwd_workspace_bytes(a, p->dtype, cus);
     IABN_TRY(check_ws(workspace, workspace_bytes, need));
     const Strided outs[] = {strided(out, s.qb, s.qr, H, D, es), lse_tensor(p, s, lse),
                             flat(need ? workspace : nullptr, int64_t(need))};

@@ -38,7 +38,7 @@ struct AttnGrads {
     Heads dout, dq, dk, dv;
 };
 
-size_t attn_fwd_workspace_bytes(const AttnArgs& a, int64_t cus);
+size_t attn_fwd_workspace_bytes(const AttnArgs& a, int dtype, int64_t cus);
 size_t attn_bwd_workspace_bytes(const AttnArgs& a, int64_t cus);
 void launch_attn_forward(const AttnArgs& a, int dtype, int64_t cus, void* ws, hipStream_t s);
 void launch_attn_backward(const AttnArgs& a, const AttnGrads& g, int dtype, int64_t cus, void* ws,

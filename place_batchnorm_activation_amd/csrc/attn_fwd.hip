@@ -11,7 +11,8 @@
 // Many rows: a workgroup of 4 waves x 32 rows shares the tiles of keys in LDS, two stages,
 // the next tile's loads in flight.  At most 32 rows (single tokens): workgroups of one wave,
 // three stages, no barriers: what counts there is bytes in flight (96 KB a CU; with 64 KB in
-// groups of four waves the same caches were read at 4.6 instead of 5.1 TB/s).  Few
+// groups of four waves that share their tiles the same caches were read at 4.6 instead of
+// 5.1 TB/s), or of four waves that part the keys and join their shares in LDS (keys_inside).  Few
 // workgroups: the keys are cut among several, whose shares (O, m, l in fp32) go through
 // the workspace and are joined by a second kernel.
 #include "attn_tile.hpp"
@@ -26,16 +27,18 @@ struct FwdSplit {
     float* o;                        // [split][row][D]
     float2* ml;                      // [split][row]
     int64_t rows;                    // B * KV * Sq * G
+    bool inside;                     // parts of the keys are waves of one workgroup
 };
 
-// WQ waves of 32 rows.
-template <int DT, int DP, int WQ>
+// WQ waves of 32 rows, or KW waves with a part of the same rows' keys each.
+template <int DT, int DP, int WQ, int KW>
 struct FwdShape {
     static constexpr int NT = 64 * WQ;
     static constexpr int KT = WQ == 1 || DT == kF32 ? 32 : 64;   // keys of a tile
     static constexpr int TILE = KT * TileShape<DT, DP>::PITCH;
-    static constexpr int STAGES = WQ == 1 && DT != kF32 ? 3 : 2;
-    static constexpr int LDS = STAGES * 2 * TILE;
+    static constexpr int STAGES = WQ == 1 && KW == 1 && DT != kF32 ? 3 : 2;
+    static constexpr int LDS = STAGES * 2 * TILE;                // of the waves that share it
+    static_assert(LDS >= 32 * DP * 4, "a wave's share of the results takes its tiles' place");
     static constexpr int WAVES = WQ == 1 || DT == kF32 ? 1 : 2;  // of a SIMD
 };
 
@@ -54,18 +57,20 @@ struct RowOut {
     }
 };
 
-template <int DT, int DP, int WQ>
-__global__ __launch_bounds__(64 * WQ, (FwdShape<DT, DP, WQ>::WAVES)) void k_attn_fwd(
+template <int DT, int DP, int WQ, int KW>
+__global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) void k_attn_fwd(
     AttnArgs a, FwdSplit sp, int tiles)
 {
-    using F = FwdShape<DT, DP, WQ>;
+    using F = FwdShape<DT, DP, WQ, KW>;
+    static_assert(WQ == 1 || KW == 1, "waves for rows or for keys");
     using S = TileShape<DT, DP>;
     constexpr int ES = S::ES, KS = DP / 16, DB = DP / 32, KB = F::KT / 32;
-    __shared__ uint4 space[F::LDS / 16];
-    char* const lds = reinterpret_cast<char*>(space);
+    __shared__ uint4 space[KW * F::LDS / 16];
 
     const int lane = threadIdx.x % 64, h = lane / 32;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int id_wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wave = KW > 1 ? 0 : id_wave, part = KW > 1 ? id_wave : int(blockIdx.y);
+    char* const lds = reinterpret_cast<char*>(space) + (KW > 1 ? part * F::LDS : 0);
     uint32_t head, tile;
     head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), windowed(a), head, tile);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
@@ -101,9 +106,10 @@ __global__ __launch_bounds__(64 * WQ, (FwdShape<DT, DP, WQ>::WAVES)) void k_attn
         row_hi = max(row_lo, row_hi);
     }
 
-    if (sp.splits > 1) {                           // this workgroup's part of them
-        const int64_t first = int64_t(lo) + int64_t(blockIdx.y) * sp.chunk;
-        hi = first < hi ? int(min(int64_t(hi), first + sp.chunk)) : lo;
+    if (KW > 1 || sp.splits > 1) {                 // this workgroup's, or wave's, part of them
+        const int chunk = KW > 1 ? (max(0, hi - lo) + 32 * KW - 1) / (32 * KW) * 32 : sp.chunk;
+        const int64_t first = int64_t(lo) + int64_t(part) * chunk;
+        hi = first < hi ? int(min(int64_t(hi), first + chunk)) : lo;
         lo = first < hi ? int(first) : hi;
     }
     const int steps = hi > lo ? (hi - lo + F::KT - 1) / F::KT : 0;
@@ -121,7 +127,8 @@ __global__ __launch_bounds__(64 * WQ, (FwdShape<DT, DP, WQ>::WAVES)) void k_attn
     if (steps > 0) {
         if (a.D < DP) {
             clear<F::NT>(lds, F::LDS);
-            __syncthreads();
+            arrived<>();
+            if (WQ > 1) __syncthreads();
         }
 #pragma unroll
         for (int i = 0; i + 1 < F::STAGES; ++i)
@@ -260,14 +267,14 @@ __global__ __launch_bounds__(64 * WQ, (FwdShape<DT, DP, WQ>::WAVES)) void k_attn
     RowOut<DT> ro{nullptr, nullptr, 0.f};
     const int64_t id = (int64_t(b) * a.KV + hk) * all_rows + r;
     if (mine) {
-        if (sp.splits > 1) ro.part = sp.o + (int64_t(blockIdx.y) * sp.rows + id) * a.D;
+        if (sp.splits > 1) ro.part = sp.o + (int64_t(part) * sp.rows + id) * a.D;
         ro.out = head_of(a.out, packed_q, b, sq.q0, hq, ES) + int64_t(tok) * a.out.row * ES;
     }
     auto statistics = [&](float m_, float l_) {
         ro.inv = l_ == 0.f ? 0.f : 1.f / l_;
         if (!mine || h != 0) return;
         if (sp.splits > 1) {
-            sp.ml[int64_t(blockIdx.y) * sp.rows + id] = make_float2(m_, l_);
+            sp.ml[int64_t(part) * sp.rows + id] = make_float2(m_, l_);
         } else if (a.lse) {
             const float lse =
                 l_ == 0.f ? -INFINITY : (m_ * a.c + __builtin_amdgcn_logf(l_)) * kLn2A;
@@ -282,9 +289,50 @@ __global__ __launch_bounds__(64 * WQ, (FwdShape<DT, DP, WQ>::WAVES)) void k_attn
             if (d < a.D) ro.put(d, v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
         }
     };
-    statistics(m, l);
+    if constexpr (KW > 1) {
+        // the waves' shares, joined in their order: 8 elements of the rows a wave at a time
+        __shared__ float2 ml[KW][32];
+        float4* const share = reinterpret_cast<float4*>(lds);
 #pragma unroll
-    for (int i = 0; i < DB; ++i) write(i, o[i]);
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                share[(4 * i + g) * 64 + lane] = make_float4(o[i][4 * g], o[i][4 * g + 1],
+                                                             o[i][4 * g + 2], o[i][4 * g + 3]);
+        if (h == 0) ml[part][lane] = make_float2(m, l);
+        __syncthreads();
+        float M = -INFINITY, L = 0.f, f[KW];
+#pragma unroll
+        for (int k = 0; k < KW; ++k) M = fmaxf(M, ml[k][lane % 32].x);
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+            const float2 x = ml[k][lane % 32];
+            f[k] = x.y == 0.f ? 0.f
+                              : __builtin_amdgcn_exp2f((x.x - (M == -INFINITY ? 0.f : M)) * a.c);
+            L += x.y * f[k];
+        }
+        if (part == 0) statistics(M, L);
+        ro.inv = L == 0.f ? 0.f : 1.f / L;
+        for (int u = part; u < a.D / 8; u += KW) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                const float4 s = reinterpret_cast<const float4*>(
+                    reinterpret_cast<const char*>(space) + k * F::LDS)[u * 64 + lane];
+                if (f[k] != 0.f) {                 // else of a part that shows it no key
+                    v.x = fmaf(s.x, f[k], v.x);
+                    v.y = fmaf(s.y, f[k], v.y);
+                    v.z = fmaf(s.z, f[k], v.z);
+                    v.w = fmaf(s.w, f[k], v.w);
+                }
+            }
+            if (mine) ro.put(8 * u + 4 * h, v.x, v.y, v.z, v.w);
+        }
+    } else {
+        statistics(m, l);
+#pragma unroll
+        for (int i = 0; i < DB; ++i) write(i, o[i]);
+    }
 }
 
 // Joins the shares of the key axis.  Few shares: a thread 4 elements of a row, the shares in
@@ -404,6 +452,25 @@ int64_t row_tiles(const AttnArgs& a)
 
 int64_t all_rows(const AttnArgs& a) { return int64_t(a.B) * a.KV * a.Sq * a.G; }
 
+// Whether a few rows' keys are parted among the four waves of one workgroup, which saves the
+// shares' way through memory and a launch, rather than among workgroups or not at all.  Two such
+// workgroups fit a CU for heads up to 64, else one, with 64 KB of loads in flight.  us among
+// workgroups (or in one wave) against inside, 32 heads on 8 of 128:
+//   fewer key heads than CUs, short caches: one of 256 keys 12.3, 8.0; of 517 14.6, 11.1; of 1024
+//   12.6, 14.5; 8 of 517 15.5, 11.1; 8 of 1024 14.6, 16.1;
+//   as many or more, in well filled rounds: 32 of 512 23, 16; of 4096 102, 96; 50 of 1024 55, 40;
+//   128 of 1024 113, 106; but 40 of 4096 138, 155, and short ones of many 64 of 512 26, 29.
+// Heads of 64: 300 caches of 2000 33, 28; of 200 9.3, 6.6; 30 x 16 of 4000 105, 97.
+// Lengths of their own make a workgroup as long as its cache, where parts even them out.
+bool keys_inside(const AttnArgs& a, int64_t wgs, int64_t cus)
+{
+    const bool lengths = a.k_starts || a.k_lens;
+    if (wgs < 2 * cus && a.Sk <= 768) return true;
+    if (wgs < cus) return false;
+    if (a.D <= 64) return !lengths || wgs >= 2 * cus;
+    return !lengths && a.Sk > 768 && 4 * wgs >= 3 * ceil_div(wgs, cus) * cus;
+}
+
 // Parts of the keys where the rows' tiles are too few for the card, each at least 128 keys.
 // Many rows: two workgroups a CU in all.  Few rows: three of the small workgroups fit a CU, and
 // keys of one length come out even where all run in one round, or where one would leave a
@@ -411,17 +478,19 @@ int64_t all_rows(const AttnArgs& a) { return int64_t(a.B) * a.KV * a.Sq * a.G; }
 // parts 189 us, 16 (four a CU) 227; 32 caches of 4096 102, 118; 20 of 6000 in 4 parts 131, 7 108,
 // 9 97.  With lengths of their own part of the workgroups has nothing to do: four a CU (8
 // caches of up to 32768: 2 a CU 195, 3 130, 4 118, 6 142, 16 135).
-// Where each CU has one or two workgroups without parts, a part is at least 512 keys (us without and
-// with parts: 32 caches of 4096, 8 heads of 128, 148, 118; of 1024 39, 29; of 512 23, 26).
-// (Least keys 64, 128, 256: 517 keys of 8 heads of 64 11, 13, 16; 8192 of 8 of 128 27, 20, 21; 1027
-// rows over 777 keys, f32, 36, 32, 40.)
-FwdSplit make_split(const AttnArgs& a, int64_t cus)
+// Where each CU has one or two workgroups without parts, a part is at least 512 keys (us without
+// and with parts: 40 caches of 4096, 8 heads of 128, 163, 135; of 1024 40, 34).
+// (Least keys 64, 128, 256: 8192 of 8 heads of 128 27, 20, 21; 1027 rows over 777 keys, f32, 36,
+// 32, 40.)
+FwdSplit make_split(const AttnArgs& a, int dtype, int64_t cus)
 {
     FwdSplit sp{};
     sp.splits = 1;
     sp.chunk = a.Sk;
     sp.rows = all_rows(a);
     const int64_t wgs = int64_t(a.B) * a.KV * row_tiles(a);
+    sp.inside = few_rows(a) && dtype != kF32 && keys_inside(a, wgs, cus);
+    if (sp.inside) return sp;
     if (wgs == 0 || wgs >= (few_rows(a) ? 2 : 1) * cus) return sp;
     int64_t parts;
     if (!few_rows(a)) {
@@ -441,15 +510,15 @@ FwdSplit make_split(const AttnArgs& a, int64_t cus)
 
 }  // namespace
 
-size_t attn_fwd_workspace_bytes(const AttnArgs& a, int64_t cus)
+size_t attn_fwd_workspace_bytes(const AttnArgs& a, int dtype, int64_t cus)
 {
-    const int64_t splits = make_split(a, cus).splits;
+    const int64_t splits = make_split(a, dtype, cus).splits;
     return splits > 1 ? size_t(splits) * size_t(all_rows(a)) * size_t(4 * a.D + 8) : 0;
 }
 
 void launch_attn_forward(const AttnArgs& a, int dtype, int64_t cus, void* ws, hipStream_t s)
 {
-    FwdSplit sp = make_split(a, cus);
+    FwdSplit sp = make_split(a, dtype, cus);
     sp.o = static_cast<float*>(ws);
     sp.ml = reinterpret_cast<float2*>(sp.o + sp.splits * sp.rows * a.D);
     const int tiles = int(row_tiles(a));
@@ -458,10 +527,17 @@ void launch_attn_forward(const AttnArgs& a, int dtype, int64_t cus, void* ws, hi
         constexpr int DT = decltype(d)::value;
         auto go = [&](auto p) {
             constexpr int DP = decltype(p)::value;
+            if constexpr (DT != kF32) {
+                if (sp.inside) {
+                    hipLaunchKernelGGL((k_attn_fwd<DT, DP, 1, 4>), grid, dim3(256), 0, s, a, sp,
+                                       tiles);
+                    return;
+                }
+            }
             if (few_rows(a))
-                hipLaunchKernelGGL((k_attn_fwd<DT, DP, 1>), grid, dim3(64), 0, s, a, sp, tiles);
+                hipLaunchKernelGGL((k_attn_fwd<DT, DP, 1, 1>), grid, dim3(64), 0, s, a, sp, tiles);
             else
-                hipLaunchKernelGGL((k_attn_fwd<DT, DP, 4>), grid, dim3(256), 0, s, a, sp, tiles);
+                hipLaunchKernelGGL((k_attn_fwd<DT, DP, 4, 1>), grid, dim3(256), 0, s, a, sp, tiles);
         };
         if (a.D <= 64) go(std::integral_constant<int, 64>{});
         else if (a.D <= 96) go(std::integral_constant<int, 96>{});

@@ -305,7 +305,7 @@ struct Tiles {
 template <int NT>
 __device__ __forceinline__ void clear(char* p, int bytes)
 {
-    for (int i = int(threadIdx.x) * 16; i < bytes; i += NT * 16)
+    for (int i = int(threadIdx.x) % NT * 16; i < bytes; i += NT * 16)
         *reinterpret_cast<uint4*>(p + i) = make_uint4(0, 0, 0, 0);
 }
 

@@ -204,6 +204,39 @@ def test_a_very_long_cache(dtype):
 
 
 @DT
+@pytest.mark.parametrize("B,Sq,Sk,H,KV,D", ((32, 1, 900, 16, 8, 128), (70, 2, 300, 8, 8, 64),
+                                            (66, 1, 1030, 16, 8, 40), (40, 1, 800, 16, 8, 96)))
+def test_many_caches(dtype, B, Sq, Sk, H, KV, D):
+    """One or two tokens for each of many caches: as many key heads as CUs, and more."""
+    q, k, v, _ = make(37, B, Sq, Sk, H, KV, D, dtype)
+    spec = iabn.AttentionSpec(causal=True)
+    out, lse = torch.full_like(q, math.nan), iabn.attention_lse(q).fill_(math.nan)
+    iabn.iabn_attention_forward(spec, q, k, v, out, lse, iabn.attention_workspace(spec, q, k))
+    val, bound = heads_ref.attention(q, k, v, right=0)
+    check(dict(out=out, lse=lse), val, bound)
+
+
+@DT
+@pytest.mark.parametrize("left,right", ((-1, 0), (40, 0), (3, 300)))
+@pytest.mark.parametrize("D", (24, 64, 104))
+def test_few_rows_over_short_keys(dtype, left, right, D):
+    """Waves of one workgroup that part the keys: lengths of zero, one and all, windows that
+    leave some waves, and some rows, nothing, and what lies behind a length."""
+    ql, kl = [5, 0, 3, 5, 1, 5], [700, 33, 0, 1, 512, 3]
+    q, k, v, _ = make(38, 6, 5, 700, 6, 2, D, dtype)
+    for b in range(6):
+        q[b, ql[b]:] = math.nan
+        k[b, kl[b]:] = v[b, kl[b]:] = math.nan
+    spec = iabn.AttentionSpec(window=(left, right))
+    seq = dict(q_lens=lens(ql), k_lens=lens(kl))
+    out, lse = torch.full_like(q, math.nan), iabn.attention_lse(q).fill_(math.nan)
+    iabn.iabn_attention_forward(spec, q, k, v, out, lse,
+                                iabn.attention_workspace(spec, q, k, **seq), **seq)
+    val, bound = heads_ref.attention(q, k, v, left=left, right=right, q_lens=ql, k_lens=kl)
+    check(dict(out=out, lse=lse), val, bound)
+
+
+@DT
 @pytest.mark.parametrize("Sq,Sk,H,KV", ((24, 9000, 4, 1), (3000, 40, 8, 2), (1500, 1500, 2, 1)))
 def test_parted_gradients(dtype, Sq, Sk, H, KV):
     """Few row tiles over many keys, few key tiles under many rows: shares that are joined."""
