@@ -62,14 +62,14 @@ for _fn in ("iabn_attention_forward", "iabn_attention_backward", "iabn_rotary",
 # ---------------------------------------------------------------------------
 # tensors of heads
 
-def _heads(t, name, shape, ref=None):
-    """t as the library takes it; shape is what it must be, ref a tensor of its type and
-    device."""
+def _heads(t, name, shape, dtype=None, device=None):
+    """t as the library takes it; shape is what it must be, dtype and device (an index) too
+    where given."""
     if t.shape != shape:
         raise ValueError("%s is %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if ref is not None and (t.dtype != ref.dtype or t.get_device() != ref.get_device()):
-        raise TypeError("%s is %s on %s, expected %s on %s" % (name, t.dtype, t.device, ref.dtype,
-                                                              ref.device))
+    if dtype is not None and (t.dtype != dtype or t.get_device() != device):
+        raise TypeError("%s is %s on %s, expected %s on %s" % (
+            name, t.dtype, t.device, dtype, "cpu" if device < 0 else "cuda:%d" % device))
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1 and t.numel() > 0:
         raise ValueError("%s: a head's elements must be contiguous" % name)
@@ -108,25 +108,24 @@ class AttentionSpec:
             raise ValueError("k is %s, expected %s" % (tuple(k.shape), "[rows, heads, head_dim] "
                              "with k_starts" if k_starts is not None else
                              "[batch, rows, heads, head_dim]"))
-        H, D = q.shape[-2:]
-        KV = k.shape[-2]
-        batch = q.shape[0] if q_starts is None else \
-            k.shape[0] if k_starts is None else q_starts.numel() - 1
-        if k_starts is None and k.shape[0] != batch:
-            raise ValueError("q has %d sequences, k %d" % (batch, k.shape[0]))
+        qs, ks = q.shape, k.shape
+        H, D, KV = qs[-2], qs[-1], ks[-2]
+        batch = qs[0] if q_starts is None else ks[0] if k_starts is None else \
+            q_starts.numel() - 1
+        if k_starts is None and ks[0] != batch:
+            raise ValueError("q has %d sequences, k %d" % (batch, ks[0]))
         if H and (KV == 0 or H % KV):
             raise ValueError("%d query heads are no multiple of %d key heads" % (H, KV))
-        for starts, rows, most, side in ((q_starts, q.shape[0], max_q, "q"),
-                                         (k_starts, k.shape[0], max_k, "k")):
+        for starts, most, side in ((q_starts, max_q, "q"), (k_starts, max_k, "k")):
             if starts is not None and most is None:
                 raise ValueError("packed %s needs max_%s, the most rows of a sequence"
                                  % (side, side))
         scale = 1.0 / math.sqrt(max(1, D)) if self.scale is None else self.scale
         return _Problem(
-            batch, H, KV, D, q.shape[1] if q_starts is None else max_q,
-            k.shape[1] if k_starts is None else max_k, _dtype_code(q), scale, self.left,
+            batch, H, KV, D, qs[1] if q_starts is None else max_q,
+            ks[1] if k_starts is None else max_k, _dtype_code(q), scale, self.left,
             self.right, _counts(q_starts, "q_starts", batch + 1, q),
-            _counts(k_starts, "k_starts", batch + 1, q), q.shape[0], k.shape[0],
+            _counts(k_starts, "k_starts", batch + 1, q), qs[0], ks[0],
             _counts(q_lens, "q_lens", batch, q), _counts(k_lens, "k_lens", batch, q))
 
 
@@ -165,8 +164,9 @@ def iabn_attention_forward(spec, q, k, v, out, lse=None, workspace=None, q_start
     Packed: [rows, heads, head_dim] with q_starts (k_starts) int32 [batch + 1] on the GPU
     and max_q (max_k), the most rows of a sequence."""
     p = spec._problem(q, k, q_starts, k_starts, q_lens, k_lens, max_q, max_k)
-    at = (_heads(q, "q", q.shape), _heads(k, "k", k.shape, q), _heads(v, "v", k.shape, q),
-          _heads(out, "out", q.shape, q))
+    qs, ks, on = q.shape, k.shape, (q.dtype, q.get_device())
+    at = (_heads(q, "q", qs), _heads(k, "k", ks, *on), _heads(v, "v", ks, *on),
+          _heads(out, "out", qs, *on))
     lp = _lse(lse, q)
     ws, wb = _space(workspace, q)
     s = _stream(stream, q)
@@ -180,9 +180,10 @@ def iabn_attention_backward(spec, q, k, v, out, lse, dout, dq, dk, dv, workspace
     """dq, dk and dv from dout and the forward's out and lse; workspace:
     attention_workspace(..., backward=True)."""
     p = spec._problem(q, k, q_starts, k_starts, q_lens, k_lens, max_q, max_k)
-    at = (_heads(q, "q", q.shape), _heads(k, "k", k.shape, q), _heads(v, "v", k.shape, q),
-          _heads(out, "out", q.shape, q), _heads(dout, "dout", q.shape, q),
-          _heads(dq, "dq", q.shape, q), _heads(dk, "dk", k.shape, q), _heads(dv, "dv", k.shape, q))
+    qs, ks, on = q.shape, k.shape, (q.dtype, q.get_device())
+    at = (_heads(q, "q", qs), _heads(k, "k", ks, *on), _heads(v, "v", ks, *on),
+          _heads(out, "out", qs, *on), _heads(dout, "dout", qs, *on), _heads(dq, "dq", qs, *on),
+          _heads(dk, "dk", ks, *on), _heads(dv, "dv", ks, *on))
     if lse is None:
         raise ValueError("the backward needs the forward's lse")
     lp = _lse(lse, q)
@@ -250,7 +251,8 @@ def iabn_rotary(spec, positions, q, q_out, k=None, k_out=None, inverse=False, st
     if q.dim() not in (3, 4):
         raise ValueError("q is %s, expected [batch, rows, heads, head_dim]" % (tuple(q.shape),))
     packed = q.dim() == 3
-    lead, D, dev = tuple(q.shape[:-2]), q.shape[-1], q.get_device()
+    qs, dtype, dev = q.shape, q.dtype, q.get_device()
+    lead, D = tuple(qs[:-2]), qs[-1]
     if D != spec.head_dim:
         raise ValueError("the spec has heads of %d, q of %d" % (spec.head_dim, D))
     B, S = (1, lead[0]) if packed else lead
@@ -272,16 +274,17 @@ def iabn_rotary(spec, positions, q, q_out, k=None, k_out=None, inverse=False, st
                 _flat(spec.inv_freq, "inv_freq", n, torch.float64, dev),
                 _flat(spec.axis, "axis", n, torch.int32, dev), positions.data_ptr(),
                 _POS_TYPES[positions.dtype], pos_batch, pos_row)
-    qp, qo = _heads(q, "q", q.shape), _heads(q_out, "q_out", q.shape, q)
+    qp, qo = _heads(q, "q", qs), _heads(q_out, "q_out", qs, dtype, dev)
     KV, kp, ko = 0, None, None
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     if k is not None:
         KV = k.shape[-2] if k.dim() == q.dim() else -1
         k_shape = lead + (KV, D)
-        kp, ko = _heads(k, "k", k_shape, q), _heads(k_out, "k_out", k_shape, q)
+        kp = _heads(k, "k", k_shape, dtype, dev)
+        ko = _heads(k_out, "k_out", k_shape, dtype, dev)
     s = _stream(stream, q)
-    _check("iabn_rotary", lib.iabn_rotary(ctypes.byref(r), qp, q.shape[-2], qo, kp, KV, ko,
+    _check("iabn_rotary", lib.iabn_rotary(ctypes.byref(r), qp, qs[-2], qo, kp, KV, ko,
                                           int(bool(inverse)), s))
 
 
