@@ -38,6 +38,13 @@ struct AttnGrads {
     Heads dout, dq, dk, dv;
 };
 
+// The most keys that some of n neighbouring queries see (of queries that n neighbouring keys are
+// seen by).
+inline int64_t seen_most(const AttnArgs& a, int64_t n, int64_t most)
+{
+    return min64(most, int64_t(a.left) + a.right + n);
+}
+
 size_t attn_fwd_workspace_bytes(const AttnArgs& a, int dtype, int64_t cus);
 size_t attn_bwd_workspace_bytes(const AttnArgs& a, int64_t cus);
 void launch_attn_forward(const AttnArgs& a, int dtype, int64_t cus, void* ws, hipStream_t s);

@@ -23,7 +23,8 @@ namespace {
 constexpr float kLazy = 8.f;         // binary orders that the running maximum may lag behind
 
 struct FwdSplit {
-    int splits, chunk;               // workgroups of the keys, and keys of each
+    int splits, chunk;               // workgroups of the keys, and (at least) keys of each
+    float places;                    // 0, or workgroups of a key head that all sequences share
     float* o;                        // [split][row][D]
     float2* ml;                      // [split][row]
     int64_t rows;                    // B * KV * Sq * G
@@ -41,6 +42,22 @@ struct FwdShape {
     static_assert(LDS >= 32 * DP * 4, "a wave's share of the results takes its tiles' place");
     static constexpr int WAVES = WQ == 1 || DT == kF32 ? 1 : 2;  // of a SIMD
 };
+
+// Keys of a part with which few rows' sequences of their own lengths take about `places`
+// workgroups of a key head in all; every sequence then has parts of one size (k_attn_fwd).  (us
+// for one token over 8 caches, 8 key heads of 128, with 16 parts of a fixed size, and with these:
+// all of 32768 keys 226, 196; of random lengths up to that 175, 112, and 143 if parts do not move
+// on among the CUs (head_and_tile); one of 32768 beside 7 of 200 79, 61; 20 caches of random
+// lengths up to 6000 82, 57; 32 of 4096 118, 105.)
+__device__ __forceinline__ int even_chunk(const AttnArgs& a, float places)
+{
+    float all = 0.f;
+    for (int i = int(threadIdx.x) % 64; i < a.B; i += 64)
+        all += float(min(lane_sequence(a, i).lk, a.left + a.right + a.Sq));
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) all += __shfl_xor(all, x, 64);
+    return scalar((int(all / places) + 64) / 64 * 64);
+}
 
 // The results of one row, d = d0 .. d0 + 3 of it at a time.
 template <int DT>
@@ -72,7 +89,8 @@ __global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) vo
     const int wave = KW > 1 ? 0 : id_wave, part = KW > 1 ? id_wave : int(blockIdx.y);
     char* const lds = reinterpret_cast<char*>(space) + (KW > 1 ? part * F::LDS : 0);
     uint32_t head, tile;
-    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), windowed(a), head, tile);
+    head_and_tile(uint32_t(a.B) * a.KV, uint32_t(tiles), windowed(a), head, tile,
+                  WQ == 1 ? blockIdx.y : 0);
     const int b = int(head / uint32_t(a.KV)), hk = int(head % uint32_t(a.KV));
     tile = uint32_t(tiles) - 1 - tile;             // causal rows with many keys first
     const Sequence sq = sequence_of(a, b);
@@ -107,7 +125,12 @@ __global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) vo
     }
 
     if (KW > 1 || sp.splits > 1) {                 // this workgroup's, or wave's, part of them
-        const int chunk = KW > 1 ? (max(0, hi - lo) + 32 * KW - 1) / (32 * KW) * 32 : sp.chunk;
+        int chunk = KW > 1 ? (max(0, hi - lo) + 32 * KW - 1) / (32 * KW) * 32 : sp.chunk;
+        if (WQ == 1 && KW == 1 && sp.places > 0.f && hi > lo) {
+            chunk = max(chunk, even_chunk(a, sp.places));
+            const int n = (hi - lo + chunk - 1) / chunk;
+            chunk = ((hi - lo + n - 1) / n + 63) / 64 * 64;
+        }
         const int64_t first = int64_t(lo) + int64_t(part) * chunk;
         hi = first < hi ? int(min(int64_t(hi), first + chunk)) : lo;
         lo = first < hi ? int(first) : hi;
@@ -462,48 +485,54 @@ int64_t all_rows(const AttnArgs& a) { return int64_t(a.B) * a.KV * a.Sq * a.G; }
 //   128 of 1024 113, 106; but 40 of 4096 138, 155, and short ones of many 64 of 512 26, 29.
 // Heads of 64: 300 caches of 2000 33, 28; of 200 9.3, 6.6; 30 x 16 of 4000 105, 97.
 // Lengths of their own make a workgroup as long as its cache, where parts even them out.
-bool keys_inside(const AttnArgs& a, int64_t wgs, int64_t cus)
+bool keys_inside(const AttnArgs& a, int64_t keys, int64_t wgs, int64_t cus)
 {
     const bool lengths = a.k_starts || a.k_lens;
-    if (wgs < 2 * cus && a.Sk <= 768) return true;
+    if (wgs < 2 * cus && keys <= 768) return true;
     if (wgs < cus) return false;
     if (a.D <= 64) return !lengths || wgs >= 2 * cus;
-    return !lengths && a.Sk > 768 && 4 * wgs >= 3 * ceil_div(wgs, cus) * cus;
+    return !lengths && keys > 768 && 4 * wgs >= 3 * ceil_div(wgs, cus) * cus;
 }
 
-// Parts of the keys where the rows' tiles are too few for the card, each at least 128 keys.
-// Many rows: two workgroups a CU in all.  Few rows: three of the small workgroups fit a CU, and
-// keys of one length come out even where all run in one round, or where one would leave a
-// tenth of the places free, in two: for one token over 8 caches of 32768, 8 key heads of 128, 12
-// parts 189 us, 16 (four a CU) 227; 32 caches of 4096 102, 118; 20 of 6000 in 4 parts 131, 7 108,
-// 9 97.  With lengths of their own part of the workgroups has nothing to do: four a CU (8
-// caches of up to 32768: 2 a CU 195, 3 130, 4 118, 6 142, 16 135).
+// Parts of the keys where the rows' tiles are too few for the card, each at least 128 keys, of
+// those that a tile can see.  Many rows: as many workgroups as a CU holds, two (f32 with more
+// than 64 elements one).  Few rows: three of the small workgroups fit a CU, and keys of one length come out even
+// where all run in one round, or where one would leave a tenth of the places free, in two: for
+// one token over 8 caches of 32768, 8 key heads of 128, 12 parts 189 us, 16 (four a CU) 227; 32
+// caches of 4096 102, 118; 20 of 6000 in 4 parts 131, 7 108, 9 97.  Lengths of their own are
+// known on the device only: it chooses parts that fill nine tenths of a round (even_chunk; half
+// a part a sequence for the last ones), or of two where a sequence would have one or two.
 // Where each CU has one or two workgroups without parts, a part is at least 512 keys (us without
 // and with parts: 40 caches of 4096, 8 heads of 128, 163, 135; of 1024 40, 34).
-// (Least keys 64, 128, 256: 8192 of 8 heads of 128 27, 20, 21; 1027 rows over 777 keys, f32, 36,
-// 32, 40.)
+// (Least keys 64, 128, 256: 8192 of 8 heads of 128 27, 20, 21.  Parts of what a window of 4096
+// keys shows instead of the whole cache: 8 caches of 32768 97, 30.)
 FwdSplit make_split(const AttnArgs& a, int dtype, int64_t cus)
 {
     FwdSplit sp{};
     sp.splits = 1;
-    sp.chunk = a.Sk;
     sp.rows = all_rows(a);
+    const bool few = few_rows(a);
     const int64_t wgs = int64_t(a.B) * a.KV * row_tiles(a);
-    sp.inside = few_rows(a) && dtype != kF32 && keys_inside(a, wgs, cus);
+    const int64_t keys = seen_most(a, few ? a.Sq : 128 / a.G + 2, a.Sk);    // of a tile
+    sp.chunk = int(keys);
+    sp.inside = few && dtype != kF32 && keys_inside(a, keys, wgs, cus);
     if (sp.inside) return sp;
-    if (wgs == 0 || wgs >= (few_rows(a) ? 2 : 1) * cus) return sp;
+    if (wgs == 0 || wgs >= (few ? 2 : 1) * cus) return sp;
     int64_t parts;
-    if (!few_rows(a)) {
-        parts = ceil_div(2 * cus, wgs);
+    if (!few) {
+        parts = ceil_div((dtype == kF32 && a.D > 64 ? 1 : 2) * cus, wgs);
     } else if (a.k_starts || a.k_lens) {
-        parts = ceil_div(4 * cus, wgs);
+        parts = ceil_div(6 * cus, wgs);
+        const float round = 3.f * float(cus) / float(a.KV);
+        sp.places = 0.9f * round - 0.5f * float(a.B);
+        if (sp.places < 2.f * float(a.B)) sp.places += 0.9f * round;
     } else {
         parts = 3 * cus / wgs;
         if (10 * parts * wgs < 9 * 3 * cus) parts = 6 * cus / wgs;
     }
     const int64_t least = wgs >= cus ? 512 : 128;
-    const int64_t chunk = ceil_div(max64(least, ceil_div(a.Sk, min64(parts, 512))), 64) * 64;
-    sp.splits = int(max64(1, ceil_div(a.Sk, chunk)));
+    const int64_t chunk = ceil_div(max64(least, ceil_div(keys, min64(parts, 512))), 64) * 64;
+    sp.splits = int(max64(1, ceil_div(keys, chunk)));
     sp.chunk = int(chunk);
     return sp;
 }

@@ -334,7 +334,7 @@ struct RowFrags {
         Frag<DT> f;
 #pragma unroll
         for (int i = 0; i < (DT == kF32 ? 2 : 1); ++i) {
-            const uint32_t x = DT == kF32 ? at ^ uint32_t(64 * ks + 16 * i) : at ^ uint32_t(32 * ks);
+            const uint32_t x = at ^ uint32_t(DT == kF32 ? 64 * ks + 16 * i : 32 * ks);
             const uint4 q = *reinterpret_cast<const uint4*>(tile + row0 * S::PITCH + x);
             f.w[4 * i] = q.x; f.w[4 * i + 1] = q.y; f.w[4 * i + 2] = q.z; f.w[4 * i + 3] = q.w;
         }
@@ -439,11 +439,18 @@ __device__ __forceinline__ int64_t lse_index(const AttnArgs& a, const Sequence& 
 // 16 heads of 64: forward 93, 76, dQ 125, 107; twice 4096 tokens of 32 heads on 8, dK and dV: 850,
 // 640.  Without a mask, also of different lengths, across is slower: 16 of up to 1024 tokens, 32
 // heads of 128: forward 197, 202.)
+//
+// part: of those that blockIdx.y counts.  An XCD deals its workgroups to four groups of CUs in
+// turn, whatever their work; sequences of different lengths, whose parts would meet the same CUs
+// again and again, move on by one with each part.  (One token over 8 caches of up to 32768: see
+// even_chunk in attn_fwd.hip.)
 __device__ __forceinline__ void head_and_tile(uint32_t heads, uint32_t tiles, bool across,
-                                              uint32_t& head, uint32_t& tile)
+                                              uint32_t& head, uint32_t& tile, uint32_t part = 0)
 {
     const uint32_t xcds = heads % 8 == 0 ? 8 : 1;
-    const uint32_t x = blockIdx.x % xcds, i = blockIdx.x / xcds;
+    const uint32_t x = blockIdx.x % xcds;
+    uint32_t i = blockIdx.x / xcds;
+    if (part > 0) i = (i + part) % (heads / xcds * tiles);
     if (across) {
         tile = i / (heads / xcds);
         head = x + xcds * (i % (heads / xcds));

@@ -237,6 +237,24 @@ def test_few_rows_over_short_keys(dtype, left, right, D):
 
 
 @DT
+@pytest.mark.parametrize("padded", (False, True))
+@pytest.mark.parametrize("Sq,left,right", ((1, 2000, 0), (6, 1500, 40), (300, 900, 130)))
+def test_windows_over_long_keys(dtype, Sq, left, right, padded):
+    """Parts of what a window shows: few rows and many, sequences of their own lengths."""
+    ql, kl = [Sq, max(1, Sq // 2), Sq], [5000, 3100, 77]
+    q, k, v, _ = make(39, 3, Sq, 5000, 4, 2, 72, dtype)
+    seq, know = {}, {}
+    if padded:
+        seq, know = dict(q_lens=lens(ql), k_lens=lens(kl)), dict(q_lens=ql, k_lens=kl)
+    spec = iabn.AttentionSpec(window=(left, right))
+    out, lse = torch.full_like(q, math.nan), iabn.attention_lse(q).fill_(math.nan)
+    iabn.iabn_attention_forward(spec, q, k, v, out, lse,
+                                iabn.attention_workspace(spec, q, k, **seq), **seq)
+    val, bound = heads_ref.attention(q, k, v, left=left, right=right, **know)
+    check(dict(out=out, lse=lse), val, bound)
+
+
+@DT
 @pytest.mark.parametrize("Sq,Sk,H,KV", ((24, 9000, 4, 1), (3000, 40, 8, 2), (1500, 1500, 2, 1)))
 def test_parted_gradients(dtype, Sq, Sk, H, KV):
     """Few row tiles over many keys, few key tiles under many rows: shares that are joined."""
