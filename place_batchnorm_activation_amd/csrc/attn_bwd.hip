@@ -680,32 +680,39 @@ __global__ __launch_bounds__(256) void k_attn_dkv_join(AttnArgs a, AttnGrads g, 
     }
 }
 
-// Workgroups of a row tile's keys: two for every CU in all, each part at least 128 keys.
+// Workgroups of the keys that a row tile can see: two for every CU in all, each part at least 128
+// keys.
 Parts dq_parts(const AttnArgs& a, int64_t cus)
 {
     Parts pt{};
     const int64_t wgs = int64_t(a.B) * a.KV * ceil_div(int64_t(a.Sq) * a.G, 128);
     const int64_t want = wgs > 0 && wgs < cus ? ceil_div(2 * cus, wgs) : 1;
-    const int64_t parts = max64(1, min64(want, a.Sk / 128));
-    pt.chunk = int(max64(1, ceil_div(ceil_div(a.Sk, parts), 64)) * 64);
-    pt.parts = int(max64(1, ceil_div(a.Sk, pt.chunk)));
+    const int64_t keys = seen_most(a, 128 / a.G + 2, a.Sk);
+    const int64_t parts = max64(1, min64(want, keys / 128));
+    pt.chunk = int(max64(1, ceil_div(ceil_div(keys, parts), 64)) * 64);
+    pt.parts = int(max64(1, ceil_div(keys, pt.chunk)));
     return pt;
 }
 
-// Workgroups of a key tile's rows: two for every CU in all, and twice as many where a window
-// gives key tiles different numbers of rows, which two resident workgroups a CU do not even
-// out (twice 4096 causal tokens of 32 heads on 8: 890 us in one part, 640 in two and 28 to
-// join them); each part at least 128 rows.
+// Workgroups of the rows that can see a key tile: two for every CU in all, and twice as many where
+// a mask of one side gives key tiles different numbers of rows, which two resident workgroups a
+// CU do not even out (twice 4096 causal tokens of 32 heads on 8: 890 us in one part, 640 in two
+// and 28 to join them); each part at least 128 rows, or 256 of the few that a window of two sides
+// shows (2 x 4096 tokens, 128 to either side, 4 heads of 64: the backward 33 us in one part, 47
+// in three).  Parts of what a window shows instead of all rows: 16384 tokens, the last 1024, 8
+// heads on one of 128, 556 us and 356.
 Parts dkv_parts(const AttnArgs& a, int64_t cus)
 {
     Parts pt{};
-    const int64_t wgs = int64_t(a.B) * a.KV * ceil_div(a.Sk, 128), rows = int64_t(a.Sq) * a.G;
-    const bool uneven = a.left < kAttnMaxLen || a.right < kAttnMaxLen;
+    const int64_t wgs = int64_t(a.B) * a.KV * ceil_div(a.Sk, 128);
+    const int64_t rows = seen_most(a, 128, a.Sq) * a.G;
+    const bool window = a.left < kAttnMaxLen && a.right < kAttnMaxLen;
+    const bool uneven = !window && (a.left < kAttnMaxLen || a.right < kAttnMaxLen);
     const int64_t want = wgs > 0 ? ceil_div((uneven ? 4 : 2) * cus, wgs) : 1;
-    const int64_t parts = max64(1, min64(want, rows / 128));
+    const int64_t parts = max64(1, min64(want, rows / (window ? 256 : 128)));
     // whole tiles of rows and whole groups
     const int64_t unit = int64_t(64) * a.G;
-    const int64_t chunk = max64(1, ceil_div(ceil_div(rows, parts), unit)) * unit;
+    const int64_t chunk = max64(1, (ceil_div(rows, parts) + unit / 2) / unit) * unit;
     pt.parts = int(max64(1, ceil_div(rows, chunk)));
     pt.chunk = int(min64(chunk, max64(1, rows)));
     return pt;

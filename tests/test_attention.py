@@ -265,6 +265,16 @@ def test_parted_gradients(dtype, Sq, Sk, H, KV):
 
 
 @DT
+@pytest.mark.parametrize("left,right,H,KV", ((300, 20, 2, 1), (700, 0, 5, 1), (0, 400, 2, 2)))
+def test_parted_gradients_under_windows(dtype, left, right, H, KV):
+    """Parts of what a window shows of long sequences, the queries behind the keys and before."""
+    for Sq, Sk in ((1900, 2200), (2100, 1500)):
+        q, k, v, do = make(40, 1, Sq, Sk, H, KV, 40, dtype)
+        spec = iabn.AttentionSpec(window=(left, right))
+        check(both(q, k, v, do, spec), *heads_ref.attention(q, k, v, do, left=left, right=right))
+
+
+@DT
 def test_parted_padded_batch(dtype):
     """Joined shares under lengths: tiles that end inside a length, padded keys and rows."""
     ql, kl = [1400, 77, 0, 900], [1400, 500, 300, 0]
