@@ -540,7 +540,8 @@ size_t iabn_attention_workspace_size(const iabn_attention *problem, int backward
 /* out = softmax(scale * q k^T) v over the visible keys; lse: fp32 [batch, heads, q_len]
  * (packed queries: [heads, q_rows]), log of the sum of exp(scale * q k^T), or NULL.  out
  * overlaps none of q, k, v.  Softmax statistics and sums are fp32; for 16-bit types the
- * probabilities are rounded to them before they meet v.  workspace: device, 16-byte aligned,
+ * probabilities are rounded to them before they meet v (float16: raised by a power of two
+ * first, so that those down to 2^-25 of a row's largest keep their digits).  workspace: device, 16-byte aligned,
  * iabn_attention_workspace_size(problem, 0) bytes; it carries no status word. */
 iabn_status iabn_attention_forward(const iabn_attention *problem, const iabn_heads *q,
                                    const iabn_heads *k, const iabn_heads *v,

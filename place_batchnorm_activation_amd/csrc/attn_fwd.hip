@@ -4,9 +4,13 @@
 // One pass over the keys with the running maximum m and sum l of each row:
 //   S^T = K Q^T,  P^T = exp(S^T - m),  O^T += V^T P^T,
 // O and l scaled by exp(m_old - m_new) when m grows, which is left until it grows by more
-// than 2^8 (P then stays below 2^8, and the sums are fp32).  A wave holds 32 rows (rows of
-// a key head: attn.hpp) in registers, Q and O^T both; the statistics are scalars of the
-// lane, one exchange with the other half of the wave a tile.
+// than a factor (Range) that P then stays below; the sums are fp32.  A wave holds 32 rows
+// (rows of a key head: attn.hpp) in registers, Q and O^T both; the statistics are scalars of
+// the lane, one exchange with the other half of the wave a tile.
+//
+// P is rounded to the storage type for its product with V, which the matrix units take in one
+// type only (in two parts it would keep 16 digits, for half as many products again): half a
+// step a term, as the output's own rounding.  l sums it as it was.
 //
 // Many rows: a workgroup of 4 waves x 32 rows shares the tiles of keys in LDS, two stages,
 // the next tile's loads in flight.  At most 32 rows (single tokens): workgroups of one wave,
@@ -20,13 +24,45 @@
 namespace iabn {
 
 namespace {
-constexpr float kLazy = 8.f;         // binary orders that the running maximum may lag behind
+// Binary orders that the running maximum may lag behind, and that P is raised by.  bfloat16 and
+// float32 have float32's range.  float16 loses digits below 2^-14 and everything below 2^-25,
+// and over long caches with one large score (of a key whose value is near zero) the small
+// probabilities are the result: there P is raised as far as the lag leaves room (to 2^15), so that
+// what is more than 2^-25 of a row's largest (17.3 below its score) keeps its digits, and the
+// next ten orders some of them.  A shorter lag costs more changes of the sums: us for lag and
+// raise 8 and 0, 8 and 7, 4 and 11, 2 and 13: 2 x 4096 causal tokens, 32 heads on 8 of 128, 294,
+// 294, 295, 298, with scores spread four times as wide 289, 291, 297, 300; 4 x 2048 tokens, 16
+// heads of 64, 89.5, 89.4, 89.3, 90.8; single tokens the same.
+template <int DT>
+struct Range {
+    static constexpr float lazy = DT == kF16 ? 4.f : 8.f, up = DT == kF16 ? 11.f : 0.f;
+
+    // log2 of what P = exp2(s c - base) is relative to, for a maximum of m.  float16: rounded up,
+    // so that P passes 2^15 at no size of the scores.
+    static __device__ __forceinline__ float base(float m, float c)
+    {
+        if (m == -INFINITY) return 0.f;
+        const float b = fmaf(m, c, -up);
+        return DT == kF16 ? fmaf(fabsf(b), 0x1p-23f, b) : b;
+    }
+};
+
+// A row's statistics for its shares and its log-sum-exp: sum exp(S) = 2^x * y.
+template <int DT>
+__device__ __forceinline__ float2 share_stats(float m, float l, float c)
+{
+    return make_float2(m == -INFINITY ? -INFINITY : Range<DT>::base(m, c), l);
+}
+__device__ __forceinline__ float lse_of(float2 st)
+{
+    return st.y == 0.f ? -INFINITY : (st.x + __builtin_amdgcn_logf(st.y)) * kLn2A;
+}
 
 struct FwdSplit {
     int splits, chunk;               // workgroups of the keys, and (at least) keys of each
     float places;                    // 0, or workgroups of a key head that all sequences share
     float* o;                        // [split][row][D]
-    float2* ml;                      // [split][row]
+    float2* ml;                      // [split][row]: share_stats
     int64_t rows;                    // B * KV * Sq * G
     bool inside;                     // parts of the keys are waves of one workgroup
 };
@@ -215,9 +251,12 @@ __global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) vo
         };
         read_v(0);
         mx = both_max(mx);
-        if (__any((mx - m) * a.c > kLazy)) {
+        if (__any((mx - m) * a.c > Range<DT>::lazy)) {
             const float nm = fmaxf(m, mx);
-            const float e = __builtin_amdgcn_exp2f((m - (nm == -INFINITY ? 0.f : nm)) * a.c);
+            const float e =
+                m == -INFINITY ? 0.f
+                               : __builtin_amdgcn_exp2f(Range<DT>::base(m, a.c) -
+                                                        Range<DT>::base(nm, a.c));
             m = nm;
             l *= e;
 #pragma unroll
@@ -225,7 +264,7 @@ __global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) vo
 #pragma unroll
                 for (int j = 0; j < 16; ++j) o[i][j] *= e;
         }
-        const float base = m == -INFINITY ? 0.f : m * a.c;
+        const float base = Range<DT>::base(m, a.c);
         auto probs = [&](int t) {                  // of 16 keys
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -293,16 +332,11 @@ __global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) vo
         if (sp.splits > 1) ro.part = sp.o + (int64_t(part) * sp.rows + id) * a.D;
         ro.out = head_of(a.out, packed_q, b, sq.q0, hq, ES) + int64_t(tok) * a.out.row * ES;
     }
-    auto statistics = [&](float m_, float l_) {
-        ro.inv = l_ == 0.f ? 0.f : 1.f / l_;
+    auto statistics = [&](float2 st) {
+        ro.inv = st.y == 0.f ? 0.f : 1.f / st.y;
         if (!mine || h != 0) return;
-        if (sp.splits > 1) {
-            sp.ml[int64_t(part) * sp.rows + id] = make_float2(m_, l_);
-        } else if (a.lse) {
-            const float lse =
-                l_ == 0.f ? -INFINITY : (m_ * a.c + __builtin_amdgcn_logf(l_)) * kLn2A;
-            a.lse[lse_index(a, sq, b, hq, tok)] = lse;
-        }
+        if (sp.splits > 1) sp.ml[int64_t(part) * sp.rows + id] = st;
+        else if (a.lse) a.lse[lse_index(a, sq, b, hq, tok)] = lse_of(st);
     };
     auto write = [&](int db, const f32x16_t& v) {
         if (!mine || (sp.splits > 1 && steps == 0)) return;
@@ -322,7 +356,7 @@ __global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) vo
             for (int g = 0; g < 4; ++g)
                 share[(4 * i + g) * 64 + lane] = make_float4(o[i][4 * g], o[i][4 * g + 1],
                                                              o[i][4 * g + 2], o[i][4 * g + 3]);
-        if (h == 0) ml[part][lane] = make_float2(m, l);
+        if (h == 0) ml[part][lane] = share_stats<DT>(m, l, a.c);
         __syncthreads();
         float M = -INFINITY, L = 0.f, f[KW];
 #pragma unroll
@@ -331,10 +365,10 @@ __global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) vo
         for (int k = 0; k < KW; ++k) {
             const float2 x = ml[k][lane % 32];
             f[k] = x.y == 0.f ? 0.f
-                              : __builtin_amdgcn_exp2f((x.x - (M == -INFINITY ? 0.f : M)) * a.c);
+                              : __builtin_amdgcn_exp2f(x.x - (M == -INFINITY ? 0.f : M));
             L += x.y * f[k];
         }
-        if (part == 0) statistics(M, L);
+        if (part == 0) statistics(make_float2(M, L));
         ro.inv = L == 0.f ? 0.f : 1.f / L;
         for (int u = part; u < a.D / 8; u += KW) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -352,7 +386,7 @@ __global__ __launch_bounds__(64 * WQ * KW, (FwdShape<DT, DP, WQ, KW>::WAVES)) vo
             if (mine) ro.put(8 * u + 4 * h, v.x, v.y, v.z, v.w);
         }
     } else {
-        statistics(m, l);
+        statistics(share_stats<DT>(m, l, a.c));
 #pragma unroll
         for (int i = 0; i < DB; ++i) write(i, o[i]);
     }
@@ -381,7 +415,7 @@ __global__ __launch_bounds__(256) void k_attn_join_few(AttnArgs a, FwdSplit sp, 
     for (int s = 0; s < sp.splits; ++s) {
         const float2 x = sp.ml[s * sp.rows + id];
         if (x.y == 0.f) continue;                  // saw no key
-        const float f = __builtin_amdgcn_exp2f((x.x - ref) * a.c);
+        const float f = __builtin_amdgcn_exp2f(x.x - ref);
         const float4 p = *reinterpret_cast<const float4*>(sp.o + (s * sp.rows + id) * a.D + d);
         L += x.y * f;
         v[0] += p.x * f; v[1] += p.y * f; v[2] += p.z * f; v[3] += p.w * f;
@@ -391,10 +425,7 @@ __global__ __launch_bounds__(256) void k_attn_join_few(AttnArgs a, FwdSplit sp, 
                 int64_t(tok) * a.out.row * ES;
     if (inv == 0.f) store4<DT>(out, d, 0.f, 0.f, 0.f, 0.f);
     else store4<DT>(out, d, v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    if (d == 0 && a.lse) {
-        const float lse = L == 0.f ? -INFINITY : (M * a.c + __builtin_amdgcn_logf(L)) * kLn2A;
-        a.lse[lse_index(a, sq, b, hq, tok)] = lse;
-    }
+    if (d == 0 && a.lse) a.lse[lse_index(a, sq, b, hq, tok)] = lse_of(make_float2(M, L));
 }
 
 // More: a wave a row, 4 elements a lane, the halves of the wave every other share, eight of
@@ -424,7 +455,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, FwdSplit sp)
         float f = 0.f;
         if (s0 + lane < sp.splits) {
             const float2 x = ml[(s0 + lane) * sp.rows];
-            if (x.y != 0.f) f = __builtin_amdgcn_exp2f((x.x - ref) * a.c);      // 0: saw no key
+            if (x.y != 0.f) f = __builtin_amdgcn_exp2f(x.x - ref);      // 0: saw no key
             L += x.y * f;
         }
         const int n = min(64, sp.splits - s0);
@@ -459,10 +490,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, FwdSplit sp)
         if (inv == 0.f) store4<DT>(out, d, 0.f, 0.f, 0.f, 0.f);
         else store4<DT>(out, d, v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
     }
-    if (lane == 0 && a.lse) {
-        const float lse = L == 0.f ? -INFINITY : (M * a.c + __builtin_amdgcn_logf(L)) * kLn2A;
-        a.lse[lse_index(a, sq, b, hq, tok)] = lse;
-    }
+    if (lane == 0 && a.lse) a.lse[lse_index(a, sq, b, hq, tok)] = lse_of(make_float2(M, L));
 }
 
 // At most 32 rows a key head: the waves share the rows and part the keys.

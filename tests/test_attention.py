@@ -473,3 +473,82 @@ def test_long_offsets():
     val, bound = heads_ref.attention(q, k, v, right=0)
     heads_ref.within(out[b:], val["out"], bound["out"], "out")
     assert (out[:b] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# one key far above all others, with a value of zero: the small probabilities are the result
+
+def sink(dtype, n, gap, rows=1, heads=1, D=64):
+    """q, k, v, dout of one sequence whose first key's score lies `gap` above the others', which are
+    equal (exactly: scale 1, one element that counts)."""
+    g = torch.Generator().manual_seed(n + int(10 * gap))
+    q, k = torch.zeros(1, rows, heads, D), torch.zeros(1, n, heads, D)
+    q[..., 0], k[:, 0, :, 0] = 1.0, gap
+    v = 1 + 0.25 * torch.randn(1, n, heads, D, generator=g)
+    v[:, 0] = 0
+    do = torch.randn(1, rows, heads, D, generator=g)
+    return [t.to(dtype).cuda() for t in (q, k, v, do)]
+
+
+GAPS = pytest.mark.parametrize("gap", (12.5, 15.0, 16.5, 17.0, 17.5, 18.0))
+
+
+@DT
+@GAPS
+@pytest.mark.parametrize("B,rows,n", ((1, 1, 517), (1, 1, 4096), (1, 1, 32768), (520, 1, 517),
+                                      (520, 1, 4096), (520, 1, 32768), (1, 300, 517),
+                                      (1, 300, 4096), (1, 300, 32768), (140, 200, 517),
+                                      (140, 200, 4096)))
+def test_small_probabilities_beside_a_large_one(dtype, gap, n, B, rows):
+    """Parts among workgroups, waves of one workgroup (517 keys), and whole rows in one wave or
+    four (as many sequences as fill the card, all of the same tensors)."""
+    q, k, v, _ = sink(dtype, n, gap, rows)
+    val, bound = heads_ref.attention(q, k, v, scale=1.0)
+    q, k, v = (t.expand(B, -1, -1, -1) for t in (q, k, v))
+    out = torch.full(q.shape, math.nan, dtype=dtype, device="cuda")
+    lse = iabn.attention_lse(q).fill_(math.nan)
+    spec = iabn.AttentionSpec(scale=1.0)
+    iabn.iabn_attention_forward(spec, q, k, v, out, lse, iabn.attention_workspace(spec, q, k))
+    for b in (0, B - 1):
+        check(dict(out=out[b:b + 1], lse=lse[b:b + 1]), val, bound)
+    assert (out == out[:1]).all() and (lse == lse[:1]).all()
+
+
+@DT
+@GAPS
+@pytest.mark.parametrize("n", (517, 4096))
+def test_gradients_of_small_probabilities(dtype, gap, n):
+    """heads_ref's bounds take delta's own out as rounded by u |out|.  Here out is as small as 8e-6,
+    among float16's subnormals, whose rounding is off by up to TINY = 2^-25 (u |out| is 4e-9): with
+    |delta - exact| up to sum_d |dO| TINY more, dS is off by P times that, and dq and dk by its sums
+    with |k| and |q|, doubled as the rest of the bound."""
+    q, k, v, do = sink(dtype, n, gap, rows=200, heads=2)
+    val, bound = heads_ref.attention(q, k, v, do, scale=1.0)
+    q6, k6, do6 = (t[0].transpose(0, 1).double().cpu() for t in (q, k, do))      # [heads, rows, D]
+    p = torch.softmax(q6 @ k6.transpose(1, 2), -1)
+    off = p * do6.abs().sum(-1, keepdim=True) * 2 * heads_ref.TINY[dtype]
+    bound["dq"] += (off @ k6.abs()).transpose(0, 1)
+    bound["dk"] += (off.transpose(1, 2) @ q6.abs()).transpose(0, 1)
+    check(both(q, k, v, do, iabn.AttentionSpec(scale=1.0)), val, bound)
+
+
+@DT
+@pytest.mark.parametrize("size", (2.0 ** 6, 2.0 ** 10, 2.0 ** 12, 1.1 * 2.0 ** 13))
+@pytest.mark.parametrize("rows,n", ((1, 517), (1, 3000), (200, 300)))
+def test_equal_scores_of_any_size(dtype, size, rows, n):
+    """Scores of 2^12 to 2^26, all the same: whatever the scaled maximum's rounding makes of their
+    exponentials (an order or two at 2^26), it is one value P and cancels: out is the values'
+    mean, off by P's rounding to the type (u), the sums' (n e each) and its own (u), of sum |v| / n,
+    doubled."""
+    g = torch.Generator().manual_seed(41)
+    q, k = torch.zeros(1, rows, 2, 64), torch.zeros(1, n, 2, 64)
+    q[..., 3] = k[..., 3] = size
+    v = torch.randn(1, n, 2, 64, generator=g)
+    q, k, v = (t.to(dtype).cuda() for t in (q, k, v))
+    out = torch.full_like(q, math.nan)
+    spec = iabn.AttentionSpec(scale=1.0)
+    iabn.iabn_attention_forward(spec, q, k, v, out, None, iabn.attention_workspace(spec, q, k))
+    v6 = v.double().cpu()
+    bound = 2 * (2 * heads_ref.HALF[dtype] + 2 * n * heads_ref.E) * v6.abs().mean(1, keepdim=True)
+    heads_ref.within(out, v6.mean(1, keepdim=True).expand(1, rows, 2, 64),
+                     bound.expand(1, rows, 2, 64))
