@@ -196,8 +196,19 @@ class KVCache:
         b = torch.arange(B, device=k.device)[:, None].expand(B, n)
         self.k.index_put_((b, at), k.to(self.k.dtype))
         self.v.index_put_((b, at), v.to(self.v.dtype))
-        self.lens += n if counts is None else counts.to(torch.int32).clamp(0, n)
+        self.lens += self._counted(n, counts)
         self.used += n
+
+    def _take_back(self, n, counts=None):
+        """Undoes the last append, of n rows with these counts, whose rows are written over by
+        the next one."""
+        if n > 0:
+            self.lens -= self._counted(n, counts)
+            self.used -= n
+
+    @staticmethod
+    def _counted(n, counts):
+        return n if counts is None else counts.to(torch.int32).clamp(0, n)
 
 
 class ResidualAttention(torch.nn.Module):
@@ -213,7 +224,7 @@ class ResidualAttention(torch.nn.Module):
     max_len.  positions as iabn_rotary takes them (default: 0, 1, 2, ... on every axis of
     unpacked rows, behind a cache's tokens).  lens: int32 [batch], the rows that count.  cache: a
     KVCache that the rows' keys and values are appended to and which they attend
-    (without gradients)."""
+    (without gradients); a refused call leaves it as it was."""
 
     def __init__(self, cols, heads, kv_heads=None, head_dim=None, post="rms", pre="rms", alpha=1.0,
                  gate=False, rotary: Optional[RotarySpec] = None, causal=True, window=(-1, -1),
@@ -267,19 +278,23 @@ class ResidualAttention(torch.nn.Module):
             raise RuntimeError("a cache keeps no graph: use torch.no_grad()")
         if starts is not None:
             raise ValueError("a cache takes unpacked rows")
+        if cache.k.dtype != qkv.dtype:
+            raise TypeError("the cache is %s, the block's heads are %s" % (cache.k.dtype, qkv.dtype))
         q, k, v = qkv.split((self.heads, self.kv_heads, self.kv_heads), -2)
         if self.rotary is not None:
             iabn_rotary(self.rotary, positions, q, q, k, k)
         cache.append(k, v, lens)
-        out = _fresh(q)
-        keys, values = cache.k[:, :cache.used], cache.v[:, :cache.used]
-        if keys.dtype != q.dtype:
-            raise TypeError("the cache is %s, the block's heads are %s" % (keys.dtype, q.dtype))
-        seq = dict(k_lens=cache.lens)
-        if lens is not None:
-            seq["q_lens"] = lens
-        iabn_attention_forward(self.spec, q, keys, values, out, None,
-                               attention_workspace(self.spec, q, keys, **seq), **seq)
+        try:
+            out = _fresh(q)
+            keys, values = cache.k[:, :cache.used], cache.v[:, :cache.used]
+            seq = dict(k_lens=cache.lens)
+            if lens is not None:
+                seq["q_lens"] = lens
+            iabn_attention_forward(self.spec, q, keys, values, out, None,
+                                   attention_workspace(self.spec, q, keys, **seq), **seq)
+        except Exception:                          # a refused call leaves the cache as it was
+            cache._take_back(q.shape[1], lens)
+            raise
         return out
 
 

@@ -233,6 +233,38 @@ def test_cache_refuses():
         A.ResidualAttention(96, 4, rotary=iabn.RotarySpec(32))
 
 
+def test_a_refused_call_leaves_the_cache_as_it_was():
+    """Of another type, with lengths that the attention refuses, with a spec that the library
+    does: what the cache counts is what it held, and the call made right then gives what it gives
+    on a fresh cache."""
+    x, y = rnd(32, 2, 5, 96), rnd(33, 2, 3, 96)
+    lens = torch.tensor([2, 3], dtype=torch.int32, device="cuda")
+
+    def state(cache):
+        return cache.used, cache.lens.tolist()
+
+    block = make_block()
+    with torch.no_grad():
+        other = A.KVCache(2, 16, 2, 24, BF16)
+        with pytest.raises(TypeError, match="cache is"):
+            block(x, cache=other)
+        assert state(other) == (0, [0, 0]) and not other.k.any() and not other.v.any()
+        cache, fresh = A.KVCache(2, 16, 2, 24, F32), A.KVCache(2, 16, 2, 24, F32)
+        block(x, cache=cache), block(x, cache=fresh)
+        for bad, error in ((lens.long(), TypeError), (lens.cpu(), (TypeError, RuntimeError)),
+                           (lens[:1], ValueError)):
+            with pytest.raises(error):
+                block(y, cache=cache, lens=bad)
+            assert state(cache) == (5, [5, 5]), bad
+        right, block.spec = block.spec, iabn.AttentionSpec(scale=-1.0, causal=True)
+        with pytest.raises((ValueError, RuntimeError)):
+            block(y, cache=cache, lens=lens)
+        assert state(cache) == (5, [5, 5])
+        block.spec = right
+        got, want = (block(y, cache=c, lens=lens)[1] for c in (cache, fresh))
+        assert torch.equal(got, want) and state(cache) == state(fresh) == (8, [7, 8])
+
+
 def test_block_with_16_bit_layers_and_autocast():
     """float32 stream, bf16 layers; and autocast over float32 ones: against the float32 block to
     the rounding of a few bf16 layers (2^-8 each of five: 2% in the 2-norm)."""
