@@ -125,15 +125,20 @@ def rotary(spec: RotarySpec, positions, q, k=None):
 class QKVAttentionFunction(torch.autograd.Function):
     """The output of attention from a projection qkv [..., heads + 2 kv_heads, head_dim], whose
     queries and keys are first turned where they lie: qkv must be an intermediate that nothing
-    else reads or keeps (KeptLinear keeps its input, not its output).  Keeps qkv as turned, the
-    output and the rows' log-sum-exp; the backward writes one gradient for the projection,
-    without joining parts."""
+    else reads or keeps (KeptLinear keeps its input, not its output).  Autograd is told: a leaf is
+    refused here, and an operation that kept qkv for its own backward refuses it there.  Keeps
+    qkv as turned, the output and the rows' log-sum-exp; the backward writes one gradient for
+    the projection, without joining parts."""
 
     @staticmethod
     def forward(ctx, qkv, positions, heads, kv_heads, turn, spec, seq):
+        if turn is not None and qkv.is_leaf and qkv.requires_grad:
+            raise RuntimeError("a leaf that requires a gradient would be turned in place: pass a "
+                               "copy of it")
         q, k, v = qkv.split((heads, kv_heads, kv_heads), -2)
         if turn is not None:
             iabn_rotary(turn, positions, q, q, k, k)
+            torch.autograd.graph.increment_version(qkv)
         out = _outputs(q, seq.get("q_starts") is not None)
         train = ctx.needs_input_grad[0]
         lse = attention_lse(q) if train else None
@@ -141,7 +146,8 @@ class QKVAttentionFunction(torch.autograd.Function):
                                **seq)
         if train:
             names, tensors, plain = _kept(seq)
-            ctx.save_for_backward(qkv, positions, out, lse, *tensors)
+            # detached: its own graph, which the turn does not follow, has no part in the backward
+            ctx.save_for_backward(qkv.detach(), positions, out, lse, *tensors)
             ctx.cfg = (heads, kv_heads, turn, spec, names, plain)
         return out
 
@@ -160,6 +166,16 @@ class QKVAttentionFunction(torch.autograd.Function):
         if turn is not None:
             iabn_rotary(turn, positions, dq, dq, dk, dk, inverse=True)
         return grad, None, None, None, None, None, None
+
+
+def _projected(layer, turn, *inputs):
+    """The layer's output; where it will be turned in place, a copy if a hook may have kept it, or
+    a layer of another kind may."""
+    t = layer(*inputs)
+    if turn is None or type(layer) in (KeptLinear, torch.nn.Linear) and not (
+            layer._forward_hooks or torch.nn.modules.module._global_forward_hooks):
+        return t
+    return t.clone()
 
 
 class KVCache:
@@ -261,7 +277,7 @@ class ResidualAttention(torch.nn.Module):
                 raise ValueError("packed rows need their positions")
             positions = self._positions(n.shape, n.device, cache)
         H, KV, D = self.heads, self.kv_heads, self.head_dim
-        qkv = self.qkv(n, kept).view(*n.shape[:-1], H + 2 * KV, D)
+        qkv = _projected(self.qkv, self.rotary, n, kept).view(*n.shape[:-1], H + 2 * KV, D)
         if cache is not None:
             a = self._cached(qkv, positions, lens, starts, cache)
         else:
@@ -329,7 +345,7 @@ class MapAttention(torch.nn.Module):
         if self.rotary is not None:
             grid = [torch.arange(n, dtype=torch.int32, device=x.device) for n in x.shape[2:]]
             positions = torch.stack(torch.meshgrid(*grid, indexing="ij"), -1).flatten(0, -2)
-        qkv = self.qkv(rows)
+        qkv = _projected(self.qkv, self.rotary, rows)
         qkv = qkv.view(*rows.shape[:-1], 3 * self.heads, qkv.shape[-1] // (3 * self.heads))
         a = QKVAttentionFunction.apply(qkv, positions, self.heads, self.heads, self.rotary,
                                        self.spec, {})

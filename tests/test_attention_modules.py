@@ -162,6 +162,85 @@ def test_residual_attention():
     assert off(block.out.weight.grad, leaves["out.weight"].grad) < 1e-4
 
 
+def plainly(block, x, keeps):
+    """The block's branch with its projection through `keeps`, by operations that turn nothing
+    in place."""
+    _, n, kept = block.norm(x)
+    H, KV = block.heads, block.kv_heads
+    qkv = keeps(block.qkv(n, kept)).unflatten(-1, (H + 2 * KV, block.head_dim))
+    q, k, v = qkv.split((H, KV, KV), -2)
+    pos = torch.arange(x.shape[1], dtype=torch.int32, device="cuda")
+    return block.out(A.attention(*A.rotary(block.rotary, pos, q, k), v, causal=True).flatten(-2))
+
+
+@pytest.mark.parametrize("everywhere", (False, True))
+def test_hooks_that_keep_the_projection(everywhere):
+    """A hook may record the projection, or replace it by an operation that keeps its result for
+    its own backward: neither finds it turned.  (The same kernels on the same values, in one
+    buffer or three: sums in one order, 2^-20 for torch's own products.)"""
+    block, x, g = make_block(), rnd(34, 2, 30, 96).requires_grad_(), rnd(35, 2, 30, 96)
+    with torch.no_grad():
+        want = block.qkv(block.norm(x)[1])
+    seen = []
+
+    def hook(layer, args, out):
+        if layer is not block.qkv:
+            return None
+        seen.append(out.detach())
+        return out.tanh()
+
+    def grads(out):
+        out.backward(g)
+        got = [x.grad] + [p.grad for p in (block.qkv.weight, block.out.weight)]
+        x.grad = None
+        block.zero_grad()
+        return [out, *got]
+
+    handle = torch.nn.modules.module.register_module_forward_hook(hook) if everywhere else \
+        block.qkv.register_forward_hook(hook)
+    try:
+        got = grads(block(x)[1])
+        with torch.no_grad():
+            block(x, cache=A.KVCache(2, 30, 2, 24, F32))
+    finally:
+        handle.remove()
+    for t in seen:
+        assert off(t, want) < 2.0 ** -20
+    assert len(seen) == 2
+    for a, b in zip(got, grads(plainly(block, x, torch.tanh))):
+        assert off(a, b) < 2.0 ** -20
+
+
+def test_a_hook_that_keeps_a_maps_projection():
+    torch.manual_seed(7)
+    m, x = A.MapAttention(48, 2, groups=4, device="cuda"), rnd(36, 2, 48, 6, 5)
+    seen = []
+    with m.qkv.register_forward_hook(lambda layer, args, out: seen.append(out)):
+        want = m(x)
+    assert off(seen[0], m.qkv(m.norm(x).movedim(1, -1).flatten(1, -2))) < 2.0 ** -20
+    assert off(m(x), want) < 2.0 ** -20
+
+
+def test_a_kept_projection_is_refused():
+    """Turned in place behind an operation that keeps its result, or over a leaf."""
+    turn = iabn.RotarySpec(24)
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")
+    x = rnd(37, 1, 9, 8, 24).requires_grad_()
+    apply = lambda t: A.QKVAttentionFunction.apply(t, pos, 4, 2, turn, iabn.AttentionSpec(),  # noqa: E731
+                                                   {})
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        apply(x.tanh()).sum().backward()
+    before = x.detach().clone()
+    with pytest.raises(RuntimeError, match="leaf"):
+        apply(x)
+    assert torch.equal(x, before)
+    out = apply(x * 1)                             # an intermediate, twice through its graph
+    out.sum().backward(retain_graph=True)
+    once = x.grad.clone()
+    out.sum().backward()
+    assert torch.equal(x.grad, 2 * once)
+
+
 def test_packed_equals_padded():
     block = make_block(sections=(5, 7))
     ls = [13, 30, 1]
