@@ -610,8 +610,8 @@ size_t iabn_group_norm_workspace_size(const iabn_group_norm *layer);
 
 /* y = act(xhat * weight + bias), xhat = (x - mean) * rstd over a sample's group,
  * rstd = 1 / sqrt(biased variance + eps).  stats: fp32 [n, groups, 2], mean and rstd, or NULL.
- * y may be exactly x.  Rows n*hw below 2^31, c below 2^26.  workspace: device, 16-byte aligned;
- * it carries no status word. */
+ * y may be exactly x.  Rows n*hw below 2^31, c below 2^26, groups below 2^24.  workspace: device,
+ * 16-byte aligned; it carries no status word. */
 iabn_status iabn_group_norm_forward(const iabn_group_norm *layer, const void *x, int64_t ldx,
                                     void *y, int64_t ldy, float *stats, void *workspace,
                                     size_t workspace_bytes, hipStream_t stream);

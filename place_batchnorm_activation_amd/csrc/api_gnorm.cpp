@@ -14,6 +14,7 @@ using namespace iabn;
 namespace {
 
 constexpr int64_t kGnMaxC = int64_t(1) << 26;
+constexpr int64_t kGnMaxGroups = int64_t(1) << 24;  // a workgroup of 256 each: threads in 32 bits
 
 iabn_status check_gn(const iabn_group_norm* l)
 {
@@ -23,7 +24,7 @@ iabn_status check_gn(const iabn_group_norm* l)
     if (!isfinite(l->act_param) || !(l->eps >= 0.f) || !isfinite(l->eps)) return IABN_ERR_INVALID_ARG;
     IABN_TRY(check_vec(l->weight));
     IABN_TRY(check_vec(l->bias));
-    if (l->c >= kGnMaxC || double(l->n) * double(l->hw) > double(kMaxExtent) || l->n > kMaxExtent ||
+    if (l->c >= kGnMaxC || l->groups >= kGnMaxGroups || double(l->n) * double(l->hw) > double(kMaxExtent) || l->n > kMaxExtent ||
         l->hw > kMaxExtent)
         return IABN_ERR_UNSUPPORTED;
     return IABN_OK;

@@ -204,3 +204,26 @@ def test_gradients_against_differences():
         diff = (value(*up) - value(*down)) / (2 * h)
         want = float((got[name].double() * u.double()).sum())
         assert abs(diff - want) <= 1e-3 * math.sqrt(x.numel()), (name, diff, want)
+
+
+def test_the_most_groups():
+    """2^24 - 1 groups of one channel and two rows: every one is written.  With d half the pair's
+    difference, xhat = +-d rstd and rstd = 1/sqrt(d^2 + eps), to a few roundings of float32 (2^-20
+    of it); the gradients are those of that function."""
+    G, eps = (1 << 24) - 1, 0.1
+    x, dy = (torch.randn(1, 2, G, generator=torch.Generator(device="cuda").manual_seed(s),
+                         device="cuda") for s in (16, 17))
+    got = both(x, dy, G, None, None, "identity", eps=eps)
+    x6, dy6 = x.double(), dy.double()
+    half = (x6[:, 0] - x6[:, 1]) / 2
+    rstd = (half.square() + eps).rsqrt()
+    xhat = torch.stack((half * rstd, -half * rstd), 1)
+    m, mx = dy6.mean(1, keepdim=True), (dy6 * xhat).mean(1, keepdim=True)
+    dx = rstd[:, None] * (dy6 - m - xhat * mx)
+    for name, want, size in (("y", xhat, xhat.abs() + 1), ("stats", torch.stack((x6.mean(1), rstd), -1),
+                                                           rstd[..., None] + x6.abs().amax(1)[..., None]),
+                             ("dx", dx, rstd[:, None] * (dy6.abs().sum(1, keepdim=True) + 1)),
+                             ("dbias", dy6.sum((0, 1)), dy6.abs().sum((0, 1))),
+                             ("dweight", (dy6 * xhat).sum((0, 1)), dy6.abs().sum((0, 1)) + 1)):
+        off = (got[name].double() - want).abs()
+        assert bool((off <= 2.0 ** -20 * size).all()), (name, float((off / size).max()))

@@ -213,6 +213,21 @@ def test_group_norm_validation():
     assert gn_backward(dx=None, dw=None, db=None) == OK
 
 
+@pytest.mark.parametrize("groups", (1 << 24, (1 << 24) + 1, 3 << 24))
+def test_group_norm_of_too_many_groups(groups):
+    """A workgroup a group passes a launch's 2^32 threads: refused, and not after the first of
+    several kernels.  One group less goes on to the workspace."""
+    for call in (gn_forward, gn_backward):
+        wide = dict(n=1, hw=2, c=groups, groups=groups, weight=None, bias=None, ldx=groups)
+        ld = dict(ldy=groups) if call is gn_forward else dict(lddy=groups, lddx=groups, dw=None,
+                                                              db=None)
+        assert call(ws=None, **wide, **ld) == UNSUPPORTED
+        if groups == 1 << 24:
+            less = {n: v - 1 if v == groups else v for n, v in dict(wide, **ld).items()}
+            assert call(ws=None, **less) == WS
+    assert lib.iabn_group_norm_workspace_size(ref(gn(n=1, hw=2, c=groups, groups=groups))) == 0
+
+
 # ---------------------------------------------------------------------------
 # the binding, before it looks for a GPU
 
