@@ -25,7 +25,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x2_any4_t __attribute__((ext_vector_type(2), aligned(2)));
 
 constexpr float kLog2eA = 1.44269504088896341f;
 constexpr float kLn2A = 0.693147180559945309f;
@@ -195,13 +194,18 @@ __device__ __forceinline__ uint32_t lds_address(const char* p)
 
 // 16 bytes a lane from base + offset to LDS, lane l's to dst + 16 * l (dst the same in all
 // lanes).  In assembly, since the compiler would wait for it before any other access to
-// LDS; the wait is arrived()'s.
+// LDS; the wait is arrived()'s.  (The compiler warns of a clobbered m0, which it reserves: it
+// never keeps a value there, but an m0 that it set for instructions of its own it sets again
+// behind a statement that names it.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void to_lds(const char* base, uint32_t offset, uint32_t dst)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :: "s"(dst), "v"(offset), "s"(base)
-                 : "memory");
+                 : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 // DP: the head's elements as the kernel counts them, a multiple of 32 (those past D are
 // zeros).  Rows are NC 16-byte chunks apart, a power of two; chunk c of row r lies at
