@@ -16,7 +16,7 @@
 //
 // P and dS enter their second products in the storage type.  float16 has a range that P and
 // dS leave downwards (P is 2^-15 over 32768 keys; dS has dO's scale besides): there P is
-// carried times 2^10, and dS times a power of two of each lane's own, found from the
+// carried times 2^14, and dS times a power of two of each lane's own, found from the
 // largest magnitude so far and changed, with the sums, when a larger one would come near
 // the type's end.
 #include "attn_tile.hpp"
@@ -25,7 +25,10 @@ namespace iabn {
 
 namespace {
 
-constexpr float kUpP = 10.f;                       // f16: binary orders that P is raised by
+// f16: binary orders that P, at most 1, is raised by: what is above 2^-28 keeps its digits.  The
+// two orders left to the type's end are for the roundings of score and log-sum-exp, which pass
+// them where |score| is beyond 2^23 and P means nothing any more.
+constexpr int kUpP = 14;
 
 // The factor of dS of a lane's column, a power of two.  It begins where no dS of float16
 // tensors overflows float32, and falls to where the largest so far is far inside float16.
@@ -507,7 +510,7 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
         if (threadIdx.x < F::QT && r < hi) {
             const int t = int(fast_div(uint32_t(r), a.group));
             const float lse = a.lse[lse_index(a, sq, b, hk * a.G + r - t * a.G, t)];
-            if (lse != -INFINITY) il = lse * kLog2eA - (DT == kF16 ? kUpP : 0.f);
+            if (lse != -INFINITY) il = lse * kLog2eA - (DT == kF16 ? float(kUpP) : 0.f);
             id = delta[(int64_t(b) * a.KV + hk) * all_rows + r];
         }
     };
@@ -616,7 +619,7 @@ __global__ __launch_bounds__(256, (DkvShape<DT, DP>::WAVES)) void k_attn_dkv(Att
             ++i;
         }
     }
-    const float up = DT == kF16 ? 0x1p-10f : 1.f, f = a.scale * up / scaled.up;
+    const float up = DT == kF16 ? 1.f / (1 << kUpP) : 1.f, f = a.scale * up / scaled.up;
     if (shared) {
         if (j >= sq.lk) return;
         float* share = share_of<2>(pt, head, uint32_t(tiles), tile, int(blockIdx.y), a.D) +

@@ -552,3 +552,23 @@ def test_equal_scores_of_any_size(dtype, size, rows, n):
     bound = 2 * (2 * heads_ref.HALF[dtype] + 2 * n * heads_ref.E) * v6.abs().mean(1, keepdim=True)
     heads_ref.within(out, v6.mean(1, keepdim=True).expand(1, rows, 2, 64),
                      bound.expand(1, rows, 2, 64))
+
+
+@DT
+@pytest.mark.parametrize("gap", (18.5, 18.8, 19.1, 19.4))
+def test_value_gradients_of_small_probabilities(dtype, gap):
+    """dv of keys far below another one, under gradients of one sign as large as a loss scale makes
+    them: P of 2^-27 to
+    2^-28 of the row's largest keeps its digits.  The bound is heads_ref's without what it allows
+    float16 to lose there: u |dv| + sum P (u + x + m e) |dO|, m rows, doubled."""
+    rows, n, D, u, e = 200, 517, 64, heads_ref.HALF[dtype], heads_ref.E
+    q, k, v, do = sink(dtype, n, gap, rows)
+    do = do.abs() * 256
+    dv = both(q, k, v, do, iabn.AttentionSpec(scale=1.0))["dv"]
+    q6, k6, do6 = (t[0, :, 0].double().cpu() for t in (q, k, do))
+    s = q6 @ k6.T
+    p = torch.softmax(s, -1)
+    x = 2 * (D + 2) * e * s.abs().amax(1, keepdim=True) + 2.0 ** -22 + n * e
+    want = p.T @ do6
+    bound = 2 * (u * want.abs() + (p * (u + x + rows * e)).T @ do6.abs() + heads_ref.TINY[dtype])
+    heads_ref.within(dv[0, :, 0], want, bound, "dv")
