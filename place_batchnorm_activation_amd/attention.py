@@ -29,6 +29,13 @@ def _heads(t):
     return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
 
 
+def _head_dim(D):
+    """D, where the attention takes heads of so many elements."""
+    if D % 8 or not 8 <= D <= 128:
+        raise ValueError("heads of %d elements: a multiple of 8 up to 128 is needed" % D)
+    return D
+
+
 def _fresh(t):
     return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
@@ -253,7 +260,8 @@ class ResidualAttention(torch.nn.Module):
         if rotary is not None and rotary.head_dim != head_dim:
             raise ValueError("the rotary spec has heads of %d, the block of %d"
                              % (rotary.head_dim, head_dim))
-        self.heads, self.kv_heads, self.head_dim, self.rotary = heads, kv_heads, head_dim, rotary
+        self.heads, self.kv_heads, self.head_dim = heads, kv_heads, _head_dim(head_dim)
+        self.rotary = rotary
         self.spec = AttentionSpec(scale, causal, window)
         self.norm = ResNorm(cols, post, pre, alpha, gate=gate, device=device)
         self.qkv = KeptLinear(cols, (heads + 2 * kv_heads) * head_dim, bias=False, device=device,
@@ -325,7 +333,7 @@ class MapAttention(torch.nn.Module):
         super().__init__()
         if channels % heads:
             raise ValueError("%d heads do not divide %d channels" % (heads, channels))
-        self.heads, self.axes, D = heads, axes, channels // heads
+        self.heads, self.axes, D = heads, axes, _head_dim(channels // heads)
         self.norm = GroupNormAct(groups, channels, eps, activation="identity", device=device)
         self.qkv = KeptLinear(channels, 3 * channels, device=device, dtype=dtype)
         self.out = torch.nn.Linear(channels, channels, device=device, dtype=dtype)

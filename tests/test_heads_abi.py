@@ -342,3 +342,17 @@ def test_binding_refuses_group_norm():
         fwd(stats=torch.empty(2, 5, 2))
     with pytest.raises(TypeError, match="live on the GPU"):
         fwd()
+
+
+def test_modules_refuse_head_sizes():
+    """When they are made, not when they are called (and where no kernel would take them)."""
+    from place_batchnorm_activation_amd import attention as A
+    for channels, heads in ((512, 1), (48, 4), (160, 1), (24, 8)):
+        with pytest.raises(ValueError, match="heads of %d elements" % (channels // heads)):
+            A.MapAttention(channels, heads, groups=4, rotary=False)
+        with pytest.raises(ValueError, match="heads of %d elements" % (channels // heads)):
+            A.ResidualAttention(channels, heads)
+    with pytest.raises(ValueError, match="heads of 192 elements"):
+        A.ResidualAttention(256, 4, head_dim=192)
+    assert A.ResidualAttention(256, 4, head_dim=128).head_dim == 128
+    assert A.MapAttention(64, 8, rotary=False).heads == 8
