@@ -200,7 +200,7 @@ class KVCache:
     def append(self, k, v, counts=None):
         """k, v [batch, rows, kv_heads, head_dim]; counts: int32 [batch] of the rows that
         count (between 0 and rows; the ones behind are written over by the next append),
-        None: all of them."""
+        None: all of them.  Cast to the cache's type, and without their graph."""
         B, n = k.shape[:2]
         if k.shape != (self.k.shape[0], n) + self.k.shape[2:] or v.shape != k.shape:
             raise ValueError("k is %s, v %s, expected %s" % (
@@ -217,8 +217,8 @@ class KVCache:
         # the device's own lens, held within the bound that was checked
         at = self.lens.long().clamp(0, self.used)[:, None] + step
         b = torch.arange(B, device=k.device)[:, None].expand(B, n)
-        self.k.index_put_((b, at), k.to(self.k.dtype))
-        self.v.index_put_((b, at), v.to(self.v.dtype))
+        self.k.index_put_((b, at), k.detach().to(self.k.dtype))
+        self.v.index_put_((b, at), v.detach().to(self.v.dtype))
         self.lens += self._counted(n, counts)
         self.used += n
 

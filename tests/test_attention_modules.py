@@ -312,6 +312,16 @@ def test_cache_refuses():
         A.ResidualAttention(96, 4, rotary=iabn.RotarySpec(32))
 
 
+def test_a_cache_keeps_no_graph():
+    """Rows that need a gradient are stored, and nothing of how they were made."""
+    cache = A.KVCache(1, 8, 2, 8, BF16)
+    k = rnd(38, 1, 3, 2, 8).requires_grad_()
+    cache.append(k * 2, k * 3)
+    assert not cache.k.requires_grad and not cache.v.requires_grad
+    assert torch.equal(cache.k[:, :3], (k.detach() * 2).to(BF16))
+    assert torch.equal(cache.v[:, :3], (k.detach() * 3).to(BF16))
+
+
 def test_a_refused_call_leaves_the_cache_as_it_was():
     """Of another type, with lengths that the attention refuses, with a spec that the library
     does: what the cache counts is what it held, and the call made right then gives what it gives
