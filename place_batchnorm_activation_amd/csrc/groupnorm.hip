@@ -681,7 +681,9 @@ __global__ __launch_bounds__(kGroupThreads) void k_gn_group_grad(GnArgs a, float
 // whole vectors and twice where the last one is ragged, are few.  us, one workgroup a group
 // against many, forward and backward, bf16: 8 x 32^2 x 512 in 32 groups 9 against 15, 14
 // against 19; 2 x 48^2 x 512 11, 15, 20, 19; 2 x 64^2 x 512 15, 17, 28, 19; 1 x 64^2 x 320 21,
-// 17, 38, 19; 64 x 32^2 x 256 (2048 groups) 31, 27, 72, 46.
+// 17, 38, 19; 64 x 32^2 x 256 (2048 groups) 31, 27, 72, 46.  Ragged groups: 3 x 1073 x 150 in
+// 10 groups of 15 (17168 elements, twice) 12, 18, 18, 23; 3 x 2146 17, 18, 29, 23; 3 x 4000 30,
+// 19, 56, 23; 16 x 600 x 360 in 30 of 12 (9600) 11, 15, 19, 20; 16 x 1200 18, 18, 27, 24.
 bool small_map(int64_t N, int64_t HW, int64_t C, int64_t G, int64_t most)
 {
     const int64_t cg = C / G, wide = ceil_div(cg, kRowV) * kRowV;
